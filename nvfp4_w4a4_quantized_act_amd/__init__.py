@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the path runs in the library's HIP
 kernels.  PyTorch supplies device memory (outputs and workspace are torch
 tensors) and the current stream.  The functions carry the C ABI's names; see
-include/quads.h for the exact contract of each call.
+include/quads.h and include/quads_head.h (the output head: W4A16 product, token
+log-probabilities, distillation) for the exact contract of each call.
 
 bf16 tensors may be passed as torch.bfloat16, torch.int16 or torch.uint16
 (bit patterns).  Results are returned as torch tensors on the input's device.
@@ -23,12 +24,15 @@ __all__ = [
     "quads_nvfp4_weight_qdq", "quads_moe_pack", "quads_moe_w4a4_gemm",
     "quads_moe_w4a4_gemm_rowscale", "quads_moe_combine",
     "quads_mx_quantize", "quads_moe_mx_gemm",
+    "quads_moe_w4a16_gemv", "quads_token_logprob", "quads_token_logprob_backward",
+    "quads_topk_distill", "quads_topk_distill_backward", "quads_topk_distill_grad", "TOP_MAX",
     "EPI_NONE", "EPI_SWIGLU", "OUT_F32", "OUT_BF16", "MX_FP8", "MX_FP4",
 ]
 
 EPI_NONE, EPI_SWIGLU = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 MX_FP8, MX_FP4 = 0, 4
+TOP_MAX = 128                                        # alternatives per row
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libquads.so")
@@ -38,6 +42,8 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
+_INT = ctypes.c_int
 _SIGNATURES = {
     "quads_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "quads_version": (ctypes.c_char_p, []),
@@ -86,6 +92,21 @@ _SIGNATURES = {
                                              _SZ, _P]),
     "quads_moe_mx_gemm": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _P, _P, _P, _I32, _I64,
                                          ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P]),
+    "quads_moe_w4a16_gemv_ws": (_SZ, [_I64, _I64, _I32, _I64]),
+    "quads_moe_w4a16_gemv": (_INT, [_P, _P, _I64, _I64, _P, _P, _P, _P, _I32, _I64, _INT, _INT,
+                                    _P, _P, _SZ, _P]),
+    "quads_token_logprob_ws": (_SZ, [_I64, _I64, _I32]),
+    "quads_token_logprob": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _F, _I32, _P, _P, _P, _P, _P,
+                                   _P, _SZ, _P]),
+    "quads_token_logprob_backward": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _F, _P, _P, _P, _P,
+                                            _P, _P]),
+    "quads_topk_distill_ws": (_SZ, [_I64, _I64, _I32]),
+    "quads_topk_distill": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _I32, _P, _F, _INT, _P, _P,
+                                  _P, _SZ, _P]),
+    "quads_topk_distill_backward": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _I32, _P, _F,
+                                           _INT, _P, _P, _P, _P]),
+    "quads_topk_distill_grad": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _I32, _P, _F, _INT,
+                                       _P, _P, _P, _SZ, _P]),
 }
 
 
@@ -526,3 +547,203 @@ def quads_moe_mx_rac_gemm(a, r, sel, w, n, rows=None, offsets=None, row_token=No
         _ptr(rs) if k else None, _ptr(sel) if k else None, k, _ptr(w_codes), _ptr(w_scale),
         _ptr(offsets), e, n, epilogue, out_dtype, _ptr(out), _ptr(ws), nws, _stream(dev)))
     return out
+
+
+# ---- the output head (include/quads_head.h) ----------------------------------
+# Unlike the calls above, these check the tensors they are given (type, shape,
+# device) before the library sees a pointer, and run on the inputs' device.
+
+def _want(name, t, dtype, shape, dev):
+    """`t` dense on `dev`, checked; None stays None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, not on {t.device}")
+    return t.detach().contiguous()
+
+
+def _gpu(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU, not on {t.device}")
+    return t.device
+
+
+def _call(fn, dev, *args):
+    """lib().fn(*args, stream) on `dev`, the stream being the device's current one."""
+    if torch.cuda.current_device() == dev.index:
+        status = getattr(lib(), fn)(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib(), fn)(*args, _stream(dev))
+    _check(fn, status)
+
+
+def _logits(logits):
+    """(logits, dtype code, T, V, ld): a 2-D view with dense, 16-byte aligned rows; copied
+    if it is not one already.  A row stride above V (padded rows) needs no copy."""
+    _gpu("logits", logits)
+    if logits.dtype == torch.float32:
+        code = OUT_F32
+    elif logits.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+        code = OUT_BF16
+    else:
+        raise TypeError("logits must be float32 or bf16 (torch.bfloat16, int16 or uint16 bits)")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, V]")
+    t, v = logits.shape
+    z = logits.detach()
+    if t and v and (z.stride(1) != 1 or (t > 1 and z.stride(0) < v) or z.data_ptr() % 16):
+        z = z.clone(memory_format=torch.contiguous_format)
+    return z, code, t, v, (z.stride(0) if t > 1 else v)
+
+
+def _like_logits(z, t, v, ld, out):
+    """The gradient's tensor: `out`, checked, or a new one with the logits' row stride."""
+    if out is None:
+        if ld == v:
+            return torch.empty((t, v), dtype=z.dtype, device=z.device)
+        return torch.empty((t, ld), dtype=z.dtype, device=z.device)[:, :v]
+    if out.dtype != z.dtype or tuple(out.shape) != (t, v) or out.device != z.device:
+        raise ValueError("out must have the logits' type, shape and device")
+    if t and v and (out.stride(1) != 1 or (t > 1 and out.stride(0) != ld) or out.data_ptr() % 16):
+        raise ValueError("out must have the logits' row stride and be 16-byte aligned")
+    return out
+
+
+def quads_moe_w4a16_gemv(x, w, n, rows=None, offsets=None, row_token=None, epilogue=EPI_NONE,
+                         out_dtype=OUT_F32, out=None):
+    """Grouped W4A16 product for few rows per expert: bf16 x [Tx, K] times the NVFP4 weights
+    w = (nib [E, N, K/2], scale [E, N, K/16], ts [E]).  Returns out [rows, N] (or [rows, N/2]
+    for SwiGLU), fp32 or bf16 bits (int16)."""
+    dev = _gpu("x", x)
+    x = _bits16(x.detach())
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, K]")
+    kd = x.shape[1]
+    e = w[0].shape[0]
+    w_nib = _want("w nib", w[0], torch.uint8, (e, n, kd // 2), dev)
+    w_scale = _want("w scale", w[1], torch.uint8, (e, n, kd // 16), dev)
+    w_ts = _want("w ts", w[2], torch.float32, (e,), dev)
+    offsets = _want("offsets", offsets, torch.int32, (e + 1,), dev)
+    if row_token is not None:
+        row_token = _want("row_token", row_token, torch.int32, row_token.shape[:1], dev)
+    most = x.shape[0] if row_token is None else row_token.shape[0]
+    if rows is None:
+        rows = most
+    elif not 0 <= rows <= most:
+        raise ValueError(f"rows must be in 0 .. {most}")
+    ncols = n // 2 if epilogue == EPI_SWIGLU else n
+    dt = torch.float32 if out_dtype == OUT_F32 else torch.int16
+    if out is None:
+        out = torch.empty((rows, ncols), dtype=dt, device=dev)
+    elif (out.dtype not in ((dt,) if out_dtype == OUT_F32 else (torch.int16, torch.bfloat16))
+          or tuple(out.shape) != (rows, ncols) or out.device != dev or not out.is_contiguous()):
+        raise ValueError("out must be a dense tensor of the call's type, shape and device")
+    nws = lib().quads_moe_w4a16_gemv_ws(rows, kd, e, n)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    _call("quads_moe_w4a16_gemv", dev, _ptr(x), _ptr(row_token), rows, kd, _ptr(w_nib),
+          _ptr(w_scale), _ptr(w_ts), _ptr(offsets), e, n, epilogue, out_dtype, _ptr(out),
+          _ptr(ws), nws)
+    return out
+
+
+def quads_token_logprob(logits, ids=None, inv_temp=1.0, topk=0, want_entropy=True):
+    """Log-probabilities of the tokens ids int32 [T] under softmax(inv_temp * logits), with the
+    entropy and the topk largest entries of each row -> dict of fp32 logp [T] (with ids),
+    entropy [T] (if wanted), stats [T, 2], and top_logp [T, topk], top_id int32 (topk > 0)."""
+    z, code, t, v, ld = _logits(logits)
+    dev = z.device
+    ids = _want("ids", ids, torch.int32, (t,), dev)
+    out = {}
+    if ids is not None:
+        out["logp"] = torch.empty(t, dtype=torch.float32, device=dev)
+    if want_entropy:
+        out["entropy"] = torch.empty(t, dtype=torch.float32, device=dev)
+    out["stats"] = torch.empty((t, 2), dtype=torch.float32, device=dev)
+    if topk > 0:
+        out["top_logp"] = torch.empty((t, topk), dtype=torch.float32, device=dev)
+        out["top_id"] = torch.empty((t, topk), dtype=torch.int32, device=dev)
+    nws = lib().quads_token_logprob_ws(t, v, topk)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    _call("quads_token_logprob", dev, _ptr(z), code, t, v, ld, _ptr(ids), inv_temp, topk,
+          _ptr(out.get("logp")), _ptr(out.get("entropy")), _ptr(out["stats"]),
+          _ptr(out.get("top_logp")), _ptr(out.get("top_id")), _ptr(ws), nws)
+    return out
+
+
+def quads_token_logprob_backward(logits, ids, stats, entropy, g_logp, g_entropy=None,
+                                 inv_temp=1.0, out=None):
+    """Gradient of the logits from the gradients fp32 [T] of quads_token_logprob's logp and
+    entropy (either may be None); stats and entropy are that call's.  out may be the logits."""
+    z, code, t, v, ld = _logits(logits)
+    dev = z.device
+    ids = _want("ids", ids, torch.int32, (t,), dev)
+    stats = _want("stats", stats, torch.float32, (t, 2), dev)
+    entropy = _want("entropy", entropy, torch.float32, (t,), dev)
+    g_logp = _want("g_logp", g_logp, torch.float32, (t,), dev)
+    g_entropy = _want("g_entropy", g_entropy, torch.float32, (t,), dev)
+    out = _like_logits(z, t, v, ld, out)
+    _call("quads_token_logprob_backward", dev, _ptr(z), code, t, v, ld, _ptr(ids), inv_temp,
+          _ptr(stats), _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(out))
+    return out
+
+
+def _teacher(t_val, t_id, weight, t, dev):
+    if not isinstance(t_val, torch.Tensor) or t_val.dim() != 2:
+        raise ValueError("t_val must be a tensor [T, topk]")
+    k = t_val.shape[1]
+    return (_want("t_val", t_val, torch.float32, (t, k), dev),
+            _want("t_id", t_id, torch.int32, (t, k), dev), k,
+            _want("weight", weight, torch.float32, (t,), dev))
+
+
+def quads_topk_distill(logits, t_val, t_id, weight=None, inv_temp=1.0, renorm=True):
+    """Distillation loss of each row from a teacher's alternatives t_val fp32, t_id int32
+    [T, topk] -> (loss fp32 [T], stats fp32 [T, 2])."""
+    z, code, t, v, ld = _logits(logits)
+    dev = z.device
+    t_val, t_id, k, weight = _teacher(t_val, t_id, weight, t, dev)
+    loss = torch.empty(t, dtype=torch.float32, device=dev)
+    stats = torch.empty((t, 2), dtype=torch.float32, device=dev)
+    nws = lib().quads_topk_distill_ws(t, v, k)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    _call("quads_topk_distill", dev, _ptr(z), code, t, v, ld, _ptr(t_val), _ptr(t_id), k,
+          _ptr(weight), inv_temp, int(renorm), _ptr(loss), _ptr(stats), _ptr(ws), nws)
+    return loss, stats
+
+
+def quads_topk_distill_backward(logits, t_val, t_id, stats, g, weight=None, inv_temp=1.0,
+                                renorm=True, out=None):
+    """Gradient of the logits from the gradient g fp32 [T] of quads_topk_distill's loss; stats
+    are that call's.  out may be the logits."""
+    z, code, t, v, ld = _logits(logits)
+    dev = z.device
+    t_val, t_id, k, weight = _teacher(t_val, t_id, weight, t, dev)
+    stats = _want("stats", stats, torch.float32, (t, 2), dev)
+    g = _want("g", g, torch.float32, (t,), dev)
+    out = _like_logits(z, t, v, ld, out)
+    _call("quads_topk_distill_backward", dev, _ptr(z), code, t, v, ld, _ptr(t_val), _ptr(t_id),
+          k, _ptr(weight), inv_temp, int(renorm), _ptr(stats), _ptr(g), _ptr(out))
+    return out
+
+
+def quads_topk_distill_grad(logits, t_val, t_id, weight=None, inv_temp=1.0, renorm=True,
+                            out=None):
+    """The loss and the gradient of its sum in one call -> (loss fp32 [T], dlogits).  out may be
+    the logits."""
+    z, code, t, v, ld = _logits(logits)
+    dev = z.device
+    t_val, t_id, k, weight = _teacher(t_val, t_id, weight, t, dev)
+    loss = torch.empty(t, dtype=torch.float32, device=dev)
+    out = _like_logits(z, t, v, ld, out)
+    nws = lib().quads_topk_distill_ws(t, v, k)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    _call("quads_topk_distill_grad", dev, _ptr(z), code, t, v, ld, _ptr(t_val), _ptr(t_id), k,
+          _ptr(weight), inv_temp, int(renorm), _ptr(loss), _ptr(out), _ptr(ws), nws)
+    return loss, out

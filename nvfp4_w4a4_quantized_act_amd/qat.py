@@ -14,13 +14,17 @@ so the learner sees, bit for bit, the bf16 image of the values the rollout's
 W4A4 GEMM multiplies (Eq. (16): the weight term of the mismatch vanishes);
 where s_t is a power of two the two are the same numbers.
 
-The matrix product of the learner is the trainer's own (torch); only the QDQ
-node runs in the library.
+The matrix product of the learner is the trainer's own (torch); the QDQ node
+runs in the library, and so do the losses on its logits: the log-probabilities
+of the rollout's tokens with the entropy (`token_logprobs`, the quantity that
+the method aligns between rollout and learner) and the distillation from
+another model's top alternatives (`distill_loss`).
 """
 
 import torch
 
-from . import quads_nvfp4_weight_qdq
+from . import (quads_nvfp4_weight_qdq, quads_token_logprob, quads_token_logprob_backward,
+               quads_topk_distill, quads_topk_distill_backward)
 
 
 class WeightQDQ(torch.autograd.Function):
@@ -58,3 +62,73 @@ def qat_linear(x, w):
     k = x.shape[-1]
     y = torch.nn.functional.linear(x.reshape(-1, k), weight_qdq(w))
     return y.reshape(*x.shape[:-1], w.shape[0])
+
+
+class TokenLogprobs(torch.autograd.Function):
+    """(ln p[ids], entropy) of softmax(inv_temp * logits); gradient for the logits."""
+
+    @staticmethod
+    def forward(ctx, logits, ids, inv_temp):
+        r = quads_token_logprob(logits, ids, inv_temp=inv_temp)
+        ctx.save_for_backward(logits, ids, r["stats"], r["entropy"])
+        ctx.inv_temp = inv_temp
+        ctx.set_materialize_grads(False)
+        return r["logp"], r["entropy"]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_logp, g_entropy):
+        if g_logp is None and g_entropy is None:
+            return None, None, None
+        logits, ids, stats, entropy = ctx.saved_tensors
+        return quads_token_logprob_backward(logits, ids, stats, entropy, g_logp, g_entropy,
+                                            inv_temp=ctx.inv_temp), None, None
+
+
+def token_logprobs(logits, ids, inv_temp=1.0):
+    """Log-probabilities (fp32) of the tokens ids int32 and the entropies of the rows of logits
+    [..., V] (float32 or bf16), differentiable in the logits.  An id outside [0, V) marks a
+    position without a token: its log-probability is 0, without a gradient."""
+    if ids.shape != logits.shape[:-1]:
+        raise ValueError("ids must have the shape of the logits without the last dimension")
+    lp, h = TokenLogprobs.apply(logits.reshape(-1, logits.shape[-1]), ids.reshape(-1),
+                                float(inv_temp))
+    return lp.reshape(ids.shape), h.reshape(ids.shape)
+
+
+class DistillLoss(torch.autograd.Function):
+    """Loss per row from a teacher's top alternatives; gradient for the logits."""
+
+    @staticmethod
+    def forward(ctx, logits, t_val, t_id, weight, inv_temp, renorm):
+        loss, stats = quads_topk_distill(logits, t_val, t_id, weight, inv_temp, renorm)
+        ctx.save_for_backward(logits, t_val, t_id, weight, stats)
+        ctx.inv_temp, ctx.renorm = inv_temp, renorm
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        logits, t_val, t_id, weight, stats = ctx.saved_tensors
+        return (quads_topk_distill_backward(logits, t_val, t_id, stats, g, weight, ctx.inv_temp,
+                                            ctx.renorm), None, None, None, None, None)
+
+
+def distill_loss(logits, t_val, t_id, weight=None, inv_temp=1.0, renorm=True):
+    """Distillation loss (fp32) of each row of logits [..., V] from a teacher's alternatives
+    t_val fp32 and t_id int32 [..., topk] (`quads_token_logprob`'s top_logp and top_id of the
+    teacher's logits): w sum_i q_i (ln q_i - ln p_i), q the teacher's probabilities, over the
+    list renormalised (`renorm`) or as they stand.  Differentiable in the logits only."""
+    lead = logits.shape[:-1]
+    if t_val.shape[:-1] != lead or t_id.shape != t_val.shape:
+        raise ValueError("t_val and t_id must be [..., topk] over the logits' rows")
+    if weight is not None and weight.shape != lead:
+        raise ValueError("weight must have one entry per row of the logits")
+    if t_val.requires_grad or (weight is not None and weight.requires_grad):
+        raise ValueError("distill_loss has no gradient for the teacher's values or the weights")
+    k = t_val.shape[-1]
+    loss = DistillLoss.apply(logits.reshape(-1, logits.shape[-1]), t_val.reshape(-1, k),
+                             t_id.reshape(-1, k),
+                             None if weight is None else weight.reshape(-1), float(inv_temp),
+                             bool(renorm))
+    return loss.reshape(lead)

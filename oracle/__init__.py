@@ -27,6 +27,7 @@ Modules:
   rac     -- residual, fixed-order channel score, top-k, second pass
   moe     -- token packing, grouped W4A4 GEMM with compensation, SwiGLU,
              combine
+  head    -- W4A16 product, token log-probabilities, distillation, gradients
 """
 
-from . import formats, nvfp4, rac, moe  # noqa: F401
+from . import formats, nvfp4, rac, moe, head  # noqa: F401
