@@ -14,8 +14,9 @@
  *    gradient.
  *
  * The conventions of quads.h hold: device pointers, 16-byte aligned, dense and
- * row-major unless a row stride is stated, bf16 as uint16_t bit patterns,
- * asynchronous on `stream` (a stream of the calling thread's current device),
+ * row-major unless a row stride is stated, bf16 as uint16_t bit patterns
+ * (arrays of int32 and fp32 words other than logits and outputs of a product
+ * need 4-byte alignment only), asynchronous on `stream` (a stream of the calling thread's current device),
  * caller-owned workspace, host-side argument checks before any launch,
  * QUADS_* status codes, size-0 inputs a no-op.  Every call may be captured
  * into a HIP graph.  Results do not depend on the order in which work-groups
@@ -23,7 +24,7 @@
  *
  * Logits.  z [T, V], `dtype` QUADS_OUT_F32 or QUADS_OUT_BF16, row t at element
  * t * ld (ld >= V; elements V .. ld - 1 of a row are neither read nor
- * written).  1 <= V < 2^31, T < 2^31.  inv_temp > 0 and finite, it below;
+ * written).  1 <= V < 2^30, T and ld < 2^31.  0 < inv_temp <= 1e30, it below;
  * probabilities are those of softmax(it * z).  Entries may be -inf (masked):
  * their probability is 0.  A row whose every entry is -inf has entropy 0, the
  * stats (-inf, 0) and a zero gradient.  A row with +inf or NaN gives NaN.

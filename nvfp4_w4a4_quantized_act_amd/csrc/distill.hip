@@ -1,14 +1,9 @@
-// Losses on the output head's logits (include/quads_head.h): token
-// log-probabilities with entropy and top alternatives, distillation from
-// another model's alternatives, and their gradients.
-#include "common.h"
-#include "../../include/quads_head.h"
+// Distillation from another model's top alternatives and its gradient
+// (include/quads_head.h).
+#include "logits.h"
 
 namespace quads {
 namespace head {
-
-constexpr int kThreads = 256;
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct Rows {
     const void* z;
@@ -27,7 +22,7 @@ __device__ __forceinline__ void st_z(void* z, int64_t i, float v) {
 }
 
 // Reductions over the work-group; s_red holds one value per thread.
-__device__ __forceinline__ float block_max(float v, float* s_red) {
+__device__ __forceinline__ float group_max(float v, float* s_red) {
     __syncthreads();
     s_red[threadIdx.x] = v;
     __syncthreads();
@@ -40,7 +35,7 @@ __device__ __forceinline__ float block_max(float v, float* s_red) {
     }
     return s_red[0];
 }
-__device__ __forceinline__ float block_sum(float v, float* s_red) {
+__device__ __forceinline__ float group_sum(float v, float* s_red) {
     __syncthreads();
     s_red[threadIdx.x] = v;
     __syncthreads();
@@ -62,7 +57,7 @@ __device__ __forceinline__ void row_stats(const Rows& r, int64_t t, float* s_red
         const float z = ld_z<kBf16>(r.z, b + v);
         m = (z != z || z > m) ? z : m;
     }
-    m = block_max(m, s_red);
+    m = group_max(m, s_red);
     if (m == -INFINITY) {
         *m_out = m; *s_out = 1.0f; *u_out = 0.0f;
         return;
@@ -75,88 +70,8 @@ __device__ __forceinline__ void row_stats(const Rows& r, int64_t t, float* s_red
         u += e * fmaxf(d, -200.0f);
     }
     *m_out = m;
-    *s_out = block_sum(s, s_red);
-    *u_out = block_sum(u, s_red);
-}
-
-// Ranks by value, then by lower index (a larger key is a larger entry).
-__device__ __forceinline__ uint64_t rank_key(float z, uint32_t v) {
-    const uint32_t b = __float_as_uint(z + 0.0f);                 // -0 counts as 0
-    const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-    return ((uint64_t)k << 32) | (0xFFFFFFFFu - v);
-}
-
-template <int kBf16>
-__global__ __launch_bounds__(kThreads) void k_token_logprob(Rows r, const int32_t* ids, int topk,
-                                                            float* logp, float* entropy,
-                                                            float* stats, float* top_logp,
-                                                            int32_t* top_id) {
-    __shared__ float s_red[kThreads];
-    __shared__ unsigned long long s_best;
-    const int64_t t = blockIdx.x;
-    float m, s, u;
-    row_stats<kBf16>(r, t, s_red, &m, &s, &u);
-    const float ls = logf(s);
-    if (threadIdx.x == 0) {
-        stats[2 * t] = m;
-        stats[2 * t + 1] = ls;
-        if (entropy) entropy[t] = m == -INFINITY ? 0.0f : ls - u / s;
-        if (ids) {
-            const int64_t id = ids[t];
-            float y = 0.0f;
-            if (id >= 0 && id < r.V) {
-                const float z = ld_z<kBf16>(r.z, t * r.ld + id);
-                y = z == -INFINITY && m == m ? z : (z - m) * r.it - ls;
-            }
-            logp[t] = y;
-        }
-    }
-    uint64_t last = ~0ull;
-    for (int i = 0; i < topk; ++i) {
-        __syncthreads();
-        if (threadIdx.x == 0) s_best = 0;
-        __syncthreads();
-        uint64_t best = 0;
-        for (int64_t v = threadIdx.x; v < r.V; v += kThreads) {
-            const uint64_t k = rank_key(ld_z<kBf16>(r.z, t * r.ld + v), (uint32_t)v);
-            if (k < last && k > best) best = k;
-        }
-        atomicMax(&s_best, (unsigned long long)best);
-        __syncthreads();
-        last = s_best;
-        if (threadIdx.x == 0) {
-            const int64_t id = 0xFFFFFFFFu - (uint32_t)last;
-            const float z = ld_z<kBf16>(r.z, t * r.ld + id);
-            top_id[t * topk + i] = (int32_t)id;
-            top_logp[t * topk + i] = z == -INFINITY && m == m ? z : (z - m) * r.it - ls;
-        }
-    }
-}
-
-template <int kBf16>
-__global__ __launch_bounds__(kThreads) void k_token_logprob_bwd(Rows r, const int32_t* ids,
-                                                                const float* stats,
-                                                                const float* entropy,
-                                                                const float* g_logp,
-                                                                const float* g_entropy,
-                                                                void* dz) {
-    const int64_t t = blockIdx.x;
-    const float m = stats[2 * t], ls = stats[2 * t + 1];
-    const int64_t id = ids ? ids[t] : -1;
-    const bool have = id >= 0 && id < r.V;
-    const float gl = g_logp && have ? g_logp[t] : 0.0f;
-    const float gh = g_entropy ? g_entropy[t] : 0.0f;
-    const float h = g_entropy ? entropy[t] : 0.0f;
-    for (int64_t v = threadIdx.x; v < r.V; v += kThreads) {
-        const float z = ld_z<kBf16>(r.z, t * r.ld + v);
-        float g = 0.0f;
-        if (m != -INFINITY) {
-            const float lp = (z - m) * r.it - ls;
-            const float p = expf(lp);
-            g = r.it * ((v == id ? gl : 0.0f) - gl * p - gh * p * (fmaxf(lp, -200.0f) + h));
-        }
-        st_z<kBf16>(dz, t * r.ld + v, g);
-    }
+    *s_out = group_sum(s, s_red);
+    *u_out = group_sum(u, s_red);
 }
 
 // The teacher's distribution over its list, in LDS: s_q[i] = q_i (0 for an
@@ -168,13 +83,13 @@ __device__ __forceinline__ float teacher(const float* val, const int32_t* id, in
     const bool have = i < topk && id[i] >= 0 && id[i] < V;
     float y = have ? (renorm ? it * val[i] : val[i]) : -INFINITY;
     if (renorm) {
-        const float m = block_max(y, s_red);
-        const float s = block_sum(y == -INFINITY ? 0.0f : expf(y - m), s_red);
+        const float m = group_max(y, s_red);
+        const float s = group_sum(y == -INFINITY ? 0.0f : expf(y - m), s_red);
         y = y == -INFINITY ? y : y - m - logf(s);
     }
     const float q = expf(y);
     if (i < topk) { s_q[i] = q; s_lq[i] = y; }
-    return block_sum(q, s_red);
+    return group_sum(q, s_red);
 }
 
 // mode bits: 1 = loss and stats from the logits, 2 = gradient
@@ -211,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void k_topk_distill(Rows r, const float* 
             const float z = ld_z<kBf16>(r.z, t * r.ld + t_id[i]);
             y = s_q[i] * (s_lq[i] - (z == -INFINITY && m == m ? z : (z - m) * r.it - ls));
         }
-        y = block_sum(y, s_red);
+        y = group_sum(y, s_red);
         if (threadIdx.x == 0) {
             loss[t] = w * y;
             if (stats) { stats[2 * t] = m; stats[2 * t + 1] = ls; }
@@ -234,18 +149,6 @@ __global__ __launch_bounds__(kThreads) void k_topk_distill(Rows r, const float* 
     }
 }
 
-int check_rows(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, float it) {
-    if (T < 0 || T >= ((int64_t)1 << 31) || V < 1 || V >= ((int64_t)1 << 31) || ld < V ||
-        ld >= ((int64_t)1 << 31))
-        return QUADS_ESHAPE;
-    if (dtype != QUADS_OUT_F32 && dtype != QUADS_OUT_BF16) return QUADS_EINVAL;
-    if (!(it > 0.0f) || !(it < INFINITY)) return QUADS_EINVAL;
-    if (T == 0) return QUADS_OK;
-    return ok_ptr(logits) ? QUADS_OK : QUADS_EINVAL;
-}
-
-inline bool ok_opt4(const void* p) { return p == nullptr || ok_ptr4(p); }
-
 int check_list(int64_t T, const float* t_val, const int32_t* t_id, int32_t topk,
                const float* weight, int renorm) {
     if (topk < 1 || topk > QUADS_TOP_MAX) return QUADS_ESHAPE;
@@ -258,63 +161,6 @@ int check_list(int64_t T, const float* t_val, const int32_t* t_id, int32_t topk,
 }  // namespace quads
 
 using namespace quads;
-
-extern "C" size_t quads_token_logprob_ws(int64_t T, int64_t V, int32_t topk) {
-    (void)T; (void)V; (void)topk;
-    return 0;
-}
-
-extern "C" int quads_token_logprob(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
-                                   const int32_t* ids, float inv_temp, int32_t topk, float* logp,
-                                   float* entropy, float* stats, float* top_logp, int32_t* top_id,
-                                   void* ws, size_t ws_bytes, void* stream) {
-    const int rc = head::check_rows(logits, dtype, T, V, ld, inv_temp);
-    if (rc != QUADS_OK) return rc;
-    if (topk < 0 || topk > QUADS_TOP_MAX || topk > V) return QUADS_ESHAPE;
-    if (T == 0) return QUADS_OK;
-    if (!head::ok_opt4(ids) || !head::ok_opt4(logp) || (ids == nullptr) != (logp == nullptr) ||
-        !head::ok_opt4(entropy) || !ok_ptr4(stats))
-        return QUADS_EINVAL;
-    if (topk > 0 && (!ok_ptr4(top_logp) || !ok_ptr4(top_id))) return QUADS_EINVAL;
-    const size_t need = quads_token_logprob_ws(T, V, topk);
-    if (ws_bytes < need || (need > 0 && !ok_ptr(ws))) return QUADS_EWORKSPACE;
-    const head::Rows r{logits, T, V, ld, inv_temp};
-    const dim3 grid((unsigned)T), block(head::kThreads);
-    hipStream_t st = (hipStream_t)stream;
-    if (dtype == QUADS_OUT_BF16)
-        hipLaunchKernelGGL(head::k_token_logprob<1>, grid, block, 0, st, r, ids, (int)topk, logp,
-                           entropy, stats, top_logp, top_id);
-    else
-        hipLaunchKernelGGL(head::k_token_logprob<0>, grid, block, 0, st, r, ids, (int)topk, logp,
-                           entropy, stats, top_logp, top_id);
-    QUADS_CHECK_LAUNCH();
-    return QUADS_OK;
-}
-
-extern "C" int quads_token_logprob_backward(const void* logits, int dtype, int64_t T, int64_t V,
-                                            int64_t ld, const int32_t* ids, float inv_temp,
-                                            const float* stats, const float* entropy,
-                                            const float* g_logp, const float* g_entropy,
-                                            void* dlogits, void* stream) {
-    const int rc = head::check_rows(logits, dtype, T, V, ld, inv_temp);
-    if (rc != QUADS_OK || T == 0) return rc;
-    if (!head::ok_opt4(ids) || !ok_ptr4(stats) || !head::ok_opt4(entropy) ||
-        !head::ok_opt4(g_logp) || !head::ok_opt4(g_entropy) || !ok_ptr(dlogits))
-        return QUADS_EINVAL;
-    if ((g_logp != nullptr && ids == nullptr) || (g_entropy != nullptr && entropy == nullptr))
-        return QUADS_EINVAL;
-    const head::Rows r{logits, T, V, ld, inv_temp};
-    const dim3 grid((unsigned)T), block(head::kThreads);
-    hipStream_t st = (hipStream_t)stream;
-    if (dtype == QUADS_OUT_BF16)
-        hipLaunchKernelGGL(head::k_token_logprob_bwd<1>, grid, block, 0, st, r, ids, stats,
-                           entropy, g_logp, g_entropy, dlogits);
-    else
-        hipLaunchKernelGGL(head::k_token_logprob_bwd<0>, grid, block, 0, st, r, ids, stats,
-                           entropy, g_logp, g_entropy, dlogits);
-    QUADS_CHECK_LAUNCH();
-    return QUADS_OK;
-}
 
 extern "C" size_t quads_topk_distill_ws(int64_t T, int64_t V, int32_t topk) {
     (void)T; (void)V; (void)topk;

@@ -1,0 +1,207 @@
+// Pieces shared by the kernels that read the output head's logits
+// (include/quads_head.h): rows of any alignment in 16-byte vectors, the
+// running softmax statistics, and the host-side checks.
+#pragma once
+
+#include "common.h"
+#include "../../include/quads_head.h"
+
+namespace quads {
+namespace head {
+
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.69314718055994531f;
+// A term 2^d with d below this is 0 in fp32; d is clamped here where it is a
+// factor (0 * -inf would be NaN).
+constexpr float kNoTerm = -200.0f;
+
+// Logits [T, V] with row stride ld.  A row is read in 16-byte vectors at
+// 16-byte boundaries: vector j holds the entries j * kPer - shift + (0 ..
+// kPer - 1), shift the entries between the boundary before the row and its
+// first one.  The first and the last vector may be partial.
+template <int kBf16>
+struct Row {
+    static constexpr int kPer = kBf16 ? 8 : 4;
+    const char* at;                       // the boundary at or before the row
+    int shift, V, nvec;
+
+    __device__ __forceinline__ Row(const void* z, int64_t t, int64_t ld, int64_t v) {
+        const int64_t first = t * ld;
+        shift = (int)(first & (kPer - 1));
+        at = (const char*)z + (first - shift) * (16 / kPer);
+        V = (int)v;
+        nvec = (int)((v + shift + kPer - 1) / kPer);
+    }
+    __device__ __forceinline__ int index(int j, int i) const { return j * kPer + i - shift; }
+    __device__ __forceinline__ bool whole(int j) const {
+        return index(j, 0) >= 0 && index(j, kPer - 1) < V;
+    }
+    // vector j of the row; entries outside the row read as -inf
+    __device__ __forceinline__ uint4 part(int j) const {
+        uint4 r = kBf16 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
+                        : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+        uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int v = index(j, i);
+            if (v >= 0 && v < V) {
+                if (kBf16) {
+                    const uint32_t h = ((const uint16_t*)at)[(int64_t)j * kPer + i];
+                    w[i >> 1] = (i & 1) ? (w[i >> 1] & 0xFFFFu) | (h << 16)
+                                        : (w[i >> 1] & 0xFFFF0000u) | h;
+                } else {
+                    w[i] = ((const uint32_t*)at)[(int64_t)j * kPer + i];
+                }
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ const uint4* vec(int j) const {
+        return reinterpret_cast<const uint4*>(at) + j;
+    }
+    __device__ __forceinline__ float entry(int64_t v) const {
+        return kBf16 ? bf16_to_f32(((const uint16_t*)at)[shift + v])
+                     : ((const float*)at)[shift + v];
+    }
+};
+
+// Entry i of a vector in fp32.
+template <int kBf16>
+__device__ __forceinline__ float get(const uint4& q, int i) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if (kBf16) return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
+    return __uint_as_float(w[i]);
+}
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const bf16x2_t v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+template <int kBf16>
+__device__ __forceinline__ uint4 put(const float* g) {
+    if (kBf16)
+        return make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]),
+                          pack_bf16(g[6], g[7]));
+    return make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]),
+                      __float_as_uint(g[3]));
+}
+// Stores the entries of vector j that lie in the row (`at` as Row::at, of the output).
+template <int kBf16>
+__device__ __forceinline__ void store_part(const Row<kBf16>& r, char* at, int j, const uint4& q) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < Row<kBf16>::kPer; ++i) {
+        const int v = r.index(j, i);
+        if (v >= 0 && v < r.V) {
+            if (kBf16)
+                ((uint16_t*)at)[(int64_t)j * 8 + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+            else
+                ((uint32_t*)at)[(int64_t)j * 4 + i] = w[i];
+        }
+    }
+}
+template <int kBf16>
+__device__ __forceinline__ void store_vec(const Row<kBf16>& r, char* at, int j, const uint4& q) {
+    if (r.whole(j)) reinterpret_cast<uint4*>(at)[j] = q;
+    else store_part<kBf16>(r, at, j, q);
+}
+
+// Running statistics of some entries: m = max z, and with d = c (z - m),
+// c = it log2(e):  s = sum 2^d, u = sum 2^d d.  Rescaled when m rises, one
+// pass over the data.  Entries of -inf add nothing; m = -inf, s = 0 while
+// there is no other.
+struct Stat {
+    float m, s, u;
+};
+__device__ __forceinline__ float stat_base(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// `a` with its maximum raised to m (m >= a.m).
+__device__ __forceinline__ void stat_raise(Stat& a, float m, float c) {
+    const float d = __builtin_amdgcn_fmed3f((stat_base(a.m) - stat_base(m)) * c, kNoTerm, 0.0f);
+    const float r = __builtin_amdgcn_exp2f(d);
+    a.u = r * __builtin_fmaf(d, a.s, a.u);
+    a.s *= r;
+    a.m = m;
+}
+
+// Sum over the 64 lanes of a wave, the same bits in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+__device__ __forceinline__ Stat wave_stat(Stat a, float c) {
+    stat_raise(a, wave_max(a.m), c);
+    a.s = wave_sum(a.s);
+    a.u = wave_sum(a.u);
+    return a;
+}
+// Statistics of the whole work-group, in every thread (s_stat: one per wave).
+template <int kWaves>
+__device__ __forceinline__ Stat group_stat(Stat a, float c, Stat* s_stat) {
+    a = wave_stat(a, c);
+    if ((threadIdx.x & 63) == 0) s_stat[threadIdx.x >> 6] = a;
+    __syncthreads();
+    float m = s_stat[0].m;
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, s_stat[w].m);
+    Stat r = {m, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        Stat b = s_stat[w];
+        stat_raise(b, m, c);
+        r.s += b.s;
+        r.u += b.u;
+    }
+    return r;
+}
+
+// ln sum exp(it (z - m)): 0 for a row without an unmasked entry.
+__device__ __forceinline__ float log_sum(const Stat& a) {
+    return a.m == -INFINITY && a.s == 0.0f ? 0.0f : logf(a.s);
+}
+// ln p of an entry: -inf where it is masked (unless the row holds NaN or +inf).
+__device__ __forceinline__ float ln_p(float z, float m, float ls, float it) {
+    return z == -INFINITY && ls == ls ? z : (z - m) * it - ls;
+}
+
+// ------------------------------------------------------------------ host --
+
+// Row parts: a row is split over work-groups of kThreads threads where there
+// are too few rows to fill the GPU, into parts of whole chunks (kChunk
+// vectors).
+constexpr int kThreads = 256;
+constexpr int kVecs = 4;                       // vectors per thread and chunk
+constexpr int kChunk = kThreads * kVecs;
+constexpr int kMaxParts = 64;
+constexpr int kGroups = 1024;                  // work-groups wanted: four per CU
+
+inline int row_parts(int64_t T, int64_t V, int dtype) {
+    const int per = dtype == QUADS_OUT_BF16 ? 8 : 4;
+    const int64_t chunks = (V + per - 1 + (int64_t)per * kChunk) / ((int64_t)per * kChunk);
+    int64_t p = kGroups / T;
+    if (p > chunks) p = chunks;
+    if (p > kMaxParts) p = kMaxParts;
+    return p < 1 ? 1 : (int)p;
+}
+
+inline bool ok_opt4(const void* p) { return p == nullptr || ok_ptr4(p); }
+
+inline int check_rows(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, float it) {
+    if (T < 0 || T >= ((int64_t)1 << 31) || V < 1 || V >= ((int64_t)1 << 30) || ld < V ||
+        ld >= ((int64_t)1 << 31))
+        return QUADS_ESHAPE;
+    if (dtype != QUADS_OUT_F32 && dtype != QUADS_OUT_BF16) return QUADS_EINVAL;
+    if (!(it > 0.0f) || !(it <= 1e30f)) return QUADS_EINVAL;
+    if (T == 0) return QUADS_OK;
+    return ok_ptr(logits) ? QUADS_OK : QUADS_EINVAL;
+}
+
+}  // namespace head
+}  // namespace quads

@@ -1,0 +1,509 @@
+// Log-probabilities of given tokens, entropy and top alternatives, and their
+// gradient (include/quads_head.h).
+//
+// Forward.  With d = it (z - m) the log-sum s = ln sum e^d and the entropy
+// H = s - (sum e^d d) / sum e^d come from one pass over the row: every thread
+// keeps a running maximum with the two sums, rescaled when the maximum rises,
+// and the threads' statistics are joined at the end.  The top alternatives
+// come from the same pass (k_logprob below).  A row is one work-group's where
+// there are rows enough; else it is split into parts whose results k_merge
+// joins.  Everything is summed in a fixed order.
+//
+// Backward: dz = it (g_lp 1[v = id] - p (g_lp + g_H (ln p + H))), one read and
+// one write of the row, the token's entry patched by the thread that holds it.
+#include "logits.h"
+
+namespace quads {
+namespace head {
+
+// ------------------------------------------------------------ alternatives --
+
+// Ranks by value (signed zeros equal), then by lower index; never 0.
+__device__ __forceinline__ uint32_t value_key(float z) {
+    const uint32_t b = __float_as_uint(z + 0.0f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t rank_key(float z, uint32_t v) {
+    return ((uint64_t)value_key(z) << 32) | (0xFFFFFFFFu - v);
+}
+__device__ __forceinline__ float key_value(uint64_t k) {
+    const uint32_t b = (uint32_t)(k >> 32);
+    return __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b);
+}
+__device__ __forceinline__ int key_index(uint64_t k) { return (int)(0xFFFFFFFFu - (uint32_t)k); }
+
+constexpr int kCand = 1024;                    // candidates kept at once
+
+struct Cand {
+    uint64_t key[kCand];
+    uint16_t top[kThreads];                    // upper halves of the threads' maxima's keys
+    int n;
+};
+
+// A value that at least k of the work-group's values (key halves in c.top)
+// reach: the k-th largest half, rounded down.  Every wave finds it by itself,
+// one bit of the half at a time, counting with ballots.
+__device__ __forceinline__ float kth_bound(const Cand& c, int k) {
+    const uint2 w = reinterpret_cast<const uint2*>(c.top)[threadIdx.x & 63];
+    const uint32_t h[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
+    uint32_t t = 0;
+#pragma unroll
+    for (int b = 15; b >= 0; --b) {
+        const uint32_t x = t | (1u << b);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n += __popcll(__ballot(h[i] >= x));
+        if (n >= k) t = x;
+    }
+    // the lowest value of that half (none below -inf)
+    return t <= 0x007Fu ? -INFINITY : key_value((uint64_t)(t << 16) << 32);
+}
+
+// Sorts the n candidates and keeps the k largest (c.n is set; barriers on
+// both sides).  Each entry's place is the number of larger ones.
+__device__ __forceinline__ void keep_top(Cand& c, int n, int k) {
+    uint64_t mine[kCand / kThreads];
+    int place[kCand / kThreads];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kCand / kThreads; ++i) {
+        const int at = threadIdx.x + i * kThreads;
+        mine[i] = at < n ? c.key[at] : 0;
+        place[i] = 0;
+    }
+    if (n <= kThreads) {
+        for (int j = 0; j < n; ++j) place[0] += c.key[j] > mine[0] ? 1 : 0;
+    } else {
+        for (int j = 0; j < n; ++j) {
+            const uint64_t x = c.key[j];
+#pragma unroll
+            for (int i = 0; i < kCand / kThreads; ++i) place[i] += x > mine[i] ? 1 : 0;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kCand / kThreads; ++i)
+        if (mine[i] != 0 && place[i] < k) c.key[place[i]] = mine[i];
+    if (threadIdx.x == 0) c.n = n < k ? n : k;
+    __syncthreads();
+}
+
+// Drops the candidates below `bound` (at least k are not).
+__device__ __forceinline__ int drop_below(Cand& c, int n, float bound) {
+    uint64_t mine[kCand / kThreads];
+    const uint64_t low = (uint64_t)value_key(bound) << 32;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kCand / kThreads; ++i) {
+        const int at = threadIdx.x + i * kThreads;
+        mine[i] = at < n ? c.key[at] : 0;
+    }
+    if (threadIdx.x == 0) c.n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kCand / kThreads; ++i)
+        if (mine[i] >= low && mine[i] != 0) c.key[atomicAdd(&c.n, 1)] = mine[i];
+    __syncthreads();
+    return c.n;
+}
+
+// ----------------------------------------------------------------- forward --
+
+struct Out {
+    const int32_t* ids;
+    float it;
+    int topk;
+    float *logp, *entropy, *stats, *top_logp;
+    int32_t* top_id;
+};
+
+// What the parts of a row leave for k_merge: per part its statistics and, in
+// a second array, its topk candidates in order (0: none).
+struct Parts {
+    float4* stat;
+    uint64_t* key;
+};
+
+// The outputs of row t from its statistics (thread 0 and the first topk).
+template <int kBf16>
+__device__ __forceinline__ void finish(const Out& o, const Row<kBf16>& r, int64_t t, const Stat& a,
+                                       const uint64_t* key, int n) {
+    const float ls = log_sum(a);
+    if (threadIdx.x == 0) {
+        o.stats[2 * t] = a.m;
+        o.stats[2 * t + 1] = ls;
+        if (o.entropy)
+            o.entropy[t] = a.m == -INFINITY && a.s == 0.0f ? 0.0f : ls - kLn2 * a.u / a.s;
+        if (o.ids) {
+            const int id = o.ids[t];
+            o.logp[t] = id >= 0 && id < r.V ? ln_p(r.entry(id), a.m, ls, o.it) : 0.0f;
+        }
+    }
+    // fewer candidates than alternatives: the row holds NaN; any indices
+    if ((int)threadIdx.x < o.topk) {
+        const int64_t at = t * o.topk + threadIdx.x;
+        const bool have = n == o.topk;
+        o.top_id[at] = have ? key_index(key[threadIdx.x]) : (int)threadIdx.x;
+        o.top_logp[at] = have ? ln_p(key_value(key[threadIdx.x]), a.m, ls, o.it) : NAN;
+    }
+}
+
+// One work-group: part blockIdx.x % parts of row blockIdx.x / parts, in chunks
+// of kVecs vectors per thread, the next chunk's vectors requested before the
+// present one is worked on.
+//
+// kTop: a candidate is an entry above a value that topk earlier entries reach.
+// That bound is the topk-th largest of the threads' running maxima, taken
+// after the first chunk and again after 2, 4, 8, ... chunks (entries of the
+// first chunk count from the bound on, later ones only above it, as their
+// indices are higher), so that a random row yields about topk (1 + log2 of
+// the chunks) candidates and most chunks are compared with one number.  The
+// candidates are sorted once, at the end.  Where a chunk brings more than
+// there is room for (equal or rising entries), it is taken entry by entry of
+// each thread, the candidates cut to the topk largest in between.
+template <int kBf16, bool kEntropy, bool kTop>
+__global__ __launch_bounds__(kThreads, 5) void k_logprob(const void* z, int64_t V, int64_t ld,
+                                                      int parts, Out o, Parts p) {
+    constexpr int kPer = Row<kBf16>::kPer;
+    constexpr int kEnt = kPer * kVecs;
+    __shared__ Stat s_stat[kThreads / 64];
+    __shared__ Cand c;
+    const int64_t t = blockIdx.x / (unsigned)parts;
+    const int part = (int)(blockIdx.x % (unsigned)parts);
+    const Row<kBf16> r(z, t, ld, V);
+    const float cl = o.it * kLog2e;
+    const int chunks = (r.nvec + kChunk - 1) / kChunk;
+    const int c0 = (int)((int64_t)chunks * part / parts);
+    const int c1 = (int)((int64_t)chunks * (part + 1) / parts);
+    const int topk = o.topk;
+
+    auto load = [&](uint4 (&q)[kVecs], int ch) {
+        const int j0 = ch * kChunk;
+        if (r.whole(j0) && r.whole(j0 + kChunk - 1) && ch < c1) {
+            const uint4* a = r.vec(j0 + threadIdx.x);
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) q[i] = a[i * kThreads];
+        } else if (ch < c1) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int j = j0 + i * kThreads + threadIdx.x;
+                if (r.whole(j)) q[i] = *r.vec(j);
+                else q[i] = r.part(j);
+            }
+        }
+    };
+
+    Stat a = {-INFINITY, 0.0f, 0.0f};
+    float bound = -INFINITY;
+    if (kTop && threadIdx.x == 0) c.n = 0;
+    int n = 0;
+    auto work = [&](const uint4 (&q)[kVecs], int ch) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) m = fmaxf(m, get<kBf16>(q[i], e));
+        const float mine = m;
+        stat_raise(a, fmaxf(a.m, m), cl);
+        const float base = stat_base(a.m);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const float d = (get<kBf16>(q[i], e) - base) * cl;
+                const float x = __builtin_amdgcn_exp2f(d);
+                a.s += x;
+                if (kEntropy) a.u = __builtin_fmaf(x, fmaxf(d, kNoTerm), a.u);
+            }
+        if (!kTop) return;
+        const int nth = ch - c0;
+        if (nth == 0) {
+            c.top[threadIdx.x] = (uint16_t)(value_key(a.m) >> 16);
+            __syncthreads();
+            bound = kth_bound(c, topk);
+        }
+        const bool first = nth == 0;
+        const int base_v = r.index(ch * kChunk + threadIdx.x, 0);
+        if (first ? mine >= bound : mine > bound) {
+            uint32_t pass = 0;
+#pragma unroll
+            for (int i = 0; i < kEnt; ++i) {
+                const float x = get<kBf16>(q[i / kPer], i % kPer);
+                const int v = base_v + (i / kPer) * kThreads * kPer + i % kPer;
+                const bool ok = (first ? x >= bound : x > bound) && v >= 0 && v < r.V;
+                pass |= ok ? 1u << i : 0u;
+            }
+            int at = pass ? atomicAdd(&c.n, __popc(pass)) : 0;
+#pragma unroll
+            for (int i = 0; i < kEnt; ++i)
+                if (pass & (1u << i)) {
+                    const int v = base_v + (i / kPer) * kThreads * kPer + i % kPer;
+                    if (at < kCand) c.key[at] = rank_key(get<kBf16>(q[i / kPer], i % kPer), v);
+                    ++at;
+                }
+        }
+        __syncthreads();
+        const int total = c.n;
+        __syncthreads();
+        if (total <= kCand) {
+            n = total;
+        } else {
+            if (threadIdx.x == 0) c.n = n;
+            __syncthreads();
+            uint64_t over = 0;                 // the topk-th candidate, once cut
+#pragma unroll 1
+            for (int i = 0; i < kEnt; ++i) {
+                if (n + kThreads > kCand) {
+                    keep_top(c, n, topk);
+                    over = c.n == topk ? c.key[topk - 1] : 0;
+                }
+                // entry i of the thread, by a select: q stays in registers
+                uint4 w = q[0];
+#pragma unroll
+                for (int b = 1; b < kVecs; ++b)
+                    if (i / kPer == b) w = q[b];
+                float x = get<kBf16>(w, 0);
+#pragma unroll
+                for (int b = 1; b < kPer; ++b)
+                    if (i % kPer == b) x = get<kBf16>(w, b);
+                const int v = base_v + (i / kPer) * kThreads * kPer + i % kPer;
+                const uint64_t key = rank_key(x, (uint32_t)v);
+                if ((first ? x >= bound : x > bound) && v >= 0 && v < r.V && key > over)
+                    c.key[atomicAdd(&c.n, 1)] = key;
+                __syncthreads();
+                n = c.n;
+                __syncthreads();
+            }
+            keep_top(c, n, topk);
+            n = c.n;
+            if (n == topk) bound = fmaxf(bound, key_value(c.key[topk - 1]));
+            __syncthreads();
+        }
+        if ((nth & (nth + 1)) == 0 && nth > 0) {
+            c.top[threadIdx.x] = (uint16_t)(value_key(a.m) >> 16);
+            __syncthreads();
+            bound = fmaxf(bound, kth_bound(c, topk));
+            __syncthreads();
+        }
+    };
+
+    uint4 q[kVecs], next[kVecs];
+    load(next, c0);
+    for (int ch = c0; ch < c1; ++ch) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) q[i] = next[i];
+        load(next, ch + 1);
+        work(q, ch);
+    }
+
+    const float top = a.m;
+    a = group_stat<kThreads / 64>(a, cl, s_stat);
+    if (kTop) {
+        if (n > topk + topk / 2 + 16) {
+            c.top[threadIdx.x] = (uint16_t)(value_key(top) >> 16);
+            __syncthreads();
+            bound = fmaxf(bound, kth_bound(c, topk));
+            n = drop_below(c, n, bound);
+        }
+        keep_top(c, n, topk);
+        n = c.n;
+    }
+    if (parts == 1) {
+        finish<kBf16>(o, r, t, a, c.key, n);
+    } else {
+        if (threadIdx.x == 0) p.stat[blockIdx.x] = make_float4(a.m, a.s, a.u, 0.0f);
+        if (kTop && (int)threadIdx.x < topk)
+            p.key[(int64_t)blockIdx.x * topk + threadIdx.x] =
+                (int)threadIdx.x < n ? c.key[threadIdx.x] : 0;
+    }
+}
+
+// Joins the parts of a row.  The statistics: lane l of every wave holds part
+// l (kMaxParts = 64).  The alternatives: those of all parts at or above the
+// topk-th largest part maximum (upper half of the key) if there are topk
+// parts, then sorted; parts are short of topk entries only at a row's end.
+template <int kBf16>
+__global__ __launch_bounds__(kThreads) void k_merge(const void* z, int64_t V, int64_t ld,
+                                                    int parts, Out o, Parts p) {
+    __shared__ Cand c;
+    const int64_t t = blockIdx.x;
+    const Row<kBf16> r(z, t, ld, V);
+    const int lane = threadIdx.x & 63;
+    Stat a = {-INFINITY, 0.0f, 0.0f};
+    if (lane < parts) {
+        const float4 q = p.stat[t * parts + lane];
+        a = {q.x, q.y, q.z};
+    }
+    a = wave_stat(a, o.it * kLog2e);
+    int n = 0;
+    if (o.topk > 0) {
+        const uint64_t* key = p.key + t * parts * o.topk;
+        if (threadIdx.x == 0) c.n = 0;
+        __syncthreads();
+        // parts in order, topk at a time; the candidates are cut when full
+        const int all = parts * o.topk;
+        uint64_t over = 0;
+        for (int b = 0; b < all; b += kThreads) {
+            if (n + kThreads > kCand) {
+                keep_top(c, n, o.topk);
+                over = c.n == o.topk ? c.key[o.topk - 1] : 0;
+            }
+            const int i = b + threadIdx.x;
+            const uint64_t k = i < all ? key[i] : 0;
+            if (k > over) c.key[atomicAdd(&c.n, 1)] = k;
+            __syncthreads();
+            n = c.n;
+            __syncthreads();
+        }
+        keep_top(c, n, o.topk);
+        n = c.n;
+    }
+    finish<kBf16>(o, r, t, a, c.key, n);
+}
+
+// ---------------------------------------------------------------- backward --
+
+template <int kBf16>
+__global__ __launch_bounds__(kThreads) void k_logprob_bwd(const void* z, int64_t V, int64_t ld,
+                                                          int parts, const int32_t* ids, float it,
+                                                          const float* stats,
+                                                          const float* entropy,
+                                                          const float* g_logp,
+                                                          const float* g_entropy, void* dz) {
+    constexpr int kPer = Row<kBf16>::kPer;
+    const int64_t t = blockIdx.x / (unsigned)parts;
+    const int part = (int)(blockIdx.x % (unsigned)parts);
+    const Row<kBf16> r(z, t, ld, V);
+    char* out = (char*)dz + (r.at - (const char*)z);
+    const int chunks = (r.nvec + kChunk - 1) / kChunk;
+    const int c0 = (int)((int64_t)chunks * part / parts);
+    const int c1 = (int)((int64_t)chunks * (part + 1) / parts);
+
+    const float m = stats[2 * t], ls = stats[2 * t + 1];
+    const int id = ids ? ids[t] : -1;
+    const bool have = id >= 0 && id < r.V;
+    const float gl = g_logp && have ? it * g_logp[t] : 0.0f;
+    const float gh = g_entropy ? it * g_entropy[t] : 0.0f;
+    // with d = log2 p: dz = it g_lp 1[v = id] - p (f0 + f1 d)
+    const float f0 = g_entropy ? __builtin_fmaf(gh, entropy[t], gl) : gl;
+    const float f1 = gh * kLn2;
+    const bool none = m == -INFINITY && ls == ls;          // no unmasked entry: no gradient
+    const float cl = it * kLog2e, l2 = ls * kLog2e;
+    const int idv = have ? (id + r.shift) / kPer : -1, ide = have ? (id + r.shift) % kPer : 0;
+
+    for (int ch = c0; ch < c1; ++ch) {
+        uint4 q[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int j = ch * kChunk + i * kThreads + threadIdx.x;
+            if (none) q[i] = make_uint4(0, 0, 0, 0);
+            else if (r.whole(j)) q[i] = *r.vec(j);
+            else q[i] = r.part(j);
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int j = ch * kChunk + i * kThreads + threadIdx.x;
+            float g[8];
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const float d = __builtin_fmaf(get<kBf16>(q[i], e) - m, cl, -l2);
+                g[e] = -__builtin_amdgcn_exp2f(d) * __builtin_fmaf(f1, fmaxf(d, kNoTerm), f0);
+            }
+            if (j == idv) {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) g[e] += e == ide ? gl : 0.0f;
+            }
+            if (none) {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) g[e] = 0.0f;
+            }
+            if (j < r.nvec) store_vec<kBf16>(r, out, j, put<kBf16>(g));
+        }
+    }
+}
+
+template <int kBf16>
+void launch_forward(const void* z, int64_t T, int64_t V, int64_t ld, int parts, const Out& o,
+                    const Parts& p, hipStream_t st) {
+    const dim3 grid((unsigned)(T * parts)), block(kThreads);
+    if (o.topk > 0) {
+        if (o.entropy)
+            hipLaunchKernelGGL((k_logprob<kBf16, true, true>), grid, block, 0, st, z, V, ld, parts,
+                               o, p);
+        else
+            hipLaunchKernelGGL((k_logprob<kBf16, false, true>), grid, block, 0, st, z, V, ld,
+                               parts, o, p);
+    } else {
+        if (o.entropy)
+            hipLaunchKernelGGL((k_logprob<kBf16, true, false>), grid, block, 0, st, z, V, ld,
+                               parts, o, p);
+        else
+            hipLaunchKernelGGL((k_logprob<kBf16, false, false>), grid, block, 0, st, z, V, ld,
+                               parts, o, p);
+    }
+    if (parts > 1)
+        hipLaunchKernelGGL((k_merge<kBf16>), dim3((unsigned)T), block, 0, st, z, V, ld, parts, o,
+                           p);
+}
+
+}  // namespace head
+}  // namespace quads
+
+using namespace quads;
+
+// Statistics and candidates of the parts, as many as either type is split into.
+extern "C" size_t quads_token_logprob_ws(int64_t T, int64_t V, int32_t topk) {
+    if (T < 1 || V < 1 || topk < 0) return 0;
+    const int parts = head::row_parts(T, V, QUADS_OUT_F32);
+    return parts > 1 ? (size_t)T * parts * (16 + 8 * (size_t)topk) : 0;
+}
+
+extern "C" int quads_token_logprob(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                                   const int32_t* ids, float inv_temp, int32_t topk, float* logp,
+                                   float* entropy, float* stats, float* top_logp, int32_t* top_id,
+                                   void* ws, size_t ws_bytes, void* stream) {
+    const int rc = head::check_rows(logits, dtype, T, V, ld, inv_temp);
+    if (rc != QUADS_OK) return rc;
+    if (topk < 0 || topk > QUADS_TOP_MAX || topk > V) return QUADS_ESHAPE;
+    if (T == 0) return QUADS_OK;
+    if (!head::ok_opt4(ids) || !head::ok_opt4(logp) || (ids == nullptr) != (logp == nullptr) ||
+        !head::ok_opt4(entropy) || !ok_ptr4(stats))
+        return QUADS_EINVAL;
+    if (topk > 0 && (!ok_ptr4(top_logp) || !ok_ptr4(top_id))) return QUADS_EINVAL;
+    const size_t need = quads_token_logprob_ws(T, V, topk);
+    if (ws_bytes < need || (need > 0 && !ok_ptr(ws))) return QUADS_EWORKSPACE;
+    const int parts = head::row_parts(T, V, dtype);
+    const head::Out o{ids, inv_temp, (int)topk, logp, entropy, stats, top_logp, top_id};
+    const head::Parts p{(float4*)ws, (uint64_t*)((char*)ws + 16 * T * parts)};
+    if (dtype == QUADS_OUT_BF16)
+        head::launch_forward<1>(logits, T, V, ld, parts, o, p, (hipStream_t)stream);
+    else
+        head::launch_forward<0>(logits, T, V, ld, parts, o, p, (hipStream_t)stream);
+    QUADS_CHECK_LAUNCH();
+    return QUADS_OK;
+}
+
+extern "C" int quads_token_logprob_backward(const void* logits, int dtype, int64_t T, int64_t V,
+                                            int64_t ld, const int32_t* ids, float inv_temp,
+                                            const float* stats, const float* entropy,
+                                            const float* g_logp, const float* g_entropy,
+                                            void* dlogits, void* stream) {
+    const int rc = head::check_rows(logits, dtype, T, V, ld, inv_temp);
+    if (rc != QUADS_OK || T == 0) return rc;
+    if (!head::ok_opt4(ids) || !ok_ptr4(stats) || !head::ok_opt4(entropy) ||
+        !head::ok_opt4(g_logp) || !head::ok_opt4(g_entropy) || !ok_ptr(dlogits))
+        return QUADS_EINVAL;
+    if ((g_logp != nullptr && ids == nullptr) || (g_entropy != nullptr && entropy == nullptr))
+        return QUADS_EINVAL;
+    const int parts = head::row_parts(T, V, dtype);
+    const dim3 grid((unsigned)(T * parts)), block(head::kThreads);
+    hipStream_t st = (hipStream_t)stream;
+    if (dtype == QUADS_OUT_BF16)
+        hipLaunchKernelGGL(head::k_logprob_bwd<1>, grid, block, 0, st, logits, V, ld, parts, ids,
+                           inv_temp, stats, entropy, g_logp, g_entropy, dlogits);
+    else
+        hipLaunchKernelGGL(head::k_logprob_bwd<0>, grid, block, 0, st, logits, V, ld, parts, ids,
+                           inv_temp, stats, entropy, g_logp, g_entropy, dlogits);
+    QUADS_CHECK_LAUNCH();
+    return QUADS_OK;
+}

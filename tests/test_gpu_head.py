@@ -15,7 +15,10 @@ Tolerances, derived (u = 2^-24, half a step of fp32).  With d = it (z - m):
     err_H = err_s + sum p |d| (err_s + 6 u |d| + (n + 12) u) + 2 u H + 2 u s;
   * a gradient is made of terms of p with p's relative error
     err_p = err_lp + 8 u, plus 4 roundings of each term and of the sum, plus
-    half a step of the output's type and the smallest subnormal.
+    half a step of the output's type and the smallest subnormal.  The hardware's
+    exponential gives 0 below the smallest normal number, 2^-126: p has that
+    absolute error too, and a term is p times its other factors, so 2^-126
+    times those factors is added.
 """
 
 import numpy as np
@@ -138,10 +141,11 @@ def check_grad(Q, z, zr, it, ids, r, e, b, dtype, which="both", out=None):
         a = np.where(have, np.abs(gl), 0.0)[:, None]
         hot = np.zeros((t, v))
         hot[np.arange(t), np.where(have, ids, 0)] = 1
-        tol += a * (p * (ep + 4 * U) + hot * 4 * U)
+        tol += a * (p * (ep + 4 * U) + hot * 4 * U + 2.0 ** -126)
     if gh is not None:
-        a = np.abs(gh)[:, None] * p
-        tol += a * (np.abs(fin + e["entropy"][:, None]) * (ep + 4 * U) + elp + eh[:, None]
+        a = np.abs(gh)[:, None]
+        tol += a * 2.0 ** -126 * (np.abs(fin) + np.abs(e["entropy"])[:, None])
+        tol += a * p * (np.abs(fin + e["entropy"][:, None]) * (ep + 4 * U) + elp + eh[:, None]
                     + 4 * U * (np.abs(fin) + e["entropy"][:, None]))
     tol = it * tol * (1 + HALF[dtype]) + HALF[dtype] * np.abs(want) + TINY[dtype]
     close(dz, want, tol)
@@ -294,7 +298,7 @@ def distill_tolerance(zr, t_val, t_id, w, g, it, renorm, dtype, want_dz):
     tol_loss = np.abs(w) * tol * (1 + U) + np.abs(w) * 4 * U * np.where(q > 0, q * part, 0).sum(1)
     p = np.exp(lp)
     big = q.sum(1, keepdims=True)
-    tol = big * p * (elp + 8 * U + eq.max(1, keepdims=True) + (k + 8) * U)
+    tol = big * (p * (elp + 8 * U + eq.max(1, keepdims=True) + (k + 8) * U) + 2.0 ** -126)
     for i in range(t):
         for j in range(k):
             if q[i, j] > 0:
