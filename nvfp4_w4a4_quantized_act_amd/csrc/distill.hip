@@ -1,160 +1,492 @@
 // Distillation from another model's top alternatives and its gradient
 // (include/quads_head.h).
+//
+//   loss = w sum_i q_i (ln q_i - ln p_{id_i}),   dz_v = g w it (Q p_v - q_v)
+//
+// The list is at most two entries per lane of a wave, so that a wave forms q
+// and Q by itself.  The gradient is dense in Q p and differs from it at the
+// list's ids alone: those entries are worked out apart, from the logits read
+// before anything is written (dlogits may be the logits), and written over
+// the dense ones after a barrier.
+//
+// Loss and gradient of many rows in one call go through k_distill_row, which
+// reads each row once: see there.  Everything else streams a row, or its parts
+// where there are few rows (logits.h): k_distill_loss, k_distill_join,
+// k_distill_bwd.
 #include "logits.h"
 
 namespace quads {
 namespace head {
 
-struct Rows {
-    const void* z;
-    int64_t T, V, ld;
-    float it;
+struct List {
+    const float* val;
+    const int32_t* id;
+    const float* weight;
+    int topk, renorm;
 };
 
-template <int kBf16>
-__device__ __forceinline__ float ld_z(const void* z, int64_t i) {
-    return kBf16 ? bf16_to_f32(((const uint16_t*)z)[i]) : ((const float*)z)[i];
-}
-template <int kBf16>
-__device__ __forceinline__ void st_z(void* z, int64_t i, float v) {
-    if (kBf16) ((uint16_t*)z)[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
-    else ((float*)z)[i] = v;
-}
-
-// Reductions over the work-group; s_red holds one value per thread.
-__device__ __forceinline__ float group_max(float v, float* s_red) {
-    __syncthreads();
-    s_red[threadIdx.x] = v;
-    __syncthreads();
-    for (int o = kThreads / 2; o > 0; o >>= 1) {
-        if ((int)threadIdx.x < o) {
-            const float b = s_red[threadIdx.x + o], a = s_red[threadIdx.x];
-            s_red[threadIdx.x] = (a != a || a > b) ? a : b;      // NaN stays
-        }
-        __syncthreads();
+// A lane's two entries of a row's list: q = 0 and ln q = -inf where there is
+// none; Q over the wave.
+struct Teacher {
+    float q[2], lq[2], all;
+    int id[2];
+};
+struct Entries {
+    float val[2];
+    int id[2];
+};
+__device__ __forceinline__ Entries load_entries(const List& l, int64_t t) {
+    Entries x;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int i = (threadIdx.x & 63) + 64 * b;
+        x.id[b] = i < l.topk ? l.id[t * l.topk + i] : -1;
+        x.val[b] = i < l.topk ? l.val[t * l.topk + i] : 0.0f;
     }
-    return s_red[0];
+    return x;
 }
-__device__ __forceinline__ float group_sum(float v, float* s_red) {
-    __syncthreads();
-    s_red[threadIdx.x] = v;
-    __syncthreads();
-    for (int o = kThreads / 2; o > 0; o >>= 1) {
-        if ((int)threadIdx.x < o) s_red[threadIdx.x] += s_red[threadIdx.x + o];
-        __syncthreads();
+__device__ __forceinline__ Teacher teacher(const Entries& x, int V, float it, int renorm) {
+    Teacher r;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const bool have = x.id[b] >= 0 && x.id[b] < V;
+        r.id[b] = have ? x.id[b] : -1;
+        r.lq[b] = have ? (renorm ? it * x.val[b] : x.val[b]) : -INFINITY;
     }
-    return s_red[0];
-}
-
-// m = max z, s = sum exp(it (z - m)), u = sum exp(d) d with d = it (z - m);
-// (-inf, 1, 0) for a row without an unmasked entry.
-template <int kBf16>
-__device__ __forceinline__ void row_stats(const Rows& r, int64_t t, float* s_red, float* m_out,
-                                          float* s_out, float* u_out) {
-    const int64_t b = t * r.ld;
-    float m = -INFINITY;
-    for (int64_t v = threadIdx.x; v < r.V; v += kThreads) {
-        const float z = ld_z<kBf16>(r.z, b + v);
-        m = (z != z || z > m) ? z : m;
-    }
-    m = group_max(m, s_red);
-    if (m == -INFINITY) {
-        *m_out = m; *s_out = 1.0f; *u_out = 0.0f;
-        return;
-    }
-    float s = 0.0f, u = 0.0f;
-    for (int64_t v = threadIdx.x; v < r.V; v += kThreads) {
-        const float d = (ld_z<kBf16>(r.z, b + v) - m) * r.it;
-        const float e = expf(d);
-        s += e;
-        u += e * fmaxf(d, -200.0f);
-    }
-    *m_out = m;
-    *s_out = group_sum(s, s_red);
-    *u_out = group_sum(u, s_red);
-}
-
-// The teacher's distribution over its list, in LDS: s_q[i] = q_i (0 for an
-// entry left out), returns Q = sum q; s_lq[i] = ln q_i.
-__device__ __forceinline__ float teacher(const float* val, const int32_t* id, int topk, int64_t V,
-                                         float it, int renorm, float* s_q, float* s_lq,
-                                         float* s_red) {
-    const int i = threadIdx.x;
-    const bool have = i < topk && id[i] >= 0 && id[i] < V;
-    float y = have ? (renorm ? it * val[i] : val[i]) : -INFINITY;
     if (renorm) {
-        const float m = group_max(y, s_red);
-        const float s = group_sum(y == -INFINITY ? 0.0f : expf(y - m), s_red);
-        y = y == -INFINITY ? y : y - m - logf(s);
+        const float m = stat_base(wave_max(fmaxf(r.lq[0], r.lq[1])));
+        const float s = wave_sum(expf(r.lq[0] - m) + expf(r.lq[1] - m));
+        const float ls = logf(s);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)            // an empty list has s = 0: nothing to normalise
+            r.lq[b] = r.id[b] < 0 || s == 0.0f ? -INFINITY : r.lq[b] - m - ls;
     }
-    const float q = expf(y);
-    if (i < topk) { s_q[i] = q; s_lq[i] = y; }
-    return group_sum(q, s_red);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) r.q[b] = expf(r.lq[b]);
+    r.all = wave_sum(r.q[0] + r.q[1]);
+    return r;
 }
 
-// mode bits: 1 = loss and stats from the logits, 2 = gradient
-template <int kBf16, int kMode>
-__global__ __launch_bounds__(kThreads) void k_topk_distill(Rows r, const float* t_val,
-                                                           const int32_t* t_id, int topk,
-                                                           const float* weight, int renorm,
-                                                           float* loss, float* stats,
-                                                           const float* stats_in, const float* g,
-                                                           void* dz) {
-    __shared__ float s_red[kThreads], s_q[QUADS_TOP_MAX], s_lq[QUADS_TOP_MAX];
-    const int64_t t = blockIdx.x;
-    const float w = weight ? weight[t] : 1.0f;
-    if (w == 0.0f) {
-        if ((kMode & 1) && threadIdx.x == 0) {
-            loss[t] = 0.0f;
-            if (stats) stats[2 * t] = stats[2 * t + 1] = 0.0f;
+// sum_i q_i (ln q_i - ln p_i) over the wave, z the logits at the entries' ids.
+__device__ __forceinline__ float cross(const Teacher& a, const float z[2], float m, float ls,
+                                       float it) {
+    float y = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+        if (!(a.q[b] == 0.0f)) y += a.q[b] * (a.lq[b] - ln_p(z[b], m, ls, it));
+    return wave_sum(y);
+}
+
+// The logits at a lane's entries (-inf where there is none).
+template <int kBf16>
+__device__ __forceinline__ void gather(const Row<kBf16>& r, const Teacher& a, float z[2]) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) z[b] = a.id[b] >= 0 ? r.entry(a.id[b]) : -INFINITY;
+}
+
+// Gradients at the list's ids: by (Q p - q), q summed over the entries with
+// the same id in the list's order, so that every one of them has the same
+// value.  One wave; the list and the gradients stay in LDS until the dense
+// ones are written.
+struct Parked {
+    int id[QUADS_TOP_MAX];
+    float q[QUADS_TOP_MAX], g[QUADS_TOP_MAX];
+};
+__device__ __forceinline__ void at_entries(const Teacher& a, const float z[2], int topk, float by,
+                                           float m, float ls, float it, Parked& p) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        p.id[lane + 64 * b] = a.id[b];
+        p.q[lane + 64 * b] = a.q[b];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    float q[2] = {0.0f, 0.0f};
+    for (int i = 0; i < topk; ++i)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) q[b] += p.id[i] == a.id[b] ? p.q[i] : 0.0f;
+    const bool none = m == -INFINITY && ls == ls;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const float d = __builtin_fmaf(z[b] - stat_base(m), it * kLog2e, -ls * kLog2e);
+        p.g[lane + 64 * b] =
+            none ? 0.0f : by * __builtin_fmaf(a.all, __builtin_amdgcn_exp2f(d), -q[b]);
+    }
+}
+template <int kBf16>
+__device__ __forceinline__ void patch(const Row<kBf16>& r, char* at, const Parked& p, int v0,
+                                      int v1) {
+    for (int i = threadIdx.x; i < QUADS_TOP_MAX; i += 64) {
+        const int v = p.id[i];
+        if (v >= v0 && v < v1) {
+            if (kBf16)
+                ((uint16_t*)at)[r.shift + v] = __builtin_bit_cast(uint16_t, (__bf16)p.g[i]);
+            else
+                ((float*)at)[r.shift + v] = p.g[i];
         }
-        if (kMode & 2)
-            for (int64_t v = threadIdx.x; v < r.V; v += kThreads) st_z<kBf16>(dz, t * r.ld + v, 0.0f);
+    }
+}
+
+// One vector's gradient by Q p (by Q = a): p = 2^((z - base) cl - l2).
+template <int kBf16>
+__device__ __forceinline__ uint4 dense(const uint4& q, float base, float cl, float l2, float a) {
+    float g[8];
+#pragma unroll
+    for (int e = 0; e < Row<kBf16>::kPer; ++e)
+        g[e] = a * __builtin_amdgcn_exp2f(__builtin_fmaf(get<kBf16>(q, e) - base, cl, -l2));
+    return put<kBf16>(g);
+}
+template <int kBf16>
+__device__ __forceinline__ float vec_max(const uint4& q, float m) {
+#pragma unroll
+    for (int e = 0; e < Row<kBf16>::kPer; ++e) m = fmaxf(m, get<kBf16>(q, e));
+    return m;
+}
+template <int kBf16>
+__device__ __forceinline__ float vec_sum(const uint4& q, float base, float cl, float s) {
+#pragma unroll
+    for (int e = 0; e < Row<kBf16>::kPer; ++e)
+        s += __builtin_amdgcn_exp2f((get<kBf16>(q, e) - base) * cl);
+    return s;
+}
+
+// A vector that the compiler must take as new: without it the fp32 values of
+// one pass over a row kept in registers would be kept for the next one too,
+// three times the registers.
+__device__ __forceinline__ void pin(uint4& q) {
+    asm volatile("" : "+v"(q.x), "+v"(q.y), "+v"(q.z), "+v"(q.w));
+}
+
+// ------------------------------------------------------------------ streaming --
+
+// Loss and stats of a row from its statistics (one wave).
+template <int kBf16>
+__device__ __forceinline__ void finish_loss(const Row<kBf16>& r, int64_t t, const Stat& a,
+                                            const List& l, float w, float it, float* loss,
+                                            float* stats) {
+    const Teacher q = teacher(load_entries(l, t), r.V, it, l.renorm);
+    float z[2];
+    gather<kBf16>(r, q, z);
+    const float ls = log_sum(a);
+    const float y = cross(q, z, a.m, ls, it);
+    if ((threadIdx.x & 63) == 0) {
+        loss[t] = w * y;
+        stats[2 * t] = a.m;
+        stats[2 * t + 1] = ls;
+    }
+}
+__device__ __forceinline__ void no_loss(int64_t t, float* loss, float* stats) {
+    loss[t] = 0.0f;
+    stats[2 * t] = 0.0f;
+    stats[2 * t + 1] = 0.0f;
+}
+
+template <int kBf16>
+__global__ __launch_bounds__(kThreads) void k_distill_loss(const void* z, int64_t V, int64_t ld,
+                                                           int parts, List l, float it,
+                                                           float* loss, float* stats,
+                                                           float4* part_stat) {
+    __shared__ Stat s_stat[kThreads / 64];
+    const int64_t t = blockIdx.x / (unsigned)parts;
+    const int part = (int)(blockIdx.x % (unsigned)parts);
+    const float w = l.weight ? l.weight[t] : 1.0f;
+    if (w == 0.0f) {
+        if (parts == 1 && threadIdx.x == 0) no_loss(t, loss, stats);
         return;
     }
-    t_val += t * topk;
-    t_id += t * topk;
-    const float q_all = teacher(t_val, t_id, topk, r.V, r.it, renorm, s_q, s_lq, s_red);
-    float m, ls;
-    if (kMode & 1) {
-        float s, u;
-        row_stats<kBf16>(r, t, s_red, &m, &s, &u);
-        ls = logf(s);
-        float y = 0.0f;
-        const int i = threadIdx.x;
-        if (i < topk && s_q[i] > 0.0f) {
-            const float z = ld_z<kBf16>(r.z, t * r.ld + t_id[i]);
-            y = s_q[i] * (s_lq[i] - (z == -INFINITY && m == m ? z : (z - m) * r.it - ls));
+    const Row<kBf16> r(z, t, ld, V);
+    const float cl = it * kLog2e;
+    const int chunks = (r.nvec + kChunk - 1) / kChunk;
+    const int c0 = (int)((int64_t)chunks * part / parts);
+    const int c1 = (int)((int64_t)chunks * (part + 1) / parts);
+    auto load = [&](uint4 (&q)[kVecs], int ch) {
+        if (ch >= c1) return;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int j = ch * kChunk + i * kThreads + threadIdx.x;
+            if (r.whole(j)) q[i] = *r.vec(j);
+            else q[i] = r.part(j);
         }
-        y = group_sum(y, s_red);
-        if (threadIdx.x == 0) {
-            loss[t] = w * y;
-            if (stats) { stats[2 * t] = m; stats[2 * t + 1] = ls; }
-        }
-    } else {
-        m = stats_in[2 * t];
-        ls = stats_in[2 * t + 1];
+    };
+    Stat a = {-INFINITY, 0.0f, 0.0f};
+    uint4 q[kVecs], next[kVecs];
+    load(next, c0);
+    for (int ch = c0; ch < c1; ++ch) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) q[i] = next[i];
+        load(next, ch + 1);
+        float m = a.m;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) m = vec_max<kBf16>(q[i], m);
+        stat_raise(a, m, cl);
+        const float base = stat_base(m);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) a.s = vec_sum<kBf16>(q[i], base, cl, a.s);
     }
-    if (kMode & 2) {
-        const float by = w * r.it * (g ? g[t] : 1.0f);
-        __syncthreads();
-        for (int64_t v = threadIdx.x; v < r.V; v += kThreads) {
-            float p = 0.0f;
-            if (m != -INFINITY) {
-                p = q_all * expf((ld_z<kBf16>(r.z, t * r.ld + v) - m) * r.it - ls);
-                for (int i = 0; i < topk; ++i) p -= t_id[i] == v ? s_q[i] : 0.0f;
-            }
-            st_z<kBf16>(dz, t * r.ld + v, by * p);
-        }
+    a = group_stat<kThreads / 64>(a, cl, s_stat);
+    if (parts > 1) {
+        if (threadIdx.x == 0) part_stat[blockIdx.x] = make_float4(a.m, a.s, 0.0f, 0.0f);
+    } else if (threadIdx.x < 64) {
+        finish_loss<kBf16>(r, t, a, l, w, it, loss, stats);
     }
 }
 
-int check_list(int64_t T, const float* t_val, const int32_t* t_id, int32_t topk,
-               const float* weight, int renorm) {
+// Joins the parts of a row: one wave, lane l part l.
+template <int kBf16>
+__global__ __launch_bounds__(64) void k_distill_join(const void* z, int64_t V, int64_t ld,
+                                                     int parts, List l, float it, float* loss,
+                                                     float* stats, const float4* part_stat) {
+    const int64_t t = blockIdx.x;
+    const float w = l.weight ? l.weight[t] : 1.0f;
+    if (w == 0.0f) {
+        if (threadIdx.x == 0) no_loss(t, loss, stats);
+        return;
+    }
+    Stat a = {-INFINITY, 0.0f, 0.0f};
+    if ((int)threadIdx.x < parts) {
+        const float4 q = part_stat[t * parts + threadIdx.x];
+        a = {q.x, q.y, q.z};
+    }
+    a = wave_stat(a, it * kLog2e);
+    finish_loss<kBf16>(Row<kBf16>(z, t, ld, V), t, a, l, w, it, loss, stats);
+}
+
+template <int kBf16>
+__global__ __launch_bounds__(kThreads) void k_distill_bwd(const void* z, int64_t V, int64_t ld,
+                                                          int parts, List l, float it,
+                                                          const float* stats, const float* g,
+                                                          void* dz) {
+    __shared__ Parked s_list;
+    const int64_t t = blockIdx.x / (unsigned)parts;
+    const int part = (int)(blockIdx.x % (unsigned)parts);
+    const Row<kBf16> r(z, t, ld, V);
+    char* out = (char*)dz + (r.at - (const char*)z);
+    const int chunks = (r.nvec + kChunk - 1) / kChunk;
+    const int c0 = (int)((int64_t)chunks * part / parts);
+    const int c1 = (int)((int64_t)chunks * (part + 1) / parts);
+    const float w = l.weight ? l.weight[t] : 1.0f;
+    if (w == 0.0f) {
+        for (int j = c0 * kChunk + threadIdx.x; j < c1 * kChunk && j < r.nvec; j += kThreads)
+            store_vec<kBf16>(r, out, j, make_uint4(0, 0, 0, 0));
+        return;
+    }
+    const float m = stats[2 * t], ls = stats[2 * t + 1];
+    const float by = w * it * (g ? g[t] : 1.0f);
+    const Teacher q = teacher(load_entries(l, t), r.V, it, l.renorm);
+    // the part's entries [v0, v1), their gradients parked before any store
+    const int v0 = c0 ? r.index(c0 * kChunk, 0) : 0, v1 = r.index(c1 * kChunk, 0);
+    if (threadIdx.x < 64) {
+        float x[2];
+        gather<kBf16>(r, q, x);
+        at_entries(q, x, l.topk, by, m, ls, it, s_list);
+    }
+    __syncthreads();
+    const float base = stat_base(m), cl = it * kLog2e, l2 = ls * kLog2e, a = by * q.all;
+    for (int ch = c0; ch < c1; ++ch) {
+        uint4 x[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int j = ch * kChunk + i * kThreads + threadIdx.x;
+            if (r.whole(j)) x[i] = *r.vec(j);
+            else x[i] = r.part(j);
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int j = ch * kChunk + i * kThreads + threadIdx.x;
+            if (j < r.nvec) store_vec<kBf16>(r, out, j, dense<kBf16>(x[i], base, cl, l2, a));
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) patch<kBf16>(r, out, s_list, v0, v1);
+}
+
+// ------------------------------------------------------- loss and gradient --
+
+// One row at a time, read once: a thread keeps kNv of the row's vectors in
+// registers between the log-sum and the gradient (a CU's registers hold 256
+// KB of a row: 131072 bf16 or 65536 fp32 entries); what a longer row has
+// beyond them is read a second time.  The work-groups are resident ones that
+// walk over the rows: a vector of the next row is requested into the registers
+// of the one whose gradient was just stored, so that loads, stores and
+// arithmetic overlap although a CU holds one row at a time.  The partial
+// vectors at a row's ends are in one more register vector of threads 0 and 1.
+template <int kBf16, int kThr, int kNv>
+__global__ __launch_bounds__(kThr, 4) void k_distill_row(const void* z, int64_t T, int64_t V,
+                                                      int64_t ld, List l, float it, float* loss,
+                                                      void* dz) {
+    constexpr int kPer = Row<kBf16>::kPer;
+    __shared__ Stat s_stat[kThr / 64];
+    __shared__ Parked s_list;
+    const uint4 masked = kBf16 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
+                               : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+    const float cl = it * kLog2e;
+    const int tid = threadIdx.x;
+
+    uint4 x[kNv], edge;
+    // the whole vectors of a row are first .. first + count - 1
+    auto first = [](const Row<kBf16>& r) { return r.shift ? 1 : 0; };
+    auto count = [](const Row<kBf16>& r) { return (r.V + r.shift) / kPer - (r.shift ? 1 : 0); };
+    // the partial vector this thread holds, or -1
+    auto edge_at = [&](const Row<kBf16>& r) {
+        const int last = (r.V + r.shift) % kPer ? r.nvec - 1 : -1;
+        if (tid == 0) return r.shift ? 0 : -1;
+        return tid == 1 && (last > 0 || !r.shift) ? last : -1;
+    };
+    // vector i of the `n` whole ones of a row, -inf past them; addressed as a
+    // uniform base plus 16 tid (one register)
+    const uint32_t lane16 = 16u * (uint32_t)tid;
+    auto load = [&](const Row<kBf16>& r, int n, int i) {
+        const char* at = r.at + 16 * (int64_t)(first(r) + i * kThr);
+        x[i] = masked;
+        if (i * kThr + tid < n) x[i] = *reinterpret_cast<const uint4*>(at + lane16);
+    };
+    auto load_edge = [&](const Row<kBf16>& r, bool live) {
+        const int j = live ? edge_at(r) : -1;
+        edge = masked;
+        if (j >= 0) edge = r.part(j);
+    };
+
+    int64_t t = blockIdx.x;
+    Entries e = load_entries(l, t);
+    float w = l.weight ? l.weight[t] : 1.0f;
+    {
+        const Row<kBf16> r(z, t, ld, V);
+        load_edge(r, w != 0.0f);
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) load(r, w != 0.0f ? count(r) : 0, i);
+    }
+    for (; t < T; t += gridDim.x) {
+        const Row<kBf16> r(z, t, ld, V);
+        char* out = (char*)dz + (r.at - (const char*)z);
+        // the next row's list and weight; a row of weight 0 is not read but
+        // taken as masked throughout, which gives the gradient 0
+        const int64_t tn = t + gridDim.x < T ? t + gridDim.x : t;
+        const Entries en = load_entries(l, tn);
+        const float wn = l.weight ? l.weight[tn] : 1.0f;
+        const Row<kBf16> rn(z, tn, ld, V);
+        const bool more = tn != t && wn != 0.0f;
+        const int n = count(r), beyond = w != 0.0f ? n : 0, nn = more ? count(rn) : 0;
+
+        Teacher q = teacher(e, r.V, it, l.renorm);
+        if (w == 0.0f) q.id[0] = q.id[1] = -1;
+        float zq[2];
+        if (tid < 64) gather<kBf16>(r, q, zq);
+        // log-sum: the vectors in registers, then those beyond them
+        Stat a = {vec_max<kBf16>(edge, -INFINITY), 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            a.m = vec_max<kBf16>(x[i], a.m);
+            pin(x[i]);
+        }
+        float base = stat_base(a.m);
+        a.s = vec_sum<kBf16>(edge, base, cl, 0.0f);
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            a.s = vec_sum<kBf16>(x[i], base, cl, a.s);
+            pin(x[i]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        for (int i = kNv * kThr + tid; i < beyond; i += kThr) {
+            const uint4 y = *r.vec(first(r) + i);
+            stat_raise(a, vec_max<kBf16>(y, a.m), cl);
+            a.s = vec_sum<kBf16>(y, stat_base(a.m), cl, a.s);
+        }
+        a = group_stat<kThr / 64>(a, cl, s_stat);
+        const float ls = log_sum(a), by = w * it;
+        if (tid < 64) {
+            const float y = cross(q, zq, a.m, ls, it);
+            if (tid == 0) loss[t] = w == 0.0f ? 0.0f : w * y;
+            at_entries(q, zq, l.topk, by, a.m, ls, it, s_list);
+        }
+        // gradient
+        base = stat_base(a.m);
+        const float l2 = ls * kLog2e, f = w == 0.0f ? 0.0f : by * q.all;
+        for (int i = kNv * kThr + tid; i < n; i += kThr) {
+            const int j = first(r) + i;
+            uint4 y = masked;
+            if (i < beyond) y = *r.vec(j);
+            reinterpret_cast<uint4*>(out)[j] = dense<kBf16>(y, base, cl, l2, f);
+        }
+        const int j = edge_at(r);
+        if (j >= 0) store_part<kBf16>(r, out, j, dense<kBf16>(edge, base, cl, l2, f));
+        load_edge(rn, more);
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            const uint4 y = dense<kBf16>(x[i], base, cl, l2, f);
+            char* to = out + 16 * (int64_t)(first(r) + i * kThr);
+            if (i * kThr + tid < n) *reinterpret_cast<uint4*>(to + lane16) = y;
+            load(rn, nn, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();
+        if (tid < 64) patch<kBf16>(r, out, s_list, 0, r.V);
+        e = en;
+        w = wn;
+    }
+}
+
+inline int check_list(int64_t T, const float* t_val, const int32_t* t_id, int32_t topk,
+                      const float* weight, int renorm) {
     if (topk < 1 || topk > QUADS_TOP_MAX) return QUADS_ESHAPE;
     if (renorm != 0 && renorm != 1) return QUADS_EINVAL;
     if (T == 0) return QUADS_OK;
     return ok_ptr4(t_val) && ok_ptr4(t_id) && ok_opt4(weight) ? QUADS_OK : QUADS_EINVAL;
+}
+
+// Work-groups of k_distill_row that are resident together, for rows of nvec
+// vectors: the smallest work-group whose registers hold a row.
+constexpr int kCus = 256;
+inline int row_threads(int64_t nvec) { return nvec <= 16 * 256 ? 256 : nvec <= 16 * 512 ? 512 : 1024; }
+inline int64_t row_slots(int64_t nvec) { return (int64_t)kCus * (1024 / row_threads(nvec)); }
+inline int64_t row_vectors(int64_t V, int dtype) {
+    const int per = dtype == QUADS_OUT_BF16 ? 8 : 4;
+    return (V + per - 1) / per;
+}
+// Rows enough for k_distill_row: each resident work-group has at least two.
+inline bool whole_rows(int64_t T, int64_t V, int dtype) {
+    return T >= 2 * row_slots(row_vectors(V, dtype));
+}
+
+template <int kBf16>
+void launch_loss(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, float it,
+                 float* loss, float* stats, void* ws, hipStream_t st) {
+    const int parts = row_parts(T, V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32);
+    hipLaunchKernelGGL(k_distill_loss<kBf16>, dim3((unsigned)(T * parts)), dim3(kThreads), 0, st, z,
+                       V, ld, parts, l, it, loss, stats, (float4*)ws);
+    if (parts > 1)
+        hipLaunchKernelGGL(k_distill_join<kBf16>, dim3((unsigned)T), dim3(64), 0, st, z, V, ld,
+                           parts, l, it, loss, stats, (const float4*)ws);
+}
+template <int kBf16>
+void launch_bwd(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, float it,
+                const float* stats, const float* g, void* dz, hipStream_t st) {
+    const int parts = row_parts(T, V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32);
+    hipLaunchKernelGGL(k_distill_bwd<kBf16>, dim3((unsigned)(T * parts)), dim3(kThreads), 0, st, z,
+                       V, ld, parts, l, it, stats, g, dz);
+}
+template <int kBf16>
+void launch_row(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, float it,
+                float* loss, void* dz, hipStream_t st) {
+    const int64_t nvec = row_vectors(V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32);
+    const int thr = row_threads(nvec);
+    const int64_t slots = row_slots(nvec);
+    const dim3 grid((unsigned)(T < slots ? T : slots)), block(thr);
+    if (thr == 256)
+        hipLaunchKernelGGL((k_distill_row<kBf16, 256, 16>), grid, block, 0, st, z, T, V, ld, l, it,
+                           loss, dz);
+    else if (thr == 512)
+        hipLaunchKernelGGL((k_distill_row<kBf16, 512, 16>), grid, block, 0, st, z, T, V, ld, l, it,
+                           loss, dz);
+    else
+        hipLaunchKernelGGL((k_distill_row<kBf16, 1024, 16>), grid, block, 0, st, z, T, V, ld, l,
+                           it, loss, dz);
+}
+
+// Workspace: the parts' statistics, then the rows' stats (which
+// quads_topk_distill_grad keeps there between its two steps).
+inline size_t parts_ws(int64_t T, int64_t V) {
+    const int parts = row_parts(T, V, QUADS_OUT_F32);
+    return parts > 1 ? align_up((size_t)T * parts * 16, 16) : 0;
 }
 
 }  // namespace head
@@ -163,24 +495,9 @@ int check_list(int64_t T, const float* t_val, const int32_t* t_id, int32_t topk,
 using namespace quads;
 
 extern "C" size_t quads_topk_distill_ws(int64_t T, int64_t V, int32_t topk) {
-    (void)T; (void)V; (void)topk;
-    return 0;
+    if (T < 1 || V < 1 || topk < 1) return 0;
+    return head::parts_ws(T, V) + align_up((size_t)T * 8, 16);
 }
-
-#define QUADS_DISTILL(MODE, ...)                                                               \
-    do {                                                                                       \
-        const head::Rows r{logits, T, V, ld, inv_temp};                                        \
-        const dim3 grid((unsigned)T), block(head::kThreads);                                   \
-        hipStream_t st = (hipStream_t)stream;                                                  \
-        if (dtype == QUADS_OUT_BF16)                                                           \
-            hipLaunchKernelGGL((head::k_topk_distill<1, MODE>), grid, block, 0, st, r, t_val,  \
-                               t_id, (int)topk, weight, renorm, __VA_ARGS__);                  \
-        else                                                                                   \
-            hipLaunchKernelGGL((head::k_topk_distill<0, MODE>), grid, block, 0, st, r, t_val,  \
-                               t_id, (int)topk, weight, renorm, __VA_ARGS__);                  \
-        QUADS_CHECK_LAUNCH();                                                                  \
-        return QUADS_OK;                                                                       \
-    } while (0)
 
 extern "C" int quads_topk_distill(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
                                   const float* t_val, const int32_t* t_id, int32_t topk,
@@ -190,9 +507,14 @@ extern "C" int quads_topk_distill(const void* logits, int dtype, int64_t T, int6
     if (rc == QUADS_OK) rc = head::check_list(T, t_val, t_id, topk, weight, renorm);
     if (rc != QUADS_OK || T == 0) return rc;
     if (!ok_ptr4(loss) || !ok_ptr4(stats)) return QUADS_EINVAL;
-    const size_t need = quads_topk_distill_ws(T, V, topk);
-    if (ws_bytes < need || (need > 0 && !ok_ptr(ws))) return QUADS_EWORKSPACE;
-    QUADS_DISTILL(1, loss, stats, (const float*)nullptr, (const float*)nullptr, (void*)nullptr);
+    if (ws_bytes < quads_topk_distill_ws(T, V, topk) || !ok_ptr(ws)) return QUADS_EWORKSPACE;
+    const head::List l{t_val, t_id, weight, (int)topk, renorm};
+    if (dtype == QUADS_OUT_BF16)
+        head::launch_loss<1>(logits, T, V, ld, l, inv_temp, loss, stats, ws, (hipStream_t)stream);
+    else
+        head::launch_loss<0>(logits, T, V, ld, l, inv_temp, loss, stats, ws, (hipStream_t)stream);
+    QUADS_CHECK_LAUNCH();
+    return QUADS_OK;
 }
 
 extern "C" int quads_topk_distill_backward(const void* logits, int dtype, int64_t T, int64_t V,
@@ -204,7 +526,13 @@ extern "C" int quads_topk_distill_backward(const void* logits, int dtype, int64_
     if (rc == QUADS_OK) rc = head::check_list(T, t_val, t_id, topk, weight, renorm);
     if (rc != QUADS_OK || T == 0) return rc;
     if (!ok_ptr4(stats) || !ok_ptr4(g) || !ok_ptr(dlogits)) return QUADS_EINVAL;
-    QUADS_DISTILL(2, (float*)nullptr, (float*)nullptr, stats, g, dlogits);
+    const head::List l{t_val, t_id, weight, (int)topk, renorm};
+    if (dtype == QUADS_OUT_BF16)
+        head::launch_bwd<1>(logits, T, V, ld, l, inv_temp, stats, g, dlogits, (hipStream_t)stream);
+    else
+        head::launch_bwd<0>(logits, T, V, ld, l, inv_temp, stats, g, dlogits, (hipStream_t)stream);
+    QUADS_CHECK_LAUNCH();
+    return QUADS_OK;
 }
 
 extern "C" int quads_topk_distill_grad(const void* logits, int dtype, int64_t T, int64_t V,
@@ -216,7 +544,23 @@ extern "C" int quads_topk_distill_grad(const void* logits, int dtype, int64_t T,
     if (rc == QUADS_OK) rc = head::check_list(T, t_val, t_id, topk, weight, renorm);
     if (rc != QUADS_OK || T == 0) return rc;
     if (!ok_ptr4(loss) || !ok_ptr(dlogits)) return QUADS_EINVAL;
-    const size_t need = quads_topk_distill_ws(T, V, topk);
-    if (ws_bytes < need || (need > 0 && !ok_ptr(ws))) return QUADS_EWORKSPACE;
-    QUADS_DISTILL(3, loss, (float*)nullptr, (const float*)nullptr, (const float*)nullptr, dlogits);
+    if (ws_bytes < quads_topk_distill_ws(T, V, topk) || !ok_ptr(ws)) return QUADS_EWORKSPACE;
+    const head::List l{t_val, t_id, weight, (int)topk, renorm};
+    hipStream_t st = (hipStream_t)stream;
+    const bool bf16 = dtype == QUADS_OUT_BF16;
+    if (head::whole_rows(T, V, dtype)) {
+        if (bf16) head::launch_row<1>(logits, T, V, ld, l, inv_temp, loss, dlogits, st);
+        else head::launch_row<0>(logits, T, V, ld, l, inv_temp, loss, dlogits, st);
+    } else {
+        float* stats = (float*)((char*)ws + head::parts_ws(T, V));
+        if (bf16) {
+            head::launch_loss<1>(logits, T, V, ld, l, inv_temp, loss, stats, ws, st);
+            head::launch_bwd<1>(logits, T, V, ld, l, inv_temp, stats, nullptr, dlogits, st);
+        } else {
+            head::launch_loss<0>(logits, T, V, ld, l, inv_temp, loss, stats, ws, st);
+            head::launch_bwd<0>(logits, T, V, ld, l, inv_temp, stats, nullptr, dlogits, st);
+        }
+    }
+    QUADS_CHECK_LAUNCH();
+    return QUADS_OK;
 }

@@ -148,18 +148,10 @@ __device__ __forceinline__ Stat group_stat(Stat a, float c, Stat* s_stat) {
     a = wave_stat(a, c);
     if ((threadIdx.x & 63) == 0) s_stat[threadIdx.x >> 6] = a;
     __syncthreads();
-    float m = s_stat[0].m;
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, s_stat[w].m);
-    Stat r = {m, 0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        Stat b = s_stat[w];
-        stat_raise(b, m, c);
-        r.s += b.s;
-        r.u += b.u;
-    }
-    return r;
+    const int l = threadIdx.x & 63;
+    Stat b = {-INFINITY, 0.0f, 0.0f};
+    if (l < kWaves) b = s_stat[l];
+    return wave_stat(b, c);
 }
 
 // ln sum exp(it (z - m)): 0 for a row without an unmasked entry.

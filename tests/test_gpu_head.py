@@ -354,6 +354,60 @@ def test_distill(Q, t, v, ld, k, renorm, dtype):
     check_distill(Q, z, zr, k, 0.6 if k % 2 else 1.0, renorm, dtype)
 
 
+@pytest.mark.parametrize("t,v,ld,dtype,k", [
+    (2100, 700, None, "bf16", 5), (2053, 1025, 1032, "f32", 70), (2048, 16383, None, "f32", 9),
+    (1030, 32771, 32776, "bf16", 20), (1025, 16405, None, "f32", 4), (515, 65539, None, "bf16", 64),
+    (513, 65537, None, "f32", 33), (512, 131081, None, "bf16", 128)])
+def test_distill_many_rows(Q, t, v, ld, dtype, k):
+    """Loss and gradient of many rows in one call: rows held by each size of work-group, rows
+    longer than its registers, partial vectors at both ends, rows of weight 0 in between, lists
+    with repeated and left-out ids.  Every seventh row against the oracle, all rows against the
+    backward call's gradient (both are within the tolerance, so they differ by twice that)."""
+    print(f"distill rows T={t} V={v} ld={ld} {dtype} k={k}", flush=True)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device=DEV).manual_seed(v)
+    full = torch.full((t, ld or v), 7.5, dtype=dt, device=DEV)
+    full[:, :v] = torch.randn((t, v), generator=g, device=DEV) * 2
+    z = full[:, :v]
+    z[3::50] = -float("inf")
+    z[5::50, : v // 2] = -float("inf")
+    t_val, t_id = (z.float() + torch.randn((t, v), generator=g, device=DEV)).topk(k, 1)
+    t_val, t_id = t_val.clamp(min=-60.0), t_id.int()
+    t_id[1::9, k // 2:] = -1
+    t_id[2::9] = v
+    t_id[4::9, -1] = t_id[4::9, 0]
+    t_id[6::9, 0] = v - 1
+    t_id[7::9, 0] = 0
+    w = torch.rand(t, generator=g, device=DEV) + 0.5
+    w[::5] = 0.0
+    loss, dz = Q.quads_topk_distill_grad(z, t_val, t_id, w, 0.8)
+    loss1, stats = Q.quads_topk_distill(z, t_val, t_id, w, 0.8)
+    dz1 = Q.quads_topk_distill_backward(z, t_val, t_id, stats, torch.ones(t, device=DEV), w, 0.8)
+    torch.cuda.synchronize()
+    assert bool((full[:, v:] == 7.5).all())
+    rows = np.unique(np.r_[np.arange(0, t, 7 if v < 20000 else 31), t - 1])
+    zr = z[rows].double().cpu().numpy()
+    tv, ti, wr = (a[rows].cpu().numpy() for a in (t_val, t_id, w))
+    one = np.ones(len(rows))
+    want = OH.distill(zr, tv, ti, wr, 0.8)
+    want_dz = OH.distill_grad(zr, tv, ti, one, wr, 0.8)
+    tol, tol_dz = distill_tolerance(zr, tv, ti, wr.astype(np.float64), one, 0.8, True, dtype,
+                                    want_dz)
+    for a, b in ((loss, dz), (loss1, dz1)):
+        close(a[rows], want, tol)
+        close(b[rows], want_dz, tol_dz)
+    # fp32: p to about (6 |d| + V / 256 + 64) u from either side, |d| < 100; bf16: two half steps
+    rel = 2 * (700 + v / 256) * U + (2 ** -7 if dtype == "bf16" else 0)
+    scale = torch.maximum(dz.float().abs(), dz1.float().abs())
+    diff = (dz.float() - dz1.float()).abs()
+    at_list = torch.zeros((t, v), device=DEV)
+    at_list.scatter_(1, t_id.clamp(0, v - 1).long(), 1.0)        # differences of near numbers
+    assert bool((diff <= rel * (scale + 2.0 * at_list) + 2.0 ** -120).all())
+    out = z.clone() if ld is None else z                         # in place
+    _, dz2 = Q.quads_topk_distill_grad(out, t_val, t_id, w, 0.8, out=out)
+    assert torch.equal(dz2, dz)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_distill_masked_rows_and_in_place(Q, dtype):
     z, zr = make(9, 5003, dtype, seed=6, masked=0.4, empty=(6,))
