@@ -1,5 +1,41 @@
 // W4A16 grouped product for few rows per expert (include/quads_head.h): bf16
 // activations times NVFP4 weights, arXiv 2607.15810, Eq. (12).
+//
+//   Y[p, n] = s_tW[e] sum_j x[row(p), j] v_w[n, j] s_b[n, j / 16]
+//
+// What bounds it is the weights' stream from HBM, 0.5625 bytes per weight, so
+// every weight is loaded once per kRt * 16 rows, straight into the registers
+// of the wave that uses it, as wide as it lies, and multiplied on the matrix
+// cores, where up to 16 rows cost no more than one.
+//
+// Operands.  A weight's v * s_b has at most 6 significant bits and lies in
+// [2^-10, 2688]: exact in fp16, converted by the hardware's fp4 convert and
+// one packed multiply per two weights.  bf16 has no packed multiply, so the
+// activations are brought to fp16 instead: every 512 channels of a row are
+// scaled by the power of two that puts their largest magnitude in [2^14,
+// 2^15), exact for every activation down to 2^-28 of that largest one (below
+// it the error is at most 2^-28 of the largest), and the scale goes into the
+// fp32 total when the matrix cores' accumulator is added to it, every 512
+// channels (gfx950's fp16 MFMA rounds once per 8 products: 64 roundings).
+//
+// Layout.  A work-group has kWaves waves; a wave owns two tiles of 16
+// features (SwiGLU: 16 gate features and the 16 up features that belong to
+// them) and streams them in blocks of 512 channels.  Lane (r, h) = (lane %
+// 16, lane / 16) holds feature r: of each 128-channel chunk the 32 codes from
+// channel 32 h on (one 16-byte load, 64 contiguous bytes per feature and
+// load), and step j of a chunk multiplies the lane's codes 8 j .. 8 j + 7, so
+// the channels of the four h interleave; the activations are read from LDS in
+// the same order.  The registers of a chunk are filled again, with that chunk
+// of the wave's next block, as soon as it has been multiplied.
+//   The block scales of 512 channels of a feature are 32 bytes: lane (r, h)
+// loads the 8 of chunk h, and the four lanes of a feature exchange them in
+// registers (row swaps), so that each has its two of every chunk.
+//   The activations, few and read by every wave, are in LDS for as many blocks
+// as fit.
+//
+// Where there are too few features to fill the GPU, kw waves of the
+// work-group share a pair of tiles, each taking every kw-th block, and their
+// totals are added in LDS in wave order.
 #include "common.h"
 #include "gemm_tiles.h"
 #include "../../include/quads_head.h"
@@ -7,54 +43,358 @@
 namespace quads {
 namespace w4a16 {
 
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 8;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kChunk = 128;                    // channels per 16-byte load
+constexpr int kBlk = 512;                      // channels per block
+constexpr int kLdsX = 72 << 10;                // bytes for the activations: two work-groups a CU
+
 struct Args {
-    const uint16_t* x; const int32_t* row_token; int64_t rows; int64_t K;
+    const uint16_t* x; const int32_t* row_token; int rows; int K;
     const uint8_t* w_nib; const uint8_t* w_scale; const float* w_ts; const int32_t* offsets;
-    int E; int64_t N;
+    int E; int N;
     int out_bf16; void* out;
+    int kw;                                    // waves per pair of tiles
+    int slabs;                                 // work-groups per unit of rows
+    int sb;                                    // blocks of activations in LDS at once
+    int rcap;                                  // rows of LDS
 };
 
-// Dot product of the activation row with weight row n of expert e, by a wave.
-__device__ __forceinline__ float dot(const Args& a, const uint16_t* x, int e, int64_t n) {
-    const int lane = threadIdx.x & 63;
-    const uint8_t* w = a.w_nib + ((int64_t)e * a.N + n) * (a.K / 2);
-    const uint8_t* sc = a.w_scale + ((int64_t)e * a.N + n) * (a.K / kBlock);
-    float acc = 0.0f;
-    for (int64_t b = lane; b < a.K / kBlock; b += 64) {
-        float s = 0.0f;
-        for (int h = 0; h < 2; ++h) {
-            float v[8];
-            decode8(reinterpret_cast<const uint32_t*>(w)[2 * b + h], v);
-            for (int i = 0; i < 8; ++i)
-                s = __builtin_fmaf(v[i], bf16_to_f32(x[kBlock * b + 8 * h + i]), s);
-        }
-        acc = __builtin_fmaf(s, e4m3_value(sc[b]), acc);
-    }
-    for (int o = 32; o > 0; o >>= 1) acc += __shfl_xor(acc, o);
-    return acc * a.w_ts[e];
+// Unaligned wide loads: a feature's codes start at a multiple of 8 bytes, its
+// scales anywhere.
+struct __attribute__((packed)) Bytes16 { u32x4 v; };
+struct __attribute__((packed)) Bytes8 { u32x2 v; };
+
+// 8 codes (one dword) times a block scale -> 8 exact fp16 values.
+__device__ __forceinline__ f16x8 cvt8(uint32_t w, _Float16 s) {
+    const f16x2 s2 = {s, s};
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s2;
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * s2;
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * s2;
+    const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * s2;
+    return (f16x8){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// One wave per output feature, over the packed rows in turn.
-template <int kEpi>
-__global__ __launch_bounds__(256) void k_gemv(Args a) {
-    const int64_t ncols = kEpi == QUADS_EPI_SWIGLU ? a.N / 2 : a.N;
-    const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (n >= ncols) return;
-    int e = 0;
-    for (int64_t p = 0; p < a.rows; ++p) {
-        if (a.offsets)
-            while (p >= a.offsets[e + 1]) ++e;
-        const int64_t row = a.row_token ? a.row_token[p] : p;
-        const uint16_t* x = a.x + row * a.K;
-        float y = dot(a, x, e, n);
-        if (kEpi == QUADS_EPI_SWIGLU) y = silu_mul(y, dot(a, x, e, n + ncols));
-        if ((threadIdx.x & 63) == 0) {
-            if (a.out_bf16)
-                ((uint16_t*)a.out)[p * ncols + n] = __builtin_bit_cast(uint16_t, (__bf16)y);
-            else
-                ((float*)a.out)[p * ncols + n] = y;
+// A feature's codes of chunk `cc` for the lane: 32 from channel 128 cc + 32 h
+// on.  `at` points at the lane's share of chunk 0.  Codes past K read as 0.
+__device__ __forceinline__ uint4 load_codes(const uint8_t* at, int cc, int h, int K) {
+    const uint8_t* p = at + (int64_t)cc * (kChunk / 2);
+    if ((cc + 1) * kChunk <= K) {
+        const u32x4 v = reinterpret_cast<const Bytes16*>(p)->v;
+        return make_uint4(v.x, v.y, v.z, v.w);
+    }
+    const int k = cc * kChunk + 32 * h;
+    u32x2 lo = {0, 0}, hi = {0, 0};
+    if (k < K) lo = reinterpret_cast<const Bytes8*>(p)->v;
+    if (k + 16 < K) hi = reinterpret_cast<const Bytes8*>(p + 8)->v;
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+// A feature's scales of chunk 4 b + h (8 bytes); 0 past K.
+__device__ __forceinline__ u32x2 load_scales(const uint8_t* at, int b, int h, int K) {
+    const int cc = 4 * b + h;
+    const uint8_t* p = at + (int64_t)cc * (kChunk / kBlock);
+    u32x2 v = {0, 0};
+    if ((cc + 1) * kChunk <= K) {
+        v = reinterpret_cast<const Bytes8*>(p)->v;
+    } else {
+        const int n = K / kBlock - cc * (kChunk / kBlock);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) v[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    }
+    return v;
+}
+
+// From the scales of chunk h to the lane's own two of every chunk (fp8 pairs
+// in the low 16 bits): lane h's pair of chunk c is bytes 2 h, 2 h + 1 of what
+// the lane of chunk c loaded.
+__device__ __forceinline__ void own_scales(u32x2 v, int h, uint32_t s[4]) {
+    const auto a = __builtin_amdgcn_permlane32_swap(v.x, v.y, false, false);
+    const auto e = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false);   // chunks 0, 1
+    const auto f = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);   // chunks 2, 3
+    const int sh = 16 * (h & 1);
+    s[0] = e[0] >> sh;
+    s[1] = e[1] >> sh;
+    s[2] = f[0] >> sh;
+    s[3] = f[1] >> sh;
+}
+
+// Dynamic LDS: [rcap][sb * 1024 + 16] bytes of fp16 activations, then [rcap][sb]
+// fp32 scales of their blocks; the totals of split waves reuse it.
+template <int kEpi, int kRt>
+__global__ __launch_bounds__(kThreads, kRt > 2 ? 2 : 4) void k_w4a16(Args g) {
+    constexpr bool swiglu = kEpi == QUADS_EPI_SWIGLU;
+    constexpr int kRows = 16 * kRt;
+    extern __shared__ __align__(16) char lds[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, h = lane >> 4;
+    const int slab = (int)(blockIdx.x % (unsigned)g.slabs);
+    const int rank = (int)(blockIdx.x / (unsigned)g.slabs);
+
+    // the unit of this rank: kRows rows of an expert, in expert order
+    int e = 0, p0 = kRows * rank, cnt = g.rows - p0;
+    if (g.offsets) {
+        const int per = (g.E + 63) / 64;
+        const int e0 = lane * per < g.E ? lane * per : g.E;
+        const int e1 = e0 + per < g.E ? e0 + per : g.E;
+        int na = 0;
+        for (int x = e0; x < e1; ++x) na += (g.offsets[x + 1] - g.offsets[x] + kRows - 1) / kRows;
+        const int inc = wave_incl_add(na);
+        if (rank >= __builtin_amdgcn_readlane(inc, 63)) return;
+        int found = -1, part = 0;
+        if (rank >= inc - na && rank < inc) {
+            int rr = rank - (inc - na);
+            for (int x = e0; x < e1; ++x) {
+                const int u = (g.offsets[x + 1] - g.offsets[x] + kRows - 1) / kRows;
+                if (rr < u) { found = x; part = rr; break; }
+                rr -= u;
+            }
+        }
+        const int src = __ffsll(__ballot(found >= 0)) - 1;
+        e = __builtin_amdgcn_readlane(found, src);
+        p0 = g.offsets[e] + kRows * __builtin_amdgcn_readlane(part, src);
+        cnt = g.offsets[e + 1] - p0;
+    }
+    if (cnt <= 0) return;
+    const int nr = cnt < kRows ? cnt : kRows;
+
+    // the wave's tiles and its blocks wk, wk + kw, ...
+    const int nout = swiglu ? g.N / 2 : g.N;
+    const int wk = wave % g.kw;
+    const int pair = slab * (kWaves / g.kw) + wave / g.kw;
+    const int nblk = (g.K + kBlk - 1) / kBlk;
+    int feat[2];
+    const uint8_t* nib[2];
+    const uint8_t* sc[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        feat[q] = swiglu ? 16 * pair : 32 * pair + 16 * q;         // of the output
+        int f = feat[q] + r < nout ? feat[q] + r : nout - 1;
+        if (swiglu) f += q * nout;
+        const int64_t row = (int64_t)e * g.N + f;
+        nib[q] = g.w_nib + row * (g.K / 2) + 16 * h;
+        sc[q] = g.w_scale + row * (g.K / kBlock);
+    }
+    const bool mine = feat[0] < nout;
+
+    uint4 code[2][4];
+    u32x2 scale[2];
+    if (mine && wk < nblk) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            scale[q] = load_scales(sc[q], wk, h, g.K);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) code[q][c] = load_codes(nib[q], 4 * wk + c, h, g.K);
         }
     }
+
+    f32x4 tot[2][kRt];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int t = 0; t < kRt; ++t) tot[q][t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    const int stride = g.sb * 2 * kBlk + 16;
+    float* xscale = (float*)(lds + (size_t)g.rcap * stride);
+    int xrow[kRt];
+#pragma unroll
+    for (int t = 0; t < kRt; ++t) xrow[t] = 16 * t + r < nr ? 16 * t + r : 0;
+
+    for (int s0 = 0; s0 < nblk; s0 += g.sb) {
+        const int sb = nblk - s0 < g.sb ? nblk - s0 : g.sb;
+        if (s0) __syncthreads();
+        // activations of blocks s0 .. s0 + sb - 1: a wave per (row, block)
+        for (int i = wave; i < nr * sb; i += kWaves) {
+            const int row = i / sb, b = i % sb;
+            const int64_t src = g.row_token ? g.row_token[p0 + row] : p0 + row;
+            const int k = (s0 + b) * kBlk + 8 * lane;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (k < g.K) v = *reinterpret_cast<const uint4*>(g.x + src * g.K + k);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t m = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) m = pk_max_u16(m, w[u] & 0x7FFF7FFFu);
+            m = wave_max_u32(umax32(m >> 16, m & 0xFFFFu));
+            // 2^(141 - ex) with ex the exponent of the largest magnitude; blocks
+            // below 2^-112 take the largest power that has a normal inverse
+            uint32_t ex = m >> 7;
+            ex = ex < 15u ? 15u : ex;
+            const float up = __uint_as_float((268u - ex) << 23);
+            f16x8 y;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                y[2 * u] = (_Float16)(__uint_as_float(w[u] << 16) * up);
+                y[2 * u + 1] = (_Float16)(__uint_as_float(w[u] & 0xFFFF0000u) * up);
+            }
+            *reinterpret_cast<f16x8*>(lds + row * stride + 2 * (b * kBlk + 8 * lane)) = y;
+            if (lane == 0) xscale[row * g.sb + b] = __uint_as_float((ex - 14u) << 23);
+        }
+        __syncthreads();
+        if (!mine) continue;
+        // the wave's blocks among them
+        const int first = s0 + (wk - s0 % g.kw + g.kw) % g.kw;
+        for (int b = first; b < s0 + sb; b += g.kw) {
+            const int next = b + g.kw;
+            f32x4 acc[2][kRt];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int t = 0; t < kRt; ++t) acc[q][t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t own[2][4];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                own_scales(scale[q], h, own[q]);
+                if (next < nblk) scale[q] = load_scales(sc[q], next, h, g.K);
+            }
+            const char* xb = lds + 2 * ((b - s0) * kBlk + 32 * h);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                f16x2 s[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    s[q] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(own[q][c], 1.0f, false);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f16x8 xf[kRt];
+#pragma unroll
+                    for (int t = 0; t < kRt; ++t)
+                        xf[t] = *reinterpret_cast<const f16x8*>(xb + xrow[t] * stride +
+                                                                2 * (kChunk * c + 8 * j));
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint4& w = code[q][c];
+                        const uint32_t x = j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w;
+                        const f16x8 wf = cvt8(x, s[q][j >> 1]);
+#pragma unroll
+                        for (int t = 0; t < kRt; ++t)
+                            acc[q][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf, xf[t],
+                                                                               acc[q][t], 0, 0, 0);
+                    }
+                }
+                if (next < nblk) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        code[q][c] = load_codes(nib[q], 4 * next + c, h, g.K);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int t = 0; t < kRt; ++t) {
+                const float f = xscale[xrow[t] * g.sb + b - s0];
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        tot[q][t][u] = __builtin_fmaf(acc[q][t][u], f, tot[q][t][u]);
+            }
+        }
+    }
+
+    // totals of the waves that share a pair: into LDS, added in wave order
+    if (g.kw > 1) {
+        __syncthreads();
+        f32x4* part = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int t = 0; t < kRt; ++t)
+                part[((wave * 2 + q) * kRt + t) * 64 + lane] = tot[q][t];
+        __syncthreads();
+        if (wk != 0) return;
+        for (int w = 1; w < g.kw; ++w)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int t = 0; t < kRt; ++t)
+                    tot[q][t] += part[(((wave + w) * 2 + q) * kRt + t) * 64 + lane];
+    }
+    if (!mine) return;
+
+    // lane (r, h) holds row 16 t + r of features 4 h .. 4 h + 3 of each tile
+    const float ts = g.w_ts[e];
+#pragma unroll
+    for (int t = 0; t < kRt; ++t) {
+        const bool have = 16 * t + r < nr;
+        const int64_t o = (int64_t)(p0 + 16 * t + r) * nout;
+#pragma unroll
+        for (int q = 0; q < (swiglu ? 1 : 2); ++q) {
+            const int n = feat[q] + 4 * h;
+            float y[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                y[u] = tot[q][t][u] * ts;
+                if (swiglu) y[u] = silu_mul(y[u], tot[1][t][u] * ts);
+            }
+            if (!have || n >= nout) continue;
+            if (g.out_bf16) {
+                uint16_t* a = (uint16_t*)g.out + o + n;
+                const uint32_t p01 = v2::pk_bf16(y[0], y[1]), p23 = v2::pk_bf16(y[2], y[3]);
+                if (n + 3 < nout && nout % 4 == 0) {
+                    *reinterpret_cast<uint2*>(a) = make_uint2(p01, p23);
+                } else {
+                    const uint32_t b4[4] = {p01, p01 >> 16, p23, p23 >> 16};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (n + u < nout) a[u] = (uint16_t)b4[u];
+                }
+            } else {
+                float* a = (float*)g.out + o + n;
+                if (n + 3 < nout && nout % 4 == 0) {
+                    *reinterpret_cast<float4*>(a) = make_float4(y[0], y[1], y[2], y[3]);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (n + u < nout) a[u] = y[u];
+                }
+            }
+        }
+    }
+}
+
+// Rows per unit: 16 while an expert has few rows on average, else up to 64, so
+// that its weights are read once.
+template <int kEpi, int kRt>
+int launch(Args g, hipStream_t st) {
+    constexpr int kRows = 16 * kRt;
+    const int nout = kEpi == QUADS_EPI_SWIGLU ? g.N / 2 : g.N;
+    const int tile = kEpi == QUADS_EPI_SWIGLU ? 16 : 32;
+    const int64_t pairs = ((int64_t)nout + tile - 1) / tile;
+    const int64_t units = g.offsets ? (int64_t)(g.E < g.rows ? g.E : g.rows) + g.rows / kRows
+                                    : ((int64_t)g.rows + kRows - 1) / kRows;
+    const int64_t live = g.offsets ? (g.E < g.rows ? g.E : g.rows) : units;
+    const int nblk = (g.K + kBlk - 1) / kBlk;
+    g.rcap = g.rows < kRows ? g.rows : kRows;
+    g.sb = kLdsX / (g.rcap * (2 * kBlk + 4) + 16);
+    if (g.sb > nblk) g.sb = nblk;
+    g.kw = 1;
+    while (g.kw < kWaves && live * ((pairs * g.kw + kWaves - 1) / kWaves) < 512 &&
+           2 * g.kw <= g.sb)
+        g.kw *= 2;
+    if (g.sb > g.kw) g.sb -= g.sb % g.kw;
+    const int64_t slabs = (pairs * g.kw + kWaves - 1) / kWaves;
+    if (slabs * units >= ((int64_t)1 << 31)) return QUADS_ESHAPE;
+    g.slabs = (int)slabs;
+    size_t bytes = (size_t)g.rcap * (g.sb * (2 * kBlk + 4) + 16);
+    const size_t join = g.kw > 1 ? (size_t)kWaves * 2 * kRt * 64 * 16 : 0;
+    if (join > bytes) bytes = join;
+    hipLaunchKernelGGL((k_w4a16<kEpi, kRt>), dim3((unsigned)(slabs * units)), dim3(kThreads),
+                       bytes, st, g);
+    QUADS_CHECK_LAUNCH();
+    return QUADS_OK;
+}
+
+template <int kEpi>
+int dispatch(const Args& g, hipStream_t st) {
+    const int64_t mean = g.offsets ? ((int64_t)g.rows + g.E - 1) / g.E : g.rows;
+    const int64_t most = g.offsets ? 2 * mean : mean;      // experts are not loaded evenly
+    if (most <= 16) return launch<kEpi, 1>(g, st);
+    if (most <= 32) return launch<kEpi, 2>(g, st);
+    return launch<kEpi, 4>(g, st);
 }
 
 }  // namespace w4a16
@@ -86,14 +426,10 @@ extern "C" int quads_moe_w4a16_gemv(const uint16_t* x, const int32_t* row_token,
         return QUADS_EINVAL;
     const size_t need = quads_moe_w4a16_gemv_ws(rows, K, E, N);
     if (ws_bytes < need || (need > 0 && !ok_ptr(ws))) return QUADS_EWORKSPACE;
-    const w4a16::Args a{x, row_token, rows, K, w_nib, w_scale, w_ts, offsets, (int)E, N,
-                        out_dtype == QUADS_OUT_BF16, out};
-    const int64_t ncols = epilogue == QUADS_EPI_SWIGLU ? N / 2 : N;
-    const dim3 grid((unsigned)((ncols + 3) / 4)), block(256);
-    if (epilogue == QUADS_EPI_SWIGLU)
-        hipLaunchKernelGGL(w4a16::k_gemv<QUADS_EPI_SWIGLU>, grid, block, 0, (hipStream_t)stream, a);
-    else
-        hipLaunchKernelGGL(w4a16::k_gemv<QUADS_EPI_NONE>, grid, block, 0, (hipStream_t)stream, a);
-    QUADS_CHECK_LAUNCH();
-    return QUADS_OK;
+    w4a16::Args g{};
+    g.x = x; g.row_token = row_token; g.rows = (int)rows; g.K = (int)K;
+    g.w_nib = w_nib; g.w_scale = w_scale; g.w_ts = w_ts; g.offsets = offsets;
+    g.E = (int)E; g.N = (int)N; g.out_bf16 = out_dtype == QUADS_OUT_BF16; g.out = out;
+    return epilogue == QUADS_EPI_SWIGLU ? w4a16::dispatch<QUADS_EPI_SWIGLU>(g, (hipStream_t)stream)
+                                        : w4a16::dispatch<QUADS_EPI_NONE>(g, (hipStream_t)stream);
 }
