@@ -73,8 +73,8 @@ int quads_moe_w4a16_gemv(const uint16_t* x, const int32_t* row_token, int64_t ro
  *   stats     out fp32 [T, 2]
  *   top_logp, top_id   out fp32, int32 [T, topk] (NULL when topk == 0): the
  *             topk largest entries of the row, descending, equal entries in
- *             ascending index order.  In a row with NaN, top_id holds
- *             distinct indices in [0, V) in no stated order.
+ *             ascending index order.  In a row with +inf or NaN, top_id
+ *             holds distinct indices in [0, V) in no stated order.
  */
 size_t quads_token_logprob_ws(int64_t T, int64_t V, int32_t topk);
 int quads_token_logprob(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,

@@ -559,29 +559,34 @@ def _want(name, t, dtype, shape, dev):
         return None
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, not on {t.device}")
-    return t.detach().contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _gpu(name, t):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU, not on {t.device}")
     return t.device
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _call(fn, dev, *args):
     """lib().fn(*args, stream) on `dev`, the stream being the device's current one."""
     if torch.cuda.current_device() == dev.index:
-        status = getattr(lib(), fn)(*args, _stream(dev))
+        status = getattr(lib(), fn)(*args, torch.cuda.current_stream(dev).cuda_stream)
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib(), fn)(*args, _stream(dev))
-    _check(fn, status)
+            status = getattr(lib(), fn)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != 0:
+        raise QuadsError(fn, status)
 
 
 def _logits(logits):
@@ -597,9 +602,9 @@ def _logits(logits):
     if logits.dim() != 2:
         raise ValueError("logits must be [T, V]")
     t, v = logits.shape
-    z = logits.detach()
+    z = logits
     if t and v and (z.stride(1) != 1 or (t > 1 and z.stride(0) < v) or z.data_ptr() % 16):
-        z = z.clone(memory_format=torch.contiguous_format)
+        z = z.detach().clone(memory_format=torch.contiguous_format)
     return z, code, t, v, (z.stride(0) if t > 1 else v)
 
 
@@ -622,7 +627,7 @@ def quads_moe_w4a16_gemv(x, w, n, rows=None, offsets=None, row_token=None, epilo
     w = (nib [E, N, K/2], scale [E, N, K/16], ts [E]).  Returns out [rows, N] (or [rows, N/2]
     for SwiGLU), fp32 or bf16 bits (int16)."""
     dev = _gpu("x", x)
-    x = _bits16(x.detach())
+    x = _bits16(x)
     if x.dim() != 2:
         raise ValueError("x must be [rows, K]")
     kd = x.shape[1]
@@ -647,9 +652,9 @@ def quads_moe_w4a16_gemv(x, w, n, rows=None, offsets=None, row_token=None, epilo
         raise ValueError("out must be a dense tensor of the call's type, shape and device")
     nws = lib().quads_moe_w4a16_gemv_ws(rows, kd, e, n)
     ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
-    _call("quads_moe_w4a16_gemv", dev, _ptr(x), _ptr(row_token), rows, kd, _ptr(w_nib),
-          _ptr(w_scale), _ptr(w_ts), _ptr(offsets), e, n, epilogue, out_dtype, _ptr(out),
-          _ptr(ws), nws)
+    _call("quads_moe_w4a16_gemv", dev, _at(x), _at(row_token), rows, kd, _at(w_nib),
+          _at(w_scale), _at(w_ts), _at(offsets), e, n, epilogue, out_dtype, _at(out),
+          _at(ws), nws)
     return out
 
 
@@ -671,9 +676,9 @@ def quads_token_logprob(logits, ids=None, inv_temp=1.0, topk=0, want_entropy=Tru
         out["top_id"] = torch.empty((t, topk), dtype=torch.int32, device=dev)
     nws = lib().quads_token_logprob_ws(t, v, topk)
     ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
-    _call("quads_token_logprob", dev, _ptr(z), code, t, v, ld, _ptr(ids), inv_temp, topk,
-          _ptr(out.get("logp")), _ptr(out.get("entropy")), _ptr(out["stats"]),
-          _ptr(out.get("top_logp")), _ptr(out.get("top_id")), _ptr(ws), nws)
+    _call("quads_token_logprob", dev, _at(z), code, t, v, ld, _at(ids), inv_temp, topk,
+          _at(out.get("logp")), _at(out.get("entropy")), _at(out["stats"]),
+          _at(out.get("top_logp")), _at(out.get("top_id")), _at(ws), nws)
     return out
 
 
@@ -689,8 +694,8 @@ def quads_token_logprob_backward(logits, ids, stats, entropy, g_logp, g_entropy=
     g_logp = _want("g_logp", g_logp, torch.float32, (t,), dev)
     g_entropy = _want("g_entropy", g_entropy, torch.float32, (t,), dev)
     out = _like_logits(z, t, v, ld, out)
-    _call("quads_token_logprob_backward", dev, _ptr(z), code, t, v, ld, _ptr(ids), inv_temp,
-          _ptr(stats), _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(out))
+    _call("quads_token_logprob_backward", dev, _at(z), code, t, v, ld, _at(ids), inv_temp,
+          _at(stats), _at(entropy), _at(g_logp), _at(g_entropy), _at(out))
     return out
 
 
@@ -713,8 +718,8 @@ def quads_topk_distill(logits, t_val, t_id, weight=None, inv_temp=1.0, renorm=Tr
     stats = torch.empty((t, 2), dtype=torch.float32, device=dev)
     nws = lib().quads_topk_distill_ws(t, v, k)
     ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
-    _call("quads_topk_distill", dev, _ptr(z), code, t, v, ld, _ptr(t_val), _ptr(t_id), k,
-          _ptr(weight), inv_temp, int(renorm), _ptr(loss), _ptr(stats), _ptr(ws), nws)
+    _call("quads_topk_distill", dev, _at(z), code, t, v, ld, _at(t_val), _at(t_id), k,
+          _at(weight), inv_temp, int(renorm), _at(loss), _at(stats), _at(ws), nws)
     return loss, stats
 
 
@@ -728,8 +733,8 @@ def quads_topk_distill_backward(logits, t_val, t_id, stats, g, weight=None, inv_
     stats = _want("stats", stats, torch.float32, (t, 2), dev)
     g = _want("g", g, torch.float32, (t,), dev)
     out = _like_logits(z, t, v, ld, out)
-    _call("quads_topk_distill_backward", dev, _ptr(z), code, t, v, ld, _ptr(t_val), _ptr(t_id),
-          k, _ptr(weight), inv_temp, int(renorm), _ptr(stats), _ptr(g), _ptr(out))
+    _call("quads_topk_distill_backward", dev, _at(z), code, t, v, ld, _at(t_val), _at(t_id),
+          k, _at(weight), inv_temp, int(renorm), _at(stats), _at(g), _at(out))
     return out
 
 
@@ -744,6 +749,6 @@ def quads_topk_distill_grad(logits, t_val, t_id, weight=None, inv_temp=1.0, reno
     out = _like_logits(z, t, v, ld, out)
     nws = lib().quads_topk_distill_ws(t, v, k)
     ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
-    _call("quads_topk_distill_grad", dev, _ptr(z), code, t, v, ld, _ptr(t_val), _ptr(t_id), k,
-          _ptr(weight), inv_temp, int(renorm), _ptr(loss), _ptr(out), _ptr(ws), nws)
+    _call("quads_topk_distill_grad", dev, _at(z), code, t, v, ld, _at(t_val), _at(t_id), k,
+          _at(weight), inv_temp, int(renorm), _at(loss), _at(out), _at(ws), nws)
     return loss, out

@@ -34,17 +34,23 @@ __device__ __forceinline__ int key_index(uint64_t k) { return (int)(0xFFFFFFFFu 
 
 constexpr int kCand = 1024;                    // candidates kept at once
 
-struct Cand {
+struct __align__(16) Cand {
     uint64_t key[kCand];
-    uint16_t top[kThreads];                    // upper halves of the threads' maxima's keys
+    uint16_t top[2][kThreads];                 // upper halves of the threads' maxima's keys
     int n;
 };
 
-// A value that at least k of the work-group's values (key halves in c.top)
+// The smallest fp32 above x (x no NaN; NaN above +inf, which no entry reaches).
+__device__ __forceinline__ float next_up(float x) {
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return __uint_as_float((int32_t)b >= 0 ? b + 1u : b - 1u);
+}
+
+// A value that at least k of the work-group's values (key halves in `top`)
 // reach: the k-th largest half, rounded down.  Every wave finds it by itself,
 // one bit of the half at a time, counting with ballots.
-__device__ __forceinline__ float kth_bound(const Cand& c, int k) {
-    const uint2 w = reinterpret_cast<const uint2*>(c.top)[threadIdx.x & 63];
+__device__ __forceinline__ float kth_bound(const uint16_t* top, int k) {
+    const uint2 w = reinterpret_cast<const uint2*>(top)[threadIdx.x & 63];
     const uint32_t h[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
     uint32_t t = 0;
 #pragma unroll
@@ -124,25 +130,54 @@ struct Parts {
     uint64_t* key;
 };
 
-// The outputs of row t from its statistics (thread 0 and the first topk).
+// The row's token, read early.
+struct Token {
+    int id;
+    float z;
+};
+template <int kBf16>
+__device__ __forceinline__ Token load_token(const Out& o, const Row<kBf16>& r, int64_t t) {
+    Token k = {-1, 0.0f};
+    if (o.ids && threadIdx.x == 0) {
+        k.id = o.ids[t];
+        if (k.id >= 0 && k.id < r.V) k.z = r.entry(k.id);
+    }
+    return k;
+}
+
+// The outputs of row t from its statistics and its n largest entries (thread
+// 0 and the first topk; key in LDS, sorted).  n < topk: no further entry is
+// above -inf, so that the masked ones of lowest index follow.
 template <int kBf16>
 __device__ __forceinline__ void finish(const Out& o, const Row<kBf16>& r, int64_t t, const Stat& a,
-                                       const uint64_t* key, int n) {
+                                       const Token& k, uint64_t* key, int n) {
     const float ls = log_sum(a);
     if (threadIdx.x == 0) {
         o.stats[2 * t] = a.m;
         o.stats[2 * t + 1] = ls;
         if (o.entropy)
             o.entropy[t] = a.m == -INFINITY && a.s == 0.0f ? 0.0f : ls - kLn2 * a.u / a.s;
-        if (o.ids) {
-            const int id = o.ids[t];
-            o.logp[t] = id >= 0 && id < r.V ? ln_p(r.entry(id), a.m, ls, o.it) : 0.0f;
-        }
+        if (o.ids) o.logp[t] = k.id >= 0 && k.id < r.V ? ln_p(k.z, a.m, ls, o.it) : 0.0f;
     }
-    // fewer candidates than alternatives: the row holds NaN; any indices
+    if (o.topk == 0) return;
+    const bool number = ls == ls;              // no NaN or +inf in the row
+    if (n < o.topk && number) {
+        if (threadIdx.x < 64) {
+            for (int b = 0; b < r.V && n < o.topk; b += 64) {
+                const int v = b + (int)threadIdx.x;
+                const bool masked = v < r.V && r.entry(v) == -INFINITY;
+                const uint64_t all = __ballot(masked);
+                const int at = n + __popcll(all & ((1ull << threadIdx.x) - 1ull));
+                if (masked && at < o.topk) key[at] = rank_key(-INFINITY, (uint32_t)v);
+                n += __popcll(all);
+            }
+        }
+        __syncthreads();
+        n = o.topk;
+    }
     if ((int)threadIdx.x < o.topk) {
         const int64_t at = t * o.topk + threadIdx.x;
-        const bool have = n == o.topk;
+        const bool have = n >= o.topk;         // else any indices
         o.top_id[at] = have ? key_index(key[threadIdx.x]) : (int)threadIdx.x;
         o.top_logp[at] = have ? ln_p(key_value(key[threadIdx.x]), a.m, ls, o.it) : NAN;
     }
@@ -152,20 +187,19 @@ __device__ __forceinline__ void finish(const Out& o, const Row<kBf16>& r, int64_
 // of kVecs vectors per thread, the next chunk's vectors requested before the
 // present one is worked on.
 //
-// kTop: a candidate is an entry above a value that topk earlier entries reach.
-// That bound is the topk-th largest of the threads' running maxima, taken
-// after the first chunk and again after 2, 4, 8, ... chunks (entries of the
-// first chunk count from the bound on, later ones only above it, as their
-// indices are higher), so that a random row yields about topk (1 + log2 of
-// the chunks) candidates and most chunks are compared with one number.  The
-// candidates are sorted once, at the end.  Where a chunk brings more than
-// there is room for (equal or rising entries), it is taken entry by entry of
-// each thread, the candidates cut to the topk largest in between.
+// kTop: a candidate is an entry above a value that topk earlier entries reach
+// (and above -inf).  That bound is the topk-th largest of the threads' running
+// maxima, taken after the first chunk and again after 2, 4, 8, ... chunks
+// (entries of the first chunk count from the bound on, later ones only above
+// it, as their indices are higher), so that a random row yields about topk (1
+// + log2 of the chunks) candidates and most vectors are compared with one
+// number.  The candidates are sorted once, at the end.  Where there were more
+// than there is room for (equal or rising entries) the part is read again,
+// 256 entries at a time, the candidates cut to the topk largest in between.
 template <int kBf16, bool kEntropy, bool kTop>
-__global__ __launch_bounds__(kThreads, 5) void k_logprob(const void* z, int64_t V, int64_t ld,
+__global__ __launch_bounds__(kThreads) void k_logprob(const void* z, int64_t V, int64_t ld,
                                                       int parts, Out o, Parts p) {
     constexpr int kPer = Row<kBf16>::kPer;
-    constexpr int kEnt = kPer * kVecs;
     __shared__ Stat s_stat[kThreads / 64];
     __shared__ Cand c;
     const int64_t t = blockIdx.x / (unsigned)parts;
@@ -178,12 +212,13 @@ __global__ __launch_bounds__(kThreads, 5) void k_logprob(const void* z, int64_t 
     const int topk = o.topk;
 
     auto load = [&](uint4 (&q)[kVecs], int ch) {
+        if (ch >= c1) return;
         const int j0 = ch * kChunk;
-        if (r.whole(j0) && r.whole(j0 + kChunk - 1) && ch < c1) {
+        if (r.whole(j0) && r.whole(j0 + kChunk - 1)) {
             const uint4* a = r.vec(j0 + threadIdx.x);
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) q[i] = a[i * kThreads];
-        } else if (ch < c1) {
+        } else {
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
                 const int j = j0 + i * kThreads + threadIdx.x;
@@ -193,19 +228,30 @@ __global__ __launch_bounds__(kThreads, 5) void k_logprob(const void* z, int64_t 
         }
     };
 
+    uint4 q[kVecs], next[kVecs];
+    load(next, c0);
+    const Token token = parts == 1 ? load_token<kBf16>(o, r, t) : Token{-1, 0.0f};
     Stat a = {-INFINITY, 0.0f, 0.0f};
-    float bound = -INFINITY;
-    if (kTop && threadIdx.x == 0) c.n = 0;
-    int n = 0;
-    auto work = [&](const uint4 (&q)[kVecs], int ch) {
-        float m = -INFINITY;
+    float bound = -INFINITY;                   // candidates reach it
+    int fresh = 0;
+    if (kTop) {
+        if (threadIdx.x == 0) c.n = 0;
+        __syncthreads();
+    }
+    for (int ch = c0; ch < c1; ++ch) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
+        for (int i = 0; i < kVecs; ++i) q[i] = next[i];
+        load(next, ch + 1);
+        float vm[kVecs], m = a.m;
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) m = fmaxf(m, get<kBf16>(q[i], e));
-        const float mine = m;
-        stat_raise(a, fmaxf(a.m, m), cl);
-        const float base = stat_base(a.m);
+        for (int i = 0; i < kVecs; ++i) {
+            vm[i] = get<kBf16>(q[i], 0);
+#pragma unroll
+            for (int e = 1; e < kPer; ++e) vm[i] = fmaxf(vm[i], get<kBf16>(q[i], e));
+            m = fmaxf(m, vm[i]);
+        }
+        stat_raise(a, m, cl);
+        const float base = stat_base(m);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i)
 #pragma unroll
@@ -215,101 +261,87 @@ __global__ __launch_bounds__(kThreads, 5) void k_logprob(const void* z, int64_t 
                 a.s += x;
                 if (kEntropy) a.u = __builtin_fmaf(x, fmaxf(d, kNoTerm), a.u);
             }
-        if (!kTop) return;
-        const int nth = ch - c0;
-        if (nth == 0) {
-            c.top[threadIdx.x] = (uint16_t)(value_key(a.m) >> 16);
-            __syncthreads();
-            bound = kth_bound(c, topk);
-        }
-        const bool first = nth == 0;
-        const int base_v = r.index(ch * kChunk + threadIdx.x, 0);
-        if (first ? mine >= bound : mine > bound) {
-            uint32_t pass = 0;
-#pragma unroll
-            for (int i = 0; i < kEnt; ++i) {
-                const float x = get<kBf16>(q[i / kPer], i % kPer);
-                const int v = base_v + (i / kPer) * kThreads * kPer + i % kPer;
-                const bool ok = (first ? x >= bound : x > bound) && v >= 0 && v < r.V;
-                pass |= ok ? 1u << i : 0u;
-            }
-            int at = pass ? atomicAdd(&c.n, __popc(pass)) : 0;
-#pragma unroll
-            for (int i = 0; i < kEnt; ++i)
-                if (pass & (1u << i)) {
-                    const int v = base_v + (i / kPer) * kThreads * kPer + i % kPer;
-                    if (at < kCand) c.key[at] = rank_key(get<kBf16>(q[i / kPer], i % kPer), v);
-                    ++at;
-                }
-        }
-        __syncthreads();
-        const int total = c.n;
-        __syncthreads();
-        if (total <= kCand) {
-            n = total;
-        } else {
-            if (threadIdx.x == 0) c.n = n;
-            __syncthreads();
-            uint64_t over = 0;                 // the topk-th candidate, once cut
-#pragma unroll 1
-            for (int i = 0; i < kEnt; ++i) {
-                if (n + kThreads > kCand) {
-                    keep_top(c, n, topk);
-                    over = c.n == topk ? c.key[topk - 1] : 0;
-                }
-                // entry i of the thread, by a select: q stays in registers
-                uint4 w = q[0];
-#pragma unroll
-                for (int b = 1; b < kVecs; ++b)
-                    if (i / kPer == b) w = q[b];
-                float x = get<kBf16>(w, 0);
-#pragma unroll
-                for (int b = 1; b < kPer; ++b)
-                    if (i % kPer == b) x = get<kBf16>(w, b);
-                const int v = base_v + (i / kPer) * kThreads * kPer + i % kPer;
-                const uint64_t key = rank_key(x, (uint32_t)v);
-                if ((first ? x >= bound : x > bound) && v >= 0 && v < r.V && key > over)
-                    c.key[atomicAdd(&c.n, 1)] = key;
+        if (kTop) {
+            const int nth = ch - c0;
+            if (nth == 0) {
+                c.top[0][threadIdx.x] = (uint16_t)(value_key(m) >> 16);
                 __syncthreads();
-                n = c.n;
-                __syncthreads();
+                bound = kth_bound(c.top[0], topk);
             }
-            keep_top(c, n, topk);
-            n = c.n;
-            if (n == topk) bound = fmaxf(bound, key_value(c.key[topk - 1]));
-            __syncthreads();
-        }
-        if ((nth & (nth + 1)) == 0 && nth > 0) {
-            c.top[threadIdx.x] = (uint16_t)(value_key(a.m) >> 16);
-            __syncthreads();
-            bound = fmaxf(bound, kth_bound(c, topk));
-            __syncthreads();
-        }
-    };
-
-    uint4 q[kVecs], next[kVecs];
-    load(next, c0);
-    for (int ch = c0; ch < c1; ++ch) {
+            const float reach = fmaxf(bound, next_up(-INFINITY));
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) q[i] = next[i];
-        load(next, ch + 1);
-        work(q, ch);
+            for (int i = 0; i < kVecs; ++i)
+                if (vm[i] >= reach) {
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) {
+                        const float x = get<kBf16>(q[i], e);
+                        if (x >= reach) {
+                            const int at = atomicAdd(&c.n, 1);
+                            const int v = r.index(ch * kChunk + i * kThreads + threadIdx.x, e);
+                            if (at < kCand) c.key[at] = rank_key(x, (uint32_t)v);
+                        }
+                    }
+                }
+            if (nth == 0) {
+                bound = next_up(bound);
+            } else if ((nth & (nth + 1)) == 0 && ch + 1 < c1) {
+                // (two sets of maxima in turn: a wave writes the second next
+                // one only after all have read this one)
+                fresh ^= 1;
+                c.top[fresh][threadIdx.x] = (uint16_t)(value_key(m) >> 16);
+                __syncthreads();
+                bound = fmaxf(bound, next_up(kth_bound(c.top[fresh], topk)));
+            }
+        }
     }
 
     const float top = a.m;
     a = group_stat<kThreads / 64>(a, cl, s_stat);
+    int n = 0;
     if (kTop) {
-        if (n > topk + topk / 2 + 16) {
-            c.top[threadIdx.x] = (uint16_t)(value_key(top) >> 16);
+        n = c.n;                               // (group_stat has a barrier)
+        if (n > kCand) {
             __syncthreads();
-            bound = fmaxf(bound, kth_bound(c, topk));
-            n = drop_below(c, n, bound);
+            n = 0;
+            if (threadIdx.x == 0) c.n = 0;
+            __syncthreads();
+            uint64_t over = 0;                 // the topk-th candidate, once cut
+            const int v0 = max(r.index(c0 * kChunk, 0), 0);
+            const int v1 = min((int64_t)r.V, (int64_t)c1 * kChunk * kPer - r.shift);
+            for (int v = v0; v < v1; v += kThreads * 8) {
+                uint64_t k[8];
+                bool any = false;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int at = v + i * kThreads + (int)threadIdx.x;
+                    const float x = at < v1 ? r.entry(at) : -INFINITY;
+                    k[i] = x > -INFINITY ? rank_key(x, (uint32_t)at) : 0;
+                    any = any || k[i] > over;
+                }
+                if (!__syncthreads_or(any)) continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (n + kThreads > kCand) {
+                        keep_top(c, n, topk);
+                        over = c.n == topk ? c.key[topk - 1] : 0;
+                        __syncthreads();
+                    }
+                    if (k[i] > over) c.key[atomicAdd(&c.n, 1)] = k[i];
+                    __syncthreads();
+                    n = c.n;
+                    __syncthreads();
+                }
+            }
+        } else if (n > topk + topk / 2 + 16) {
+            c.top[fresh ^ 1][threadIdx.x] = (uint16_t)(value_key(top) >> 16);
+            __syncthreads();
+            n = drop_below(c, n, kth_bound(c.top[fresh ^ 1], topk));
         }
         keep_top(c, n, topk);
         n = c.n;
     }
     if (parts == 1) {
-        finish<kBf16>(o, r, t, a, c.key, n);
+        finish<kBf16>(o, r, t, a, token, c.key, n);
     } else {
         if (threadIdx.x == 0) p.stat[blockIdx.x] = make_float4(a.m, a.s, a.u, 0.0f);
         if (kTop && (int)threadIdx.x < topk)
@@ -319,9 +351,9 @@ __global__ __launch_bounds__(kThreads, 5) void k_logprob(const void* z, int64_t 
 }
 
 // Joins the parts of a row.  The statistics: lane l of every wave holds part
-// l (kMaxParts = 64).  The alternatives: those of all parts at or above the
-// topk-th largest part maximum (upper half of the key) if there are topk
-// parts, then sorted; parts are short of topk entries only at a row's end.
+// l (kMaxParts = 64).  The alternatives: the parts' candidates at or above
+// the topk-th largest of the threads' maxima, sorted; all of them, cut in
+// between, if those are more than there is room for.
 template <int kBf16>
 __global__ __launch_bounds__(kThreads) void k_merge(const void* z, int64_t V, int64_t ld,
                                                     int parts, Out o, Parts p) {
@@ -329,36 +361,56 @@ __global__ __launch_bounds__(kThreads) void k_merge(const void* z, int64_t V, in
     const int64_t t = blockIdx.x;
     const Row<kBf16> r(z, t, ld, V);
     const int lane = threadIdx.x & 63;
+    const Token token = load_token<kBf16>(o, r, t);
     Stat a = {-INFINITY, 0.0f, 0.0f};
     if (lane < parts) {
         const float4 q = p.stat[t * parts + lane];
         a = {q.x, q.y, q.z};
     }
-    a = wave_stat(a, o.it * kLog2e);
     int n = 0;
     if (o.topk > 0) {
         const uint64_t* key = p.key + t * parts * o.topk;
+        const int all = parts * o.topk;
+        uint64_t most = 0;
+        for (int i = threadIdx.x; i < all; i += kThreads) most = key[i] > most ? key[i] : most;
+        c.top[0][threadIdx.x] = (uint16_t)(most >> 48);
         if (threadIdx.x == 0) c.n = 0;
         __syncthreads();
-        // parts in order, topk at a time; the candidates are cut when full
-        const int all = parts * o.topk;
-        uint64_t over = 0;
-        for (int b = 0; b < all; b += kThreads) {
-            if (n + kThreads > kCand) {
-                keep_top(c, n, o.topk);
-                over = c.n == o.topk ? c.key[o.topk - 1] : 0;
+        const uint64_t low = (uint64_t)value_key(kth_bound(c.top[0], o.topk)) << 32;
+        for (int i = threadIdx.x; i < all; i += kThreads) {
+            const uint64_t k = key[i];
+            if (k > low) {                     // (a key's index half is not 0)
+                const int at = atomicAdd(&c.n, 1);
+                if (at < kCand) c.key[at] = k;
             }
-            const int i = b + threadIdx.x;
-            const uint64_t k = i < all ? key[i] : 0;
-            if (k > over) c.key[atomicAdd(&c.n, 1)] = k;
+        }
+        __syncthreads();
+        n = c.n;
+        if (n > kCand) {
             __syncthreads();
-            n = c.n;
+            n = 0;
+            if (threadIdx.x == 0) c.n = 0;
             __syncthreads();
+            uint64_t over = 0;
+            for (int b = 0; b < all; b += kThreads) {
+                if (n + kThreads > kCand) {
+                    keep_top(c, n, o.topk);
+                    over = c.n == o.topk ? c.key[o.topk - 1] : 0;
+                    __syncthreads();
+                }
+                const int i = b + threadIdx.x;
+                const uint64_t k = i < all ? key[i] : 0;
+                if (k > over) c.key[atomicAdd(&c.n, 1)] = k;
+                __syncthreads();
+                n = c.n;
+                __syncthreads();
+            }
         }
         keep_top(c, n, o.topk);
         n = c.n;
     }
-    finish<kBf16>(o, r, t, a, c.key, n);
+    a = wave_stat(a, o.it * kLog2e);
+    finish<kBf16>(o, r, t, a, token, c.key, n);
 }
 
 // ---------------------------------------------------------------- backward --
