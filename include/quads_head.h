@@ -48,7 +48,7 @@ extern "C" {
  * W4A16 grouped product for few rows per expert (Eq. (12) in the forward
  * direction, on the NVFP4 codes themselves): for packed row p of expert e,
  *   Y[p, n] = s_tW[e] sum_{j<K} x[row(p), j] w_e[n, j],   w the exact v*s_b.
- *   x          bf16 [Tx, K], finite, K % 16 == 0
+ *   x          bf16 [Tx, K], finite, K % 16 == 0, K < 2^26
  *   row_token  NULL: row(p) = p (Tx = rows); else int32 [rows], row(p) =
  *              row_token[p] < Tx
  *   w_nib, w_scale, w_ts, offsets, E, N, epilogue, out_dtype, out   as in

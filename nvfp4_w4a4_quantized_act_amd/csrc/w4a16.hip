@@ -25,17 +25,27 @@
 // channel 32 h on (one 16-byte load, 64 contiguous bytes per feature and
 // load), and step j of a chunk multiplies the lane's codes 8 j .. 8 j + 7, so
 // the channels of the four h interleave; the activations are read from LDS in
-// the same order.  The registers of a chunk are filled again, with that chunk
-// of the wave's next block, as soon as it has been multiplied.
+// the same order.  When a block has been multiplied the next one's loads go
+// out together, 256 contiguous bytes of every feature: spread out, chunk by
+// chunk as each was consumed, they asked for the two halves of a 128-byte line
+// at different times and cost 6% (1 x 2048 x 262144: 63.8 against 59.5 us; a
+// read of the same bytes in order takes 59.8).  The other waves of the SIMD
+// multiply meanwhile.
 //   The block scales of 512 channels of a feature are 32 bytes: lane (r, h)
 // loads the 8 of chunk h, and the four lanes of a feature exchange them in
 // registers (row swaps), so that each has its two of every chunk.
-//   The activations, few and read by every wave, are in LDS for as many blocks
-// as fit.
+//   The activations, few and read by every wave, are in LDS: all of a unit's
+// channels, brought once, where they fit, else as many blocks as do, again for
+// every step.
 //
-// Where there are too few features to fill the GPU, kw waves of the
-// work-group share a pair of tiles, each taking every kw-th block, and their
-// totals are added in LDS in wave order.
+// Work-groups are resident ones, as many as the GPU holds: a unit (up to 16 kRt
+// rows of an expert) has `slabs` of them, and each takes an equal range of its
+// features, in steps of two tiles per slot of kw waves; the kw waves of a slot
+// share its tiles, each taking every kw-th block, and their totals are added
+// in LDS in wave order.  The ranges are even to 4 features: lanes past a
+// slot's last feature load nothing, so no work-group streams more than its
+// share (whole tiles per wave, one or two of them, left a third of the waves
+// idle at the end: 13 x 2048 x 100003 took 36 us, 1 x 4096 x 150000 84 us).
 #include "common.h"
 #include "gemm_tiles.h"
 #include "../../include/quads_head.h"
@@ -52,15 +62,18 @@ constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kChunk = 128;                    // channels per 16-byte load
 constexpr int kBlk = 512;                      // channels per block
-constexpr int kLdsX = 72 << 10;                // bytes for the activations: two work-groups a CU
+constexpr int kStage = 4;                      // activation loads in flight per wave
+constexpr int kLds = 160 << 10;                // LDS bytes of a CU
+constexpr int kCus = 256;
 
 struct Args {
     const uint16_t* x; const int32_t* row_token; int rows; int K;
     const uint8_t* w_nib; const uint8_t* w_scale; const float* w_ts; const int32_t* offsets;
     int E; int N;
     int out_bf16; void* out;
-    int kw;                                    // waves per pair of tiles
+    int kw;                                    // waves per slot
     int slabs;                                 // work-groups per unit of rows
+    int steps;                                 // of the largest slot
     int sb;                                    // blocks of activations in LDS at once
     int rcap;                                  // rows of LDS
 };
@@ -81,24 +94,29 @@ __device__ __forceinline__ f16x8 cvt8(uint32_t w, _Float16 s) {
 }
 
 // A feature's codes of chunk `cc` for the lane: 32 from channel 128 cc + 32 h
-// on.  `at` points at the lane's share of chunk 0.  Codes past K read as 0.
-__device__ __forceinline__ uint4 load_codes(const uint8_t* at, int cc, int h, int K) {
+// on, at the uniform base `at` (the tile's first feature) plus the lane's
+// `off`.  Codes past K read as 0; a lane that is not `ok` loads nothing.
+__device__ __forceinline__ uint4 load_codes(const uint8_t* at, uint32_t off, int cc, int h, int K,
+                                            bool ok) {
     const uint8_t* p = at + (int64_t)cc * (kChunk / 2);
     if ((cc + 1) * kChunk <= K) {
-        const u32x4 v = reinterpret_cast<const Bytes16*>(p)->v;
+        u32x4 v = {0, 0, 0, 0};
+        if (ok) v = reinterpret_cast<const Bytes16*>(p + off)->v;
         return make_uint4(v.x, v.y, v.z, v.w);
     }
     const int k = cc * kChunk + 32 * h;
     u32x2 lo = {0, 0}, hi = {0, 0};
-    if (k < K) lo = reinterpret_cast<const Bytes8*>(p)->v;
-    if (k + 16 < K) hi = reinterpret_cast<const Bytes8*>(p + 8)->v;
+    if (ok && k < K) lo = reinterpret_cast<const Bytes8*>(p + off)->v;
+    if (ok && k + 16 < K) hi = reinterpret_cast<const Bytes8*>(p + off + 8)->v;
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 // A feature's scales of chunk 4 b + h (8 bytes); 0 past K.
-__device__ __forceinline__ u32x2 load_scales(const uint8_t* at, int b, int h, int K) {
+__device__ __forceinline__ u32x2 load_scales(const uint8_t* at, uint32_t off, int b, int h, int K,
+                                             bool ok) {
     const int cc = 4 * b + h;
-    const uint8_t* p = at + (int64_t)cc * (kChunk / kBlock);
+    const uint8_t* p = at + (int64_t)b * (kBlk / kBlock) + (off + 8u * h);
     u32x2 v = {0, 0};
+    if (!ok) return v;
     if ((cc + 1) * kChunk <= K) {
         v = reinterpret_cast<const Bytes8*>(p)->v;
     } else {
@@ -124,8 +142,9 @@ __device__ __forceinline__ void own_scales(u32x2 v, int h, uint32_t s[4]) {
     s[3] = f[1] >> sh;
 }
 
-// Dynamic LDS: [rcap][sb * 1024 + 16] bytes of fp16 activations, then [rcap][sb]
-// fp32 scales of their blocks; the totals of split waves reuse it.
+// Dynamic LDS: [rcap][sb * 1024 + 16] bytes of fp16 activations, [rcap][sb]
+// fp32 scales of their blocks, then the totals of each slot's waves but the
+// first.
 template <int kEpi, int kRt>
 __global__ __launch_bounds__(kThreads, kRt > 2 ? 2 : 4) void k_w4a16(Args g) {
     constexpr bool swiglu = kEpi == QUADS_EPI_SWIGLU;
@@ -163,231 +182,290 @@ __global__ __launch_bounds__(kThreads, kRt > 2 ? 2 : 4) void k_w4a16(Args g) {
     }
     if (cnt <= 0) return;
     const int nr = cnt < kRows ? cnt : kRows;
+    // lane l: the activation row of the unit's row l
+    int token = 0;
+    if (lane < nr) token = g.row_token ? g.row_token[p0 + lane] : p0 + lane;
 
-    // the wave's tiles and its blocks wk, wk + kw, ...
+    // the slot's output features [lo, hi), taken kStep at a time
+    constexpr int kStep = swiglu ? 16 : 32;
     const int nout = swiglu ? g.N / 2 : g.N;
     const int wk = wave % g.kw;
-    const int pair = slab * (kWaves / g.kw) + wave / g.kw;
+    const int slots = kWaves / g.kw;
+    const int64_t slot = (int64_t)slab * slots + wave / g.kw, all = (int64_t)g.slabs * slots;
+    const int64_t quads_n = (nout + 3) / 4;
+    const int lo = __builtin_amdgcn_readfirstlane((int)(4 * (quads_n * slot / all)));
+    const int hi =
+        __builtin_amdgcn_readfirstlane(min(nout, (int)(4 * (quads_n * (slot + 1) / all))));
     const int nblk = (g.K + kBlk - 1) / kBlk;
-    int feat[2];
+    // each tile's first feature (of the weight rows), kStep rows further per
+    // step, and how many features up to hi there are from it on; the lane's
+    // offset from it
     const uint8_t* nib[2];
     const uint8_t* sc[2];
+    int left[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        feat[q] = swiglu ? 16 * pair : 32 * pair + 16 * q;         // of the output
-        int f = feat[q] + r < nout ? feat[q] + r : nout - 1;
-        if (swiglu) f += q * nout;
-        const int64_t row = (int64_t)e * g.N + f;
-        nib[q] = g.w_nib + row * (g.K / 2) + 16 * h;
+        const int f = lo + (swiglu ? 0 : 16 * q);
+        const int64_t row = (int64_t)e * g.N + f + (swiglu ? q * nout : 0);
+        nib[q] = g.w_nib + row * (g.K / 2);
         sc[q] = g.w_scale + row * (g.K / kBlock);
+        left[q] = hi - f;
     }
-    const bool mine = feat[0] < nout;
+    const uint32_t nib_off = (uint32_t)r * (g.K / 2) + 16 * h, sc_off = (uint32_t)r * (g.K / kBlock);
+    const int64_t nib_step = (int64_t)kStep * (g.K / 2), sc_step = (int64_t)kStep * (g.K / kBlock);
 
     uint4 code[2][4];
     u32x2 scale[2];
-    if (mine && wk < nblk) {
+    auto load = [&](int b) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            scale[q] = load_scales(sc[q], wk, h, g.K);
+            const bool ok = r < left[q] && b < nblk;
+            scale[q] = load_scales(sc[q], sc_off, b, h, g.K, ok);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) code[q][c] = load_codes(nib[q], 4 * wk + c, h, g.K);
+            for (int c = 0; c < 4; ++c)
+                code[q][c] = load_codes(nib[q], nib_off, 4 * b + c, h, g.K, ok);
         }
-    }
+    };
+    load(wk);
 
-    f32x4 tot[2][kRt];
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int t = 0; t < kRt; ++t) tot[q][t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     const int stride = g.sb * 2 * kBlk + 16;
     float* xscale = (float*)(lds + (size_t)g.rcap * stride);
+    f32x4* part = reinterpret_cast<f32x4*>(
+        lds + (((size_t)g.rcap * (stride + 4 * g.sb) + 15) & ~(size_t)15));
     int xrow[kRt];
 #pragma unroll
     for (int t = 0; t < kRt; ++t) xrow[t] = 16 * t + r < nr ? 16 * t + r : 0;
+    const float ts = g.w_ts[e];
 
-    for (int s0 = 0; s0 < nblk; s0 += g.sb) {
-        const int sb = nblk - s0 < g.sb ? nblk - s0 : g.sb;
-        if (s0) __syncthreads();
-        // activations of blocks s0 .. s0 + sb - 1: a wave per (row, block)
-        for (int i = wave; i < nr * sb; i += kWaves) {
-            const int row = i / sb, b = i % sb;
-            const int64_t src = g.row_token ? g.row_token[p0 + row] : p0 + row;
-            const int k = (s0 + b) * kBlk + 8 * lane;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (k < g.K) v = *reinterpret_cast<const uint4*>(g.x + src * g.K + k);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t m = 0;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) m = pk_max_u16(m, w[u] & 0x7FFF7FFFu);
-            m = wave_max_u32(umax32(m >> 16, m & 0xFFFFu));
-            // 2^(141 - ex) with ex the exponent of the largest magnitude; blocks
-            // below 2^-112 take the largest power that has a normal inverse
-            uint32_t ex = m >> 7;
-            ex = ex < 15u ? 15u : ex;
-            const float up = __uint_as_float((268u - ex) << 23);
-            f16x8 y;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                y[2 * u] = (_Float16)(__uint_as_float(w[u] << 16) * up);
-                y[2 * u + 1] = (_Float16)(__uint_as_float(w[u] & 0xFFFF0000u) * up);
-            }
-            *reinterpret_cast<f16x8*>(lds + row * stride + 2 * (b * kBlk + 8 * lane)) = y;
-            if (lane == 0) xscale[row * g.sb + b] = __uint_as_float((ex - 14u) << 23);
-        }
-        __syncthreads();
-        if (!mine) continue;
-        // the wave's blocks among them
-        const int first = s0 + (wk - s0 % g.kw + g.kw) % g.kw;
-        for (int b = first; b < s0 + sb; b += g.kw) {
-            const int next = b + g.kw;
-            f32x4 acc[2][kRt];
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int t = 0; t < kRt; ++t) acc[q][t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-            uint32_t own[2][4];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                own_scales(scale[q], h, own[q]);
-                if (next < nblk) scale[q] = load_scales(sc[q], next, h, g.K);
-            }
-            const char* xb = lds + 2 * ((b - s0) * kBlk + 32 * h);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                f16x2 s[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    s[q] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(own[q][c], 1.0f, false);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f16x8 xf[kRt];
-#pragma unroll
-                    for (int t = 0; t < kRt; ++t)
-                        xf[t] = *reinterpret_cast<const f16x8*>(xb + xrow[t] * stride +
-                                                                2 * (kChunk * c + 8 * j));
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint4& w = code[q][c];
-                        const uint32_t x = j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w;
-                        const f16x8 wf = cvt8(x, s[q][j >> 1]);
-#pragma unroll
-                        for (int t = 0; t < kRt; ++t)
-                            acc[q][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf, xf[t],
-                                                                               acc[q][t], 0, 0, 0);
-                    }
-                }
-                if (next < nblk) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        code[q][c] = load_codes(nib[q], 4 * next + c, h, g.K);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-#pragma unroll
-            for (int t = 0; t < kRt; ++t) {
-                const float f = xscale[xrow[t] * g.sb + b - s0];
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        tot[q][t][u] = __builtin_fmaf(acc[q][t][u], f, tot[q][t][u]);
-            }
-        }
-    }
-
-    // totals of the waves that share a pair: into LDS, added in wave order
-    if (g.kw > 1) {
-        __syncthreads();
-        f32x4* part = reinterpret_cast<f32x4*>(lds);
+    for (int st = 0; st < g.steps; ++st) {
+        f32x4 tot[2][kRt];
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int t = 0; t < kRt; ++t)
-                part[((wave * 2 + q) * kRt + t) * 64 + lane] = tot[q][t];
-        __syncthreads();
-        if (wk != 0) return;
-        for (int w = 1; w < g.kw; ++w)
+            for (int t = 0; t < kRt; ++t) tot[q][t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s0 = 0; s0 < nblk; s0 += g.sb) {
+            const int sb = nblk - s0 < g.sb ? nblk - s0 : g.sb;
+            if (st == 0 || g.sb < nblk) {
+                if (st > 0 || s0 > 0) __syncthreads();
+                // activations of blocks s0 .. s0 + sb - 1: a wave per (row,
+                // block), kStage of them requested together
+                for (int i0 = wave; i0 < nr * sb; i0 += kStage * kWaves) {
+                    uint4 v[kStage];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+                    for (int a = 0; a < kStage; ++a) {
+                        const int i = i0 + a * kWaves;
+                        v[a] = make_uint4(0, 0, 0, 0);
+                        if (i < nr * sb) {
+                            const int k = (s0 + i % sb) * kBlk + 8 * lane;
+                            const int64_t src = __builtin_amdgcn_readlane(token, i / sb);
+                            if (k < g.K)
+                                v[a] = *reinterpret_cast<const uint4*>(g.x + src * g.K + k);
+                        }
+                    }
 #pragma unroll
-                for (int t = 0; t < kRt; ++t)
-                    tot[q][t] += part[(((wave + w) * 2 + q) * kRt + t) * 64 + lane];
-    }
-    if (!mine) return;
-
-    // lane (r, h) holds row 16 t + r of features 4 h .. 4 h + 3 of each tile
-    const float ts = g.w_ts[e];
+                    for (int a = 0; a < kStage; ++a) {
+                        const int i = i0 + a * kWaves;
+                        if (i >= nr * sb) break;
+                        const int row = i / sb, b = i % sb;
+                        const uint32_t w[4] = {v[a].x, v[a].y, v[a].z, v[a].w};
+                        uint32_t m = 0;
 #pragma unroll
-    for (int t = 0; t < kRt; ++t) {
-        const bool have = 16 * t + r < nr;
-        const int64_t o = (int64_t)(p0 + 16 * t + r) * nout;
+                        for (int u = 0; u < 4; ++u) m = pk_max_u16(m, w[u] & 0x7FFF7FFFu);
+                        m = wave_max_u32(umax32(m >> 16, m & 0xFFFFu));
+                        // 2^(141 - ex) with ex the exponent of the largest
+                        // magnitude; blocks below 2^-112 take the largest
+                        // power with a normal inverse
+                        uint32_t ex = m >> 7;
+                        ex = ex < 15u ? 15u : ex;
+                        const float up = __uint_as_float((268u - ex) << 23);
+                        f16x8 y;
 #pragma unroll
-        for (int q = 0; q < (swiglu ? 1 : 2); ++q) {
-            const int n = feat[q] + 4 * h;
-            float y[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                y[u] = tot[q][t][u] * ts;
-                if (swiglu) y[u] = silu_mul(y[u], tot[1][t][u] * ts);
-            }
-            if (!have || n >= nout) continue;
-            if (g.out_bf16) {
-                uint16_t* a = (uint16_t*)g.out + o + n;
-                const uint32_t p01 = v2::pk_bf16(y[0], y[1]), p23 = v2::pk_bf16(y[2], y[3]);
-                if (n + 3 < nout && nout % 4 == 0) {
-                    *reinterpret_cast<uint2*>(a) = make_uint2(p01, p23);
-                } else {
-                    const uint32_t b4[4] = {p01, p01 >> 16, p23, p23 >> 16};
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (n + u < nout) a[u] = (uint16_t)b4[u];
+                        for (int u = 0; u < 4; ++u) {
+                            y[2 * u] = (_Float16)(__uint_as_float(w[u] << 16) * up);
+                            y[2 * u + 1] = (_Float16)(__uint_as_float(w[u] & 0xFFFF0000u) * up);
+                        }
+                        *reinterpret_cast<f16x8*>(lds + row * stride + 2 * (b * kBlk + 8 * lane)) =
+                            y;
+                        if (lane == 0) xscale[row * g.sb + b] = __uint_as_float((ex - 14u) << 23);
+                    }
                 }
-            } else {
-                float* a = (float*)g.out + o + n;
-                if (n + 3 < nout && nout % 4 == 0) {
-                    *reinterpret_cast<float4*>(a) = make_float4(y[0], y[1], y[2], y[3]);
-                } else {
+                __syncthreads();
+            }
+            // the wave's blocks among them (sb is a multiple of kw, or all)
+            for (int b = s0 + wk; b < s0 + sb; b += g.kw) {
+                f32x4 acc[2][kRt];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (n + u < nout) a[u] = y[u];
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int t = 0; t < kRt; ++t) acc[q][t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+                uint32_t own[2][4];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) own_scales(scale[q], h, own[q]);
+                const char* xb = lds + 2 * ((b - s0) * kBlk + 32 * h);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    f16x2 s[2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        s[q] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(own[q][c], 1.0f, false);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        f16x8 xf[kRt];
+#pragma unroll
+                        for (int t = 0; t < kRt; ++t)
+                            xf[t] = *reinterpret_cast<const f16x8*>(xb + xrow[t] * stride +
+                                                                    2 * (kChunk * c + 8 * j));
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const uint4& w = code[q][c];
+                            const uint32_t x = j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w;
+                            const f16x8 wf = cvt8(x, s[q][j >> 1]);
+#pragma unroll
+                            for (int t = 0; t < kRt; ++t)
+                                acc[q][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                                    wf, xf[t], acc[q][t], 0, 0, 0);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                // what follows this block: the wave's next one, or its first
+                // of the next step
+                const bool turn = b + g.kw >= nblk;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (turn) {
+                        nib[q] += nib_step;
+                        sc[q] += sc_step;
+                        left[q] -= kStep;
+                    }
+                load(turn ? wk : b + g.kw);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int t = 0; t < kRt; ++t) {
+                    const float f = xscale[xrow[t] * g.sb + b - s0];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            tot[q][t][u] = __builtin_fmaf(acc[q][t][u], f, tot[q][t][u]);
+                }
+            }
+        }
+
+        // totals of the slot's waves: into LDS, added in wave order
+        if (g.kw > 1) {
+            if (st > 0) __syncthreads();
+            if (wk > 0) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int t = 0; t < kRt; ++t)
+                        part[(((wave - 1) * 2 + q) * kRt + t) * 64 + lane] = tot[q][t];
+            }
+            __syncthreads();
+            if (wk > 0) continue;
+            for (int w = 1; w < g.kw; ++w)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int t = 0; t < kRt; ++t)
+                        tot[q][t] += part[(((wave + w - 1) * 2 + q) * kRt + t) * 64 + lane];
+        }
+
+        // lane (r, h) holds row 16 t + r of features 4 h .. 4 h + 3 of each tile
+#pragma unroll
+        for (int t = 0; t < kRt; ++t) {
+            const bool have = 16 * t + r < nr;
+            const int64_t o = (int64_t)(p0 + 16 * t + r) * nout;
+#pragma unroll
+            for (int q = 0; q < (swiglu ? 1 : 2); ++q) {
+                const int n = lo + st * kStep + 16 * q + 4 * h;
+                float y[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    y[u] = tot[q][t][u] * ts;
+                    if (swiglu) y[u] = silu_mul(y[u], tot[1][t][u] * ts);
+                }
+                if (!have || n >= hi) continue;
+                if (g.out_bf16) {
+                    uint16_t* a = (uint16_t*)g.out + o + n;
+                    const uint32_t p01 = v2::pk_bf16(y[0], y[1]), p23 = v2::pk_bf16(y[2], y[3]);
+                    if (nout % 4 == 0) {
+                        *reinterpret_cast<uint2*>(a) = make_uint2(p01, p23);
+                    } else {
+                        const uint32_t b4[4] = {p01, p01 >> 16, p23, p23 >> 16};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (n + u < hi) a[u] = (uint16_t)b4[u];
+                    }
+                } else {
+                    float* a = (float*)g.out + o + n;
+                    if (nout % 4 == 0) {
+                        *reinterpret_cast<float4*>(a) = make_float4(y[0], y[1], y[2], y[3]);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (n + u < hi) a[u] = y[u];
+                    }
                 }
             }
         }
     }
 }
 
-// Rows per unit: 16 while an expert has few rows on average, else up to 64, so
-// that its weights are read once.
 template <int kEpi, int kRt>
 int launch(Args g, hipStream_t st) {
     constexpr int kRows = 16 * kRt;
+    constexpr int kStep = kEpi == QUADS_EPI_SWIGLU ? 16 : 32;
     const int nout = kEpi == QUADS_EPI_SWIGLU ? g.N / 2 : g.N;
-    const int tile = kEpi == QUADS_EPI_SWIGLU ? 16 : 32;
-    const int64_t pairs = ((int64_t)nout + tile - 1) / tile;
     const int64_t units = g.offsets ? (int64_t)(g.E < g.rows ? g.E : g.rows) + g.rows / kRows
                                     : ((int64_t)g.rows + kRows - 1) / kRows;
     const int64_t live = g.offsets ? (g.E < g.rows ? g.E : g.rows) : units;
     const int nblk = (g.K + kBlk - 1) / kBlk;
     g.rcap = g.rows < kRows ? g.rows : kRows;
-    g.sb = kLdsX / (g.rcap * (2 * kBlk + 4) + 16);
-    if (g.sb > nblk) g.sb = nblk;
+    // All channels in LDS, two work-groups a CU if that fits, else one; the
+    // waves of a slot then share out its blocks.  Else a wave takes its tiles
+    // alone, and the activations are brought anew for every step.
+    const size_t row = 2 * kBlk + 4, part = (size_t)2 * kRt * 64 * 16;
     g.kw = 1;
-    while (g.kw < kWaves && live * ((pairs * g.kw + kWaves - 1) / kWaves) < 512 &&
-           2 * g.kw <= g.sb)
-        g.kw *= 2;
-    if (g.sb > g.kw) g.sb -= g.sb % g.kw;
-    const int64_t slabs = (pairs * g.kw + kWaves - 1) / kWaves;
+    while (g.kw < kWaves && 2 * g.kw <= nblk) g.kw *= 2;
+    const size_t join = g.kw > 1 ? (kWaves - 1) * part : 0;
+    auto blocks = [&](size_t bytes) {
+        return bytes < 1024 ? 0 : ((int64_t)((bytes - 16) / g.rcap) - 16) / (int64_t)row;
+    };
+    const size_t two = kRt > 2 ? 0 : kLds / 2, one = kLds - 1024;
+    bool pairs = true;
+    if (two > join && blocks(two - join) >= nblk) {
+        g.sb = nblk;
+    } else if (blocks(one - join) >= nblk) {
+        g.sb = nblk;
+        pairs = false;
+    } else {
+        g.kw = 1;
+        pairs = kRt <= 2;
+        g.sb = (int)blocks(pairs ? two : one);
+        if (g.sb > nblk) g.sb = nblk;
+    }
+    // as many work-groups as are resident, but at least 16 features per slot
+    const int slots = kWaves / g.kw;
+    int64_t slabs = (pairs ? 2 : 1) * kCus / live;
+    const int64_t most = ((int64_t)nout + 16 * slots - 1) / (16 * slots);
+    if (slabs > most) slabs = most;
+    if (slabs < 1) slabs = 1;
     if (slabs * units >= ((int64_t)1 << 31)) return QUADS_ESHAPE;
     g.slabs = (int)slabs;
-    size_t bytes = (size_t)g.rcap * (g.sb * (2 * kBlk + 4) + 16);
-    const size_t join = g.kw > 1 ? (size_t)kWaves * 2 * kRt * 64 * 16 : 0;
-    if (join > bytes) bytes = join;
+    const int64_t quads_n = (nout + 3) / 4, share = (quads_n + slabs * slots - 1) / (slabs * slots);
+    g.steps = (int)((4 * share + kStep - 1) / kStep);
+    size_t bytes = (g.rcap * (16 + g.sb * row) + 15) & ~(size_t)15;
+    if (g.kw > 1) bytes += (kWaves - 1) * part;
     hipLaunchKernelGGL((k_w4a16<kEpi, kRt>), dim3((unsigned)(slabs * units)), dim3(kThreads),
                        bytes, st, g);
     QUADS_CHECK_LAUNCH();
     return QUADS_OK;
 }
 
+// Rows per unit: 16 while an expert has few rows on average, else up to 64, so
+// that its weights are read once.
 template <int kEpi>
 int dispatch(const Args& g, hipStream_t st) {
     const int64_t mean = g.offsets ? ((int64_t)g.rows + g.E - 1) / g.E : g.rows;
@@ -412,7 +490,7 @@ extern "C" int quads_moe_w4a16_gemv(const uint16_t* x, const int32_t* row_token,
                                     const float* w_ts, const int32_t* offsets, int32_t E,
                                     int64_t N, int epilogue, int out_dtype, void* out, void* ws,
                                     size_t ws_bytes, void* stream) {
-    if (rows < 0 || rows >= ((int64_t)1 << 31) || K <= 0 || K % kBlock || K >= ((int64_t)1 << 30) ||
+    if (rows < 0 || rows >= ((int64_t)1 << 31) || K <= 0 || K % kBlock || K >= ((int64_t)1 << 26) ||
         E < 1 || E > 4096 || N < 1 || N >= ((int64_t)1 << 30))
         return QUADS_ESHAPE;
     if (epilogue != QUADS_EPI_NONE && epilogue != QUADS_EPI_SWIGLU) return QUADS_EINVAL;
