@@ -24,7 +24,7 @@
  *
  * Logits.  z [T, V], `dtype` QUADS_OUT_F32 or QUADS_OUT_BF16, row t at element
  * t * ld (ld >= V; elements V .. ld - 1 of a row are neither read nor
- * written).  1 <= V < 2^30, T and ld < 2^31.  0 < inv_temp <= 1e30, it below;
+ * written).  1 <= V < 2^30, T < 2^24, ld < 2^31.  0 < inv_temp <= 1e30, it below;
  * probabilities are those of softmax(it * z).  Entries may be -inf (masked):
  * their probability is 0.  A row whose every entry is -inf has entropy 0, the
  * stats (-inf, 0) and a zero gradient.  A row with +inf or NaN gives NaN.
@@ -48,14 +48,18 @@ extern "C" {
  * W4A16 grouped product for few rows per expert (Eq. (12) in the forward
  * direction, on the NVFP4 codes themselves): for packed row p of expert e,
  *   Y[p, n] = s_tW[e] sum_{j<K} x[row(p), j] w_e[n, j],   w the exact v*s_b.
- *   x          bf16 [Tx, K], finite, K % 16 == 0, K < 2^26
+ *   x          bf16 [Tx, K], finite, K % 16 == 0, K < 2^26; rows < 2^24
  *   row_token  NULL: row(p) = p (Tx = rows); else int32 [rows], row(p) =
  *              row_token[p] < Tx
  *   w_nib, w_scale, w_ts, offsets, E, N, epilogue, out_dtype, out   as in
  *              quads_moe_w4a4_gemm (offsets may be NULL when E == 1)
- * Any number of rows is computed; the cost is one read of an expert's weights
- * per 16 of its rows, so that larger batches belong to a GEMM.
- * Workspace: quads_moe_w4a16_gemv_ws bytes.
+ * Any number of rows is computed, with one read of an expert's weights per 16
+ * of its rows where experts have few on average, per 64 where they have more:
+ * larger batches belong to a GEMM.
+ * The error is below (176 + K / 1024) 2^-24 sum |x w| per output element plus
+ * the rounding to bf16, and 2^-28 times the largest |x| of a row's 512-channel
+ * block times sum |w| where a block spans more than 28 binary orders.
+ * Workspace: quads_moe_w4a16_gemv_ws bytes (0: NULL is allowed).
  */
 size_t quads_moe_w4a16_gemv_ws(int64_t rows, int64_t K, int32_t E, int64_t N);
 int quads_moe_w4a16_gemv(const uint16_t* x, const int32_t* row_token, int64_t rows, int64_t K,

@@ -460,7 +460,7 @@ void launch_loss(const void* z, int64_t T, int64_t V, int64_t ld, const List& l,
 template <int kBf16>
 void launch_bwd(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, float it,
                 const float* stats, const float* g, void* dz, hipStream_t st) {
-    const int parts = row_parts(T, V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32);
+    const int parts = grad_parts(T, V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32);
     hipLaunchKernelGGL(k_distill_bwd<kBf16>, dim3((unsigned)(T * parts)), dim3(kThreads), 0, st, z,
                        V, ld, parts, l, it, stats, g, dz);
 }

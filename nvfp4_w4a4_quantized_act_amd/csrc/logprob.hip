@@ -423,8 +423,11 @@ __global__ __launch_bounds__(kThreads) void k_logprob_bwd(const void* z, int64_t
                                                           const float* g_logp,
                                                           const float* g_entropy, void* dz) {
     constexpr int kPer = Row<kBf16>::kPer;
-    const int64_t t = blockIdx.x / (unsigned)parts;
-    const int part = (int)(blockIdx.x % (unsigned)parts);
+    // the last rows first: they are the ones the forward pass has left in the
+    // cache (4096 x 65536 bf16, both passes: 327 -> 322 us)
+    const unsigned at = gridDim.x - 1 - blockIdx.x;
+    const int64_t t = at / (unsigned)parts;
+    const int part = (int)(at % (unsigned)parts);
     const Row<kBf16> r(z, t, ld, V);
     char* out = (char*)dz + (r.at - (const char*)z);
     const int chunks = (r.nvec + kChunk - 1) / kChunk;
@@ -547,7 +550,7 @@ extern "C" int quads_token_logprob_backward(const void* logits, int dtype, int64
         return QUADS_EINVAL;
     if ((g_logp != nullptr && ids == nullptr) || (g_entropy != nullptr && entropy == nullptr))
         return QUADS_EINVAL;
-    const int parts = head::row_parts(T, V, dtype);
+    const int parts = head::grad_parts(T, V, dtype);
     const dim3 grid((unsigned)(T * parts)), block(head::kThreads);
     hipStream_t st = (hipStream_t)stream;
     if (dtype == QUADS_OUT_BF16)

@@ -420,7 +420,12 @@ int launch(Args g, hipStream_t st) {
     const int nout = kEpi == QUADS_EPI_SWIGLU ? g.N / 2 : g.N;
     const int64_t units = g.offsets ? (int64_t)(g.E < g.rows ? g.E : g.rows) + g.rows / kRows
                                     : ((int64_t)g.rows + kRows - 1) / kRows;
-    const int64_t live = g.offsets ? (g.E < g.rows ? g.E : g.rows) : units;
+    // units that have work, as far as the host can tell
+    int64_t live = units;
+    if (g.offsets) {
+        live = g.E < g.rows ? g.E : g.rows;
+        if (live < g.rows / kRows) live = g.rows / kRows;
+    }
     const int nblk = (g.K + kBlk - 1) / kBlk;
     g.rcap = g.rows < kRows ? g.rows : kRows;
     // All channels in LDS, two work-groups a CU if that fits, else one; the
@@ -452,7 +457,6 @@ int launch(Args g, hipStream_t st) {
     const int64_t most = ((int64_t)nout + 16 * slots - 1) / (16 * slots);
     if (slabs > most) slabs = most;
     if (slabs < 1) slabs = 1;
-    if (slabs * units >= ((int64_t)1 << 31)) return QUADS_ESHAPE;
     g.slabs = (int)slabs;
     const int64_t quads_n = (nout + 3) / 4, share = (quads_n + slabs * slots - 1) / (slabs * slots);
     g.steps = (int)((4 * share + kStep - 1) / kStep);
@@ -490,7 +494,7 @@ extern "C" int quads_moe_w4a16_gemv(const uint16_t* x, const int32_t* row_token,
                                     const float* w_ts, const int32_t* offsets, int32_t E,
                                     int64_t N, int epilogue, int out_dtype, void* out, void* ws,
                                     size_t ws_bytes, void* stream) {
-    if (rows < 0 || rows >= ((int64_t)1 << 31) || K <= 0 || K % kBlock || K >= ((int64_t)1 << 26) ||
+    if (rows < 0 || rows >= ((int64_t)1 << 24) || K <= 0 || K % kBlock || K >= ((int64_t)1 << 26) ||
         E < 1 || E > 4096 || N < 1 || N >= ((int64_t)1 << 30))
         return QUADS_ESHAPE;
     if (epilogue != QUADS_EPI_NONE && epilogue != QUADS_EPI_SWIGLU) return QUADS_EINVAL;

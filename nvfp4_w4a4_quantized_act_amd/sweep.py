@@ -32,7 +32,16 @@ W [4096, 4096] N(0, 0.02); moe = the gate/up GEMM of the MoE layer, X [4096,
 2048] with 20 outlier channels x20, 128 experts, top-8 softmax routing, W13
 [128, 1536, 2048].  The fp64 references run on the host CPU (numpy).
 
-    python -m nvfp4_w4a4_quantized_act_amd.sweep [--workloads dense,moe] [--tokens T]
+A third workload, only on request, is the pages' own measure (Table 3) at one
+output head: head = X [256, 2048] with 20 outlier channels x20, W [32768, 2048].
+The learner's logits are the W4A16 product (quads_moe_w4a16_gemv), the
+rollout's the W4A4 GEMM of RAC(X, k), on the same NVFP4 weights; tokens are
+drawn once from the learner's distribution, and both sides' log-probabilities
+come from quads_token_logprob.  Reported per k: the largest and the mean
+|log-probability difference| of the tokens, and the divergence of the learner
+from the rollout's 64 most probable tokens (quads_topk_distill).
+
+    python -m nvfp4_w4a4_quantized_act_amd.sweep [--workloads dense,moe,head] [--tokens T]
 """
 
 import argparse
@@ -175,6 +184,53 @@ def sweep_moe(Q, torch, synth, dev, fractions=FRACTIONS, **overrides):
     return out
 
 
+HEAD = dict(m=256, k_dim=2048, n=32768, body="normal", n_outlier=20, factor=20.0)
+HEAD_TOP = 64
+
+
+def sample_tokens(z, seed=77):
+    """One token per row from softmax(z) (fp64 logits, seeded): the largest z + Gumbel noise."""
+    u = np.random.default_rng(seed).random(z.shape)
+    return np.argmax(z - np.log(-np.log(u)), axis=1).astype(np.int32)
+
+
+def sweep_head(Q, torch, synth, dev, fractions=FRACTIONS, **overrides):
+    """Rows of the sweep for the output head (sizes overridable)."""
+    d = synth.make(2, **dict(HEAD, **overrides))
+    x, w = d["x"], d["w"]
+    m, kdim = x.shape
+    n = w.shape[1]
+    top = min(HEAD_TOP, n)
+    x_t = torch.from_numpy(x.view(np.int16)).to(dev)
+    wq = Q.quads_nvfp4_weight_qdq(torch.from_numpy(w.view(np.int16)).to(dev))[:3]
+    learner = Q.quads_moe_w4a16_gemv(x_t, wq, n, out_dtype=Q.OUT_F32)
+    ids = torch.from_numpy(sample_tokens(learner.cpu().numpy().astype(np.float64))).to(dev)
+    lp = Q.quads_token_logprob(learner, ids)["logp"]
+    out = []
+    for f in fractions:
+        k = channels_for(f, kdim)
+        a = Q.quads_rac_quantize(x_t, k)
+        r = (a["r_nib"], a["r_scale"], a["r_ts"]) if k else None
+        rollout = Q.quads_moe_w4a4_gemm((a["nib"], a["scale"], a["ts"]), wq, n, rows=m, r=r,
+                                        sel=a["sel"] if k else None, out_dtype=Q.OUT_F32)
+        p = Q.quads_token_logprob(rollout, ids, topk=top)
+        gap = (lp - p["logp"]).abs().cpu().numpy().astype(np.float64)
+        div, _ = Q.quads_topk_distill(learner, p["top_logp"], p["top_id"], renorm=False)
+        out.append(dict(workload="head", M=m, K=kdim, N=n, format="nvfp4", frac=f, k=k,
+                        max_gap=float(gap.max()), mean_gap=float(gap.mean()),
+                        divergence=float(div.mean().item())))
+    return out
+
+
+def head_table(rows):
+    lines = ["| workload | k / K | k | max log-prob difference | mean | divergence (top 64) |",
+             "|---|---|---|---|---|---|"]
+    for r in rows:
+        lines.append(f"| {r['workload']} | {100 * r['frac']:.1f} % | {r['k']} | "
+                     f"{r['max_gap']:.5f} | {r['mean_gap']:.5f} | {r['divergence']:.6f} |")
+    return "\n".join(lines)
+
+
 def table(rows):
     def f5(v):
         return "—" if v is None else f"{v:.5f}"
@@ -189,7 +245,8 @@ def table(rows):
 
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
-    ap.add_argument("--workloads", default="dense,moe")
+    ap.add_argument("--workloads", default="dense,moe",
+                    help="of dense, moe and head (default: dense,moe)")
     ap.add_argument("--tokens", type=int, default=0,
                     help="override the token count (0: the workloads' own)")
     args = ap.parse_args(argv)
@@ -203,7 +260,7 @@ def main(argv=None):
     import nvfp4_w4a4_quantized_act_amd as Q
     Q.lib()
     dev = torch.device("cuda:0")
-    rows = []
+    rows, head = [], []
     for wl in args.workloads.split(","):
         if wl == "dense":
             kw = dict(m=args.tokens) if args.tokens else {}
@@ -211,12 +268,18 @@ def main(argv=None):
         elif wl == "moe":
             kw = dict(t=args.tokens) if args.tokens else {}
             got = sweep_moe(Q, torch, synth, dev, **kw)
+        elif wl == "head":
+            kw = dict(m=args.tokens) if args.tokens else {}
+            got = sweep_head(Q, torch, synth, dev, **kw)
         else:
             raise SystemExit(f"unknown workload {wl}")
         for r in got:
             print(json.dumps(r), flush=True)
-        rows += got
-    print(table(rows))
+        (head if wl == "head" else rows).extend(got)
+    if rows:
+        print(table(rows))
+    if head:
+        print(head_table(head))
 
 
 if __name__ == "__main__":

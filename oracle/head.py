@@ -88,7 +88,7 @@ def teacher(t_val, t_id, v, it=1.0, renorm=True):
         m = np.where(np.isneginf(m), 0.0, m)
         with np.errstate(divide="ignore", invalid="ignore"):
             y = y - m - np.log(np.exp(y - m).sum(axis=1, keepdims=True))
-        y = np.where(have, y, -np.inf)
+        y = np.where(have & ~np.isnan(y), y, -np.inf)    # a list of probability 0 stays 0
     return np.exp(y), y
 
 

@@ -295,7 +295,8 @@ def distill_tolerance(zr, t_val, t_id, w, g, it, renorm, dtype, want_dz):
     with np.errstate(invalid="ignore"):
         part = np.where(q > 0, np.abs(lq) + np.abs(lpi), 0.0)
         tol = np.where(q > 0, q * (np.abs(lq - lpi) * eq + eq + elpi + (k + 4) * U * part), 0).sum(1)
-    tol_loss = np.abs(w) * tol * (1 + U) + np.abs(w) * 4 * U * np.where(q > 0, q * part, 0).sum(1)
+    with np.errstate(invalid="ignore"):                      # (an infinite loss has no tolerance)
+        tol_loss = np.abs(w) * (tol * (1 + U) + 4 * U * np.where(q > 0, q * part, 0).sum(1))
     p = np.exp(lp)
     big = q.sum(1, keepdims=True)
     tol = big * (p * (elp + 8 * U + eq.max(1, keepdims=True) + (k + 8) * U) + 2.0 ** -126)
@@ -355,7 +356,8 @@ def test_distill(Q, t, v, ld, k, renorm, dtype):
 
 
 @pytest.mark.parametrize("t,v,ld,dtype,k", [
-    (2100, 700, None, "bf16", 5), (2053, 1025, 1032, "f32", 70), (2048, 16383, None, "f32", 9),
+    (2100, 1, None, "bf16", 1), (2061, 7, None, "bf16", 3), (2050, 9, None, "f32", 2),
+    (2049, 17, 24, "bf16", 17), (2100, 700, None, "bf16", 5), (2053, 1025, 1032, "f32", 70), (2048, 16383, None, "f32", 9),
     (1030, 32771, 32776, "bf16", 20), (1025, 16405, None, "f32", 4), (515, 65539, None, "bf16", 64),
     (513, 65537, None, "f32", 33), (512, 131081, None, "bf16", 128)])
 def test_distill_many_rows(Q, t, v, ld, dtype, k):

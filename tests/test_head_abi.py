@@ -42,7 +42,7 @@ def test_gemv_validation():
         return f(x, rt, rows, k, FAKE, FAKE, ts, off, e, n, epi, odt, out, ws, wsz, None)
     assert call(k=250) == -2 and call(k=0) == -2
     assert call(e=0) == -2 and call(e=4097) == -2 and call(n=0) == -2
-    assert call(rows=-1) == -2 and call(rows=1 << 31) == -2
+    assert call(rows=-1) == -2 and call(rows=1 << 24) == -2 and call(k=1 << 26) == -2
     assert call(epi=1, odt=1, n=63) == -2
     assert call(epi=1, odt=0) == -1 and call(epi=2) == -1 and call(odt=3) == -1
     assert call(off=None) == -1
@@ -61,11 +61,12 @@ def test_logprob_validation():
     def call(z=FAKE, dt=0, t=4, v=1000, ld=1000, ids=FAKE, it=1.0, k=8, lp=FAKE, ent=FAKE,
              st=FAKE, tl=FAKE, ti=FAKE, wsp=FAKE, wsz=ws):
         return f(z, dt, t, v, ld, ids, it, k, lp, ent, st, tl, ti, wsp, wsz, None)
-    assert call(t=-1) == -2 and call(t=1 << 31) == -2
-    assert call(v=0) == -2 and call(ld=999) == -2 and call(v=1 << 31, ld=1 << 31) == -2
+    assert call(t=-1) == -2 and call(t=1 << 24) == -2
+    assert call(v=0) == -2 and call(ld=999) == -2 and call(ld=1 << 31) == -2
+    assert call(v=1 << 30, ld=1 << 30) == -2
     assert call(k=129) == -2 and call(k=-1) == -2 and call(v=5, k=6) == -2
     assert call(dt=2) == -1
-    for it in (0.0, -1.0, INF, NAN):
+    for it in (0.0, -1.0, 2e30, INF, NAN):
         assert call(it=it) == -1
     assert call(z=None) == -1 and call(z=MIS) == -1 and call(ids=MIS2) == -1
     assert call(ids=None) == -1 and call(lp=None) == -1        # both or neither
