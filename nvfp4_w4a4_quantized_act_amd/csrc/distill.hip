@@ -302,6 +302,10 @@ __global__ __launch_bounds__(kThreads) void k_distill_bwd(const void* z, int64_t
 
 // ------------------------------------------------------- loss and gradient --
 
+__device__ __forceinline__ void st_stream16(char* p, const uint4& q) {
+    __builtin_nontemporal_store((u32x4){q.x, q.y, q.z, q.w}, reinterpret_cast<u32x4*>(p));
+}
+
 // One row at a time, read once: a thread keeps kNv of the row's vectors in
 // registers between the log-sum and the gradient (a CU's registers hold 256
 // KB of a row: 131072 bf16 or 65536 fp32 entries); what a longer row has
@@ -310,7 +314,13 @@ __global__ __launch_bounds__(kThreads) void k_distill_bwd(const void* z, int64_t
 // of the one whose gradient was just stored, so that loads, stores and
 // arithmetic overlap although a CU holds one row at a time.  The partial
 // vectors at a row's ends are in one more register vector of threads 0 and 1.
-template <int kBf16, int kThr, int kNv>
+//
+// kLong (rows beyond the registers): what is read or written once is marked
+// as not to be kept, so that the cache keeps the part that is read again (1000
+// x 100001 fp32: 189 -> 173 us, 512 x 100000: 95 -> 81, 1000 x 200000 bf16: 194
+// -> 192; shorter rows gain or lose by it, from 111 -> 121 us at 4096 x 30000
+// bf16 to 394 -> 379 at 4096 x 60000 fp32, and do without).
+template <int kBf16, int kThr, int kNv, bool kLong>
 __global__ __launch_bounds__(kThr, 4) void k_distill_row(const void* z, int64_t T, int64_t V,
                                                       int64_t ld, List l, float it, float* loss,
                                                       void* dz) {
@@ -338,7 +348,8 @@ __global__ __launch_bounds__(kThr, 4) void k_distill_row(const void* z, int64_t 
     auto load = [&](const Row<kBf16>& r, int n, int i) {
         const char* at = r.at + 16 * (int64_t)(first(r) + i * kThr);
         x[i] = masked;
-        if (i * kThr + tid < n) x[i] = *reinterpret_cast<const uint4*>(at + lane16);
+        if (i * kThr + tid < n)
+            x[i] = kLong ? ld_stream16(at + lane16) : *reinterpret_cast<const uint4*>(at + lane16);
     };
     auto load_edge = [&](const Row<kBf16>& r, bool live) {
         const int j = live ? edge_at(r) : -1;
@@ -386,7 +397,7 @@ __global__ __launch_bounds__(kThr, 4) void k_distill_row(const void* z, int64_t 
             pin(x[i]);
             __builtin_amdgcn_sched_barrier(0);
         }
-        for (int i = kNv * kThr + tid; i < beyond; i += kThr) {
+        for (int i = kNv * kThr + tid; kLong && i < beyond; i += kThr) {
             const uint4 y = *r.vec(first(r) + i);
             stat_raise(a, vec_max<kBf16>(y, a.m), cl);
             a.s = vec_sum<kBf16>(y, stat_base(a.m), cl, a.s);
@@ -401,11 +412,11 @@ __global__ __launch_bounds__(kThr, 4) void k_distill_row(const void* z, int64_t 
         // gradient
         base = stat_base(a.m);
         const float l2 = ls * kLog2e, f = w == 0.0f ? 0.0f : by * q.all;
-        for (int i = kNv * kThr + tid; i < n; i += kThr) {
+        for (int i = kNv * kThr + tid; kLong && i < n; i += kThr) {
             const int j = first(r) + i;
             uint4 y = masked;
             if (i < beyond) y = *r.vec(j);
-            reinterpret_cast<uint4*>(out)[j] = dense<kBf16>(y, base, cl, l2, f);
+            st_stream16(out + 16 * (int64_t)j, dense<kBf16>(y, base, cl, l2, f));
         }
         const int j = edge_at(r);
         if (j >= 0) store_part<kBf16>(r, out, j, dense<kBf16>(edge, base, cl, l2, f));
@@ -414,7 +425,10 @@ __global__ __launch_bounds__(kThr, 4) void k_distill_row(const void* z, int64_t 
         for (int i = 0; i < kNv; ++i) {
             const uint4 y = dense<kBf16>(x[i], base, cl, l2, f);
             char* to = out + 16 * (int64_t)(first(r) + i * kThr);
-            if (i * kThr + tid < n) *reinterpret_cast<uint4*>(to + lane16) = y;
+            if (i * kThr + tid < n) {
+                if (kLong) st_stream16(to + lane16, y);
+                else *reinterpret_cast<uint4*>(to + lane16) = y;
+            }
             load(rn, nn, i);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -436,7 +450,10 @@ inline int check_list(int64_t T, const float* t_val, const int32_t* t_id, int32_
 // Work-groups of k_distill_row that are resident together, for rows of nvec
 // vectors: the smallest work-group whose registers hold a row.
 constexpr int kCus = 256;
-inline int row_threads(int64_t nvec) { return nvec <= 16 * 256 ? 256 : nvec <= 16 * 512 ? 512 : 1024; }
+constexpr int kRowVecs = 16;                        // vectors of a row per thread
+inline int row_threads(int64_t nvec) {
+    return nvec <= kRowVecs * 256 ? 256 : nvec <= kRowVecs * 512 ? 512 : 1024;
+}
 inline int64_t row_slots(int64_t nvec) { return (int64_t)kCus * (1024 / row_threads(nvec)); }
 inline int64_t row_vectors(int64_t V, int dtype) {
     const int per = dtype == QUADS_OUT_BF16 ? 8 : 4;
@@ -472,14 +489,17 @@ void launch_row(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, 
     const int64_t slots = row_slots(nvec);
     const dim3 grid((unsigned)(T < slots ? T : slots)), block(thr);
     if (thr == 256)
-        hipLaunchKernelGGL((k_distill_row<kBf16, 256, 16>), grid, block, 0, st, z, T, V, ld, l, it,
-                           loss, dz);
+        hipLaunchKernelGGL((k_distill_row<kBf16, 256, kRowVecs, false>), grid, block, 0, st, z, T, V,
+                           ld, l, it, loss, dz);
     else if (thr == 512)
-        hipLaunchKernelGGL((k_distill_row<kBf16, 512, 16>), grid, block, 0, st, z, T, V, ld, l, it,
-                           loss, dz);
+        hipLaunchKernelGGL((k_distill_row<kBf16, 512, kRowVecs, false>), grid, block, 0, st, z, T, V,
+                           ld, l, it, loss, dz);
+    else if (nvec <= kRowVecs * 1024)
+        hipLaunchKernelGGL((k_distill_row<kBf16, 1024, kRowVecs, false>), grid, block, 0, st, z, T, V,
+                           ld, l, it, loss, dz);
     else
-        hipLaunchKernelGGL((k_distill_row<kBf16, 1024, 16>), grid, block, 0, st, z, T, V, ld, l,
-                           it, loss, dz);
+        hipLaunchKernelGGL((k_distill_row<kBf16, 1024, kRowVecs, true>), grid, block, 0, st, z, T, V,
+                           ld, l, it, loss, dz);
 }
 
 // Workspace: the parts' statistics, then the rows' stats (which
