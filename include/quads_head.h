@@ -54,8 +54,7 @@ extern "C" {
  *   w_nib, w_scale, w_ts, offsets, E, N, epilogue, out_dtype, out   as in
  *              quads_moe_w4a4_gemm (offsets may be NULL when E == 1)
  * Any number of rows is computed, with one read of an expert's weights per 16
- * of its rows where experts have few on average, per 64 where they have more:
- * larger batches belong to a GEMM.
+ * or 32 of its rows: larger batches belong to a GEMM.
  * The error is below (176 + K / 1024) 2^-24 sum |x w| per output element plus
  * the rounding to bf16, and 2^-28 times the largest |x| of a row's 512-channel
  * block times sum |w| where a block spans more than 28 binary orders.
@@ -128,6 +127,7 @@ int quads_topk_distill_backward(const void* logits, int dtype, int64_t T, int64_
                                 const float* t_val, const int32_t* t_id, int32_t topk,
                                 const float* weight, float inv_temp, int renorm,
                                 const float* stats, const float* g, void* dlogits, void* stream);
+size_t quads_topk_distill_grad_ws(int64_t T, int64_t V, int32_t topk);
 int quads_topk_distill_grad(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
                             const float* t_val, const int32_t* t_id, int32_t topk,
                             const float* weight, float inv_temp, int renorm, float* loss,

@@ -105,6 +105,7 @@ _SIGNATURES = {
                                   _P, _SZ, _P]),
     "quads_topk_distill_backward": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _I32, _P, _F,
                                            _INT, _P, _P, _P, _P]),
+    "quads_topk_distill_grad_ws": (_SZ, [_I64, _I64, _I32]),
     "quads_topk_distill_grad": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _I32, _P, _F, _INT,
                                        _P, _P, _P, _SZ, _P]),
 }
@@ -754,7 +755,7 @@ def quads_topk_distill_grad(logits, t_val, t_id, weight=None, inv_temp=1.0, reno
     t_val, t_id, k, weight = _teacher(t_val, t_id, weight, t, dev)
     loss = torch.empty(t, dtype=torch.float32, device=dev)
     out = _like_logits(z, t, v, ld, out)
-    nws = lib().quads_topk_distill_ws(t, v, k)
+    nws = lib().quads_topk_distill_grad_ws(t, v, k)
     ws = _scratch(nws, dev)
     _call("quads_topk_distill_grad", dev, _at(z), code, t, v, ld, _at(t_val), _at(t_id), k,
           _at(weight), inv_temp, int(renorm), _at(loss), _at(out), _at(ws), nws)

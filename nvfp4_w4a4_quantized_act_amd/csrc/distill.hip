@@ -9,9 +9,9 @@
 // before anything is written (dlogits may be the logits), and written over
 // the dense ones after a barrier.
 //
-// Loss and gradient of many rows in one call go through k_distill_row, which
-// reads each row once: see there.  Everything else streams a row, or its parts
-// where there are few rows (logits.h): k_distill_loss, k_distill_join,
+// Loss and gradient in one call go through k_distill_row, which reads each row
+// once: see there.  The loss alone and the gradient alone stream a row, or its
+// parts where there are few rows (logits.h): k_distill_loss, k_distill_join,
 // k_distill_bwd.
 #include "logits.h"
 
@@ -385,18 +385,20 @@ __global__ __launch_bounds__(kThr, 4) void k_distill_row(const void* z, int64_t 
         // log-sum: the vectors in registers, then those beyond them
         Stat a = {vec_max<kBf16>(edge, -INFINITY), 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < kNv; ++i) {
-            a.m = vec_max<kBf16>(x[i], a.m);
-            pin(x[i]);
-        }
+        for (int i = 0; i < kNv; ++i)
+            if (i * kThr < n) {
+                a.m = vec_max<kBf16>(x[i], a.m);
+                pin(x[i]);
+            }
         float base = stat_base(a.m);
         a.s = vec_sum<kBf16>(edge, base, cl, 0.0f);
 #pragma unroll
-        for (int i = 0; i < kNv; ++i) {
-            a.s = vec_sum<kBf16>(x[i], base, cl, a.s);
-            pin(x[i]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int i = 0; i < kNv; ++i)
+            if (i * kThr < n) {
+                a.s = vec_sum<kBf16>(x[i], base, cl, a.s);
+                pin(x[i]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         for (int i = kNv * kThr + tid; kLong && i < beyond; i += kThr) {
             const uint4 y = *r.vec(first(r) + i);
             stat_raise(a, vec_max<kBf16>(y, a.m), cl);
@@ -423,11 +425,13 @@ __global__ __launch_bounds__(kThr, 4) void k_distill_row(const void* z, int64_t 
         load_edge(rn, more);
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
-            const uint4 y = dense<kBf16>(x[i], base, cl, l2, f);
-            char* to = out + 16 * (int64_t)(first(r) + i * kThr);
-            if (i * kThr + tid < n) {
-                if (kLong) st_stream16(to + lane16, y);
-                else *reinterpret_cast<uint4*>(to + lane16) = y;
+            if (i * kThr < n) {
+                const uint4 y = dense<kBf16>(x[i], base, cl, l2, f);
+                char* to = out + 16 * (int64_t)(first(r) + i * kThr);
+                if (i * kThr + tid < n) {
+                    if (kLong) st_stream16(to + lane16, y);
+                    else *reinterpret_cast<uint4*>(to + lane16) = y;
+                }
             }
             load(rn, nn, i);
             __builtin_amdgcn_sched_barrier(0);
@@ -447,21 +451,27 @@ inline int check_list(int64_t T, const float* t_val, const int32_t* t_id, int32_
     return ok_ptr4(t_val) && ok_ptr4(t_id) && ok_opt4(weight) ? QUADS_OK : QUADS_EINVAL;
 }
 
-// Work-groups of k_distill_row that are resident together, for rows of nvec
-// vectors: the smallest work-group whose registers hold a row.
+// The work-group of k_distill_row: the smallest whose registers hold a row of
+// nvec vectors (4096 x 2000 bf16: 16 us with 64 threads, 21 with 128, 33 with
+// 256), and how many of them are resident together.
 constexpr int kCus = 256;
-constexpr int kRowVecs = 16;                        // vectors of a row per thread
+constexpr int kRowVecs = 16;                   // vectors of a row per thread
 inline int row_threads(int64_t nvec) {
-    return nvec <= kRowVecs * 256 ? 256 : nvec <= kRowVecs * 512 ? 512 : 1024;
+    int n = 64;
+    while (n < 1024 && nvec > kRowVecs * n) n *= 2;
+    return n;
 }
 inline int64_t row_slots(int64_t nvec) { return (int64_t)kCus * (1024 / row_threads(nvec)); }
 inline int64_t row_vectors(int64_t V, int dtype) {
     const int per = dtype == QUADS_OUT_BF16 ? 8 : 4;
     return (V + per - 1) / per;
 }
-// Rows enough for k_distill_row: each resident work-group has at least two.
+// Whether loss and gradient take k_distill_row: always, but for a few rows that
+// are longer than a work-group's registers, which are split (in us, row by row
+// / split: 1 x 20000 bf16 13 / 20, 64 x 131072 bf16 22 / 21, 300 x 131072 55 /
+// 49, 600 x 131072 84 / 101, 64 x 100001 fp32 23 / 25).
 inline bool whole_rows(int64_t T, int64_t V, int dtype) {
-    return T >= 2 * row_slots(row_vectors(V, dtype));
+    return T >= 64 || row_vectors(V, dtype) <= kRowVecs * 1024;
 }
 
 template <int kBf16>
@@ -488,25 +498,22 @@ void launch_row(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, 
     const int thr = row_threads(nvec);
     const int64_t slots = row_slots(nvec);
     const dim3 grid((unsigned)(T < slots ? T : slots)), block(thr);
-    if (thr == 256)
-        hipLaunchKernelGGL((k_distill_row<kBf16, 256, kRowVecs, false>), grid, block, 0, st, z, T, V,
-                           ld, l, it, loss, dz);
-    else if (thr == 512)
-        hipLaunchKernelGGL((k_distill_row<kBf16, 512, kRowVecs, false>), grid, block, 0, st, z, T, V,
-                           ld, l, it, loss, dz);
-    else if (nvec <= kRowVecs * 1024)
-        hipLaunchKernelGGL((k_distill_row<kBf16, 1024, kRowVecs, false>), grid, block, 0, st, z, T, V,
-                           ld, l, it, loss, dz);
-    else
-        hipLaunchKernelGGL((k_distill_row<kBf16, 1024, kRowVecs, true>), grid, block, 0, st, z, T, V,
-                           ld, l, it, loss, dz);
+#define QUADS_ROW(THR, LONG)                                                                  \
+    hipLaunchKernelGGL((k_distill_row<kBf16, THR, kRowVecs, LONG>), grid, block, 0, st, z, T, V, \
+                       ld, l, it, loss, dz)
+    if (thr == 64) QUADS_ROW(64, false);
+    else if (thr == 128) QUADS_ROW(128, false);
+    else if (thr == 256) QUADS_ROW(256, false);
+    else if (thr == 512) QUADS_ROW(512, false);
+    else if (nvec <= kRowVecs * 1024) QUADS_ROW(1024, false);
+    else QUADS_ROW(1024, true);
+#undef QUADS_ROW
 }
 
-// Workspace: the parts' statistics, then the rows' stats (which
-// quads_topk_distill_grad keeps there between its two steps).
+// The parts' statistics.
 inline size_t parts_ws(int64_t T, int64_t V) {
     const int parts = row_parts(T, V, QUADS_OUT_F32);
-    return parts > 1 ? align_up((size_t)T * parts * 16, 16) : 0;
+    return parts > 1 ? (size_t)T * parts * 16 : 0;
 }
 
 }  // namespace head
@@ -515,8 +522,14 @@ inline size_t parts_ws(int64_t T, int64_t V) {
 using namespace quads;
 
 extern "C" size_t quads_topk_distill_ws(int64_t T, int64_t V, int32_t topk) {
-    if (T < 1 || V < 1 || topk < 1) return 0;
-    return head::parts_ws(T, V) + align_up((size_t)T * 8, 16);
+    return T < 1 || V < 1 || topk < 1 ? 0 : head::parts_ws(T, V);
+}
+
+// The split rows' statistics, then the stats their second step reads (whether
+// rows are split depends on the type: as much as either needs).
+extern "C" size_t quads_topk_distill_grad_ws(int64_t T, int64_t V, int32_t topk) {
+    if (T < 1 || V < 1 || topk < 1 || head::whole_rows(T, V, QUADS_OUT_F32)) return 0;
+    return head::parts_ws(T, V) + (size_t)T * 8;
 }
 
 extern "C" int quads_topk_distill(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
@@ -527,7 +540,8 @@ extern "C" int quads_topk_distill(const void* logits, int dtype, int64_t T, int6
     if (rc == QUADS_OK) rc = head::check_list(T, t_val, t_id, topk, weight, renorm);
     if (rc != QUADS_OK || T == 0) return rc;
     if (!ok_ptr4(loss) || !ok_ptr4(stats)) return QUADS_EINVAL;
-    if (ws_bytes < quads_topk_distill_ws(T, V, topk) || !ok_ptr(ws)) return QUADS_EWORKSPACE;
+    const size_t need = quads_topk_distill_ws(T, V, topk);
+    if (ws_bytes < need || (need > 0 && !ok_ptr(ws))) return QUADS_EWORKSPACE;
     const head::List l{t_val, t_id, weight, (int)topk, renorm};
     if (dtype == QUADS_OUT_BF16)
         head::launch_loss<1>(logits, T, V, ld, l, inv_temp, loss, stats, ws, (hipStream_t)stream);
@@ -564,7 +578,8 @@ extern "C" int quads_topk_distill_grad(const void* logits, int dtype, int64_t T,
     if (rc == QUADS_OK) rc = head::check_list(T, t_val, t_id, topk, weight, renorm);
     if (rc != QUADS_OK || T == 0) return rc;
     if (!ok_ptr4(loss) || !ok_ptr(dlogits)) return QUADS_EINVAL;
-    if (ws_bytes < quads_topk_distill_ws(T, V, topk) || !ok_ptr(ws)) return QUADS_EWORKSPACE;
+    const size_t need = quads_topk_distill_grad_ws(T, V, topk);
+    if (ws_bytes < need || (need > 0 && !ok_ptr(ws))) return QUADS_EWORKSPACE;
     const head::List l{t_val, t_id, weight, (int)topk, renorm};
     hipStream_t st = (hipStream_t)stream;
     const bool bf16 = dtype == QUADS_OUT_BF16;

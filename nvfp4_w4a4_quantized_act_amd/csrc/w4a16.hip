@@ -4,7 +4,7 @@
 //   Y[p, n] = s_tW[e] sum_j x[row(p), j] v_w[n, j] s_b[n, j / 16]
 //
 // What bounds it is the weights' stream from HBM, 0.5625 bytes per weight, so
-// every weight is loaded once per kRt * 16 rows, straight into the registers
+// every weight is loaded once per 16 kRt rows, straight into the registers
 // of the wave that uses it, as wide as it lies, and multiplied on the matrix
 // cores, where up to 16 rows cost no more than one.
 //
@@ -146,7 +146,7 @@ __device__ __forceinline__ void own_scales(u32x2 v, int h, uint32_t s[4]) {
 // fp32 scales of their blocks, then the totals of each slot's waves but the
 // first.
 template <int kEpi, int kRt>
-__global__ __launch_bounds__(kThreads, kRt > 2 ? 2 : 4) void k_w4a16(Args g) {
+__global__ __launch_bounds__(kThreads, 4) void k_w4a16(Args g) {
     constexpr bool swiglu = kEpi == QUADS_EPI_SWIGLU;
     constexpr int kRows = 16 * kRt;
     extern __shared__ __align__(16) char lds[];
@@ -438,17 +438,16 @@ int launch(Args g, hipStream_t st) {
     auto blocks = [&](size_t bytes) {
         return bytes < 1024 ? 0 : ((int64_t)((bytes - 16) / g.rcap) - 16) / (int64_t)row;
     };
-    const size_t two = kRt > 2 ? 0 : kLds / 2, one = kLds - 1024;
+    const size_t two = kLds / 2, one = kLds - 1024;
     bool pairs = true;
-    if (two > join && blocks(two - join) >= nblk) {
+    if (blocks(two - join) >= nblk) {
         g.sb = nblk;
     } else if (blocks(one - join) >= nblk) {
         g.sb = nblk;
         pairs = false;
     } else {
         g.kw = 1;
-        pairs = kRt <= 2;
-        g.sb = (int)blocks(pairs ? two : one);
+        g.sb = (int)blocks(two);
         if (g.sb > nblk) g.sb = nblk;
     }
     // as many work-groups as are resident, but at least 16 features per slot
@@ -468,15 +467,19 @@ int launch(Args g, hipStream_t st) {
     return QUADS_OK;
 }
 
-// Rows per unit: 16 while an expert has few rows on average, else up to 64, so
-// that its weights are read once.
+// Rows per unit: 16; 32, so that the weights are read half as often, where
+// experts have that many, all channels of 32 rows fit in LDS (K <= 2048: one
+// work-group a CU) and the weights are larger than the 32 MB of L2, which
+// otherwise serves the second read.  In us with 16 / 32 rows: 40 x 2048 x
+// 32768 30.6 / 28.0; gate/up of 128 experts of 1536 x 2048, top 8, 256 tokens
+// 71 / 62, 128 tokens 52 / 60; 16 such experts, 64 tokens 29 / 36; 64 x 4096 x
+// 4096 17.6 / 38.  64 rows were never better than both.
 template <int kEpi>
 int dispatch(const Args& g, hipStream_t st) {
-    const int64_t mean = g.offsets ? ((int64_t)g.rows + g.E - 1) / g.E : g.rows;
-    const int64_t most = g.offsets ? 2 * mean : mean;      // experts are not loaded evenly
-    if (most <= 16) return launch<kEpi, 1>(g, st);
-    if (most <= 32) return launch<kEpi, 2>(g, st);
-    return launch<kEpi, 4>(g, st);
+    const int64_t bytes = (int64_t)g.E * g.N * g.K / 16 * 9;
+    const bool many = g.offsets ? g.rows / g.E >= 16 : g.rows > 16;
+    if (many && g.K <= 2048 && bytes > ((int64_t)32 << 20)) return launch<kEpi, 2>(g, st);
+    return launch<kEpi, 1>(g, st);
 }
 
 }  // namespace w4a16

@@ -349,7 +349,8 @@ def check_distill(Q, z, zr, k, it, renorm, dtype, seed=1, weights=True, out=None
                                       (300, 700, None, 5), (6, 4097, None, 16),
                                       (9, 32768, None, 64), (270, 16384, None, 20),
                                       (6, 50001, None, 20), (6, 131072, None, 64),
-                                      (1, 300001, None, 3)])
+                                      (1, 300001, None, 3), (70, 140001, None, 2),
+                                      (5, 131081, 131088, 9)])
 def test_distill(Q, t, v, ld, k, renorm, dtype):
     z, zr = make(t, v, dtype, seed=v + k, ld=ld)
     check_distill(Q, z, zr, k, 0.6 if k % 2 else 1.0, renorm, dtype)
@@ -359,6 +360,7 @@ def test_distill(Q, t, v, ld, k, renorm, dtype):
     (2100, 1, None, "bf16", 1), (2061, 7, None, "bf16", 3), (2050, 9, None, "f32", 2),
     (2049, 17, 24, "bf16", 17), (2100, 700, None, "bf16", 5), (2053, 1025, 1032, "f32", 70), (2048, 16383, None, "f32", 9),
     (1030, 32771, 32776, "bf16", 20), (1025, 16405, None, "f32", 4), (515, 65539, None, "bf16", 64),
+    (4200, 1027, None, "f32", 11), (4097, 8200, None, "bf16", 20), (2049, 8203, 8204, "f32", 6),
     (513, 65537, None, "f32", 33), (512, 131081, None, "bf16", 128)])
 def test_distill_many_rows(Q, t, v, ld, dtype, k):
     """Loss and gradient of many rows in one call: rows held by each size of work-group, rows
@@ -481,7 +483,8 @@ def test_autograd_over_three_dimensions(Q, qat):
     z.grad = None
     loss = qat.distill_loss(z, tv.reshape(3, 4, 6), ti.reshape(3, 4, 6), w.reshape(3, 4))
     loss.sum().backward()
-    loss2, want = Q.quads_topk_distill_grad(z0, tv, ti, w)
+    loss2, stats = Q.quads_topk_distill(z0, tv, ti, w)
+    want = Q.quads_topk_distill_backward(z0, tv, ti, stats, one, w)
     assert torch.equal(loss.reshape(-1), loss2) and torch.equal(z.grad.reshape(12, 999), want)
 
 

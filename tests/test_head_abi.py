@@ -26,7 +26,7 @@ def test_library_exports_every_declared_symbol():
     assert names == {"quads_moe_w4a16_gemv", "quads_moe_w4a16_gemv_ws", "quads_token_logprob",
                      "quads_token_logprob_ws", "quads_token_logprob_backward",
                      "quads_topk_distill", "quads_topk_distill_ws", "quads_topk_distill_backward",
-                     "quads_topk_distill_grad"}
+                     "quads_topk_distill_grad", "quads_topk_distill_grad_ws"}
     lib = Q.lib()
     assert all(hasattr(lib, n) for n in names)
     assert int(re.search(r"#define QUADS_TOP_MAX (\d+)", src).group(1)) == Q.TOP_MAX
@@ -89,7 +89,7 @@ def test_logprob_validation():
 def test_distill_validation():
     lib = Q.lib()
     f, b, c = lib.quads_topk_distill, lib.quads_topk_distill_backward, lib.quads_topk_distill_grad
-    ws = lib.quads_topk_distill_ws(4, 1000, 8)
+    ws = lib.quads_topk_distill_ws(4, 1000, 8) + lib.quads_topk_distill_grad_ws(4, 1000, 8)
 
     def every(z=FAKE, dt=0, t=4, v=1000, ld=1000, tv=FAKE, ti=FAKE, k=8, w=FAKE, it=1.0, rn=1,
               out=FAKE, dz=FAKE):
@@ -106,6 +106,12 @@ def test_distill_validation():
     big = lib.quads_topk_distill_ws(1, 1 << 20, 8)
     if big:
         assert f(FAKE, 0, 1, 1 << 20, 1 << 20, FAKE, FAKE, 8, None, 1.0, 1, FAKE, FAKE, FAKE,
+                 big - 1, None) == -3
+    big = lib.quads_topk_distill_grad_ws(1, 1 << 20, 8)
+    assert lib.quads_topk_distill_grad_ws(1, 1000, 8) == 0
+    assert lib.quads_topk_distill_grad_ws(64, 1 << 20, 8) == 0
+    if big:
+        assert c(FAKE, 0, 1, 1 << 20, 1 << 20, FAKE, FAKE, 8, None, 1.0, 1, FAKE, FAKE, FAKE,
                  big - 1, None) == -3
         assert c(FAKE, 0, 1, 1 << 20, 1 << 20, FAKE, FAKE, 8, None, 1.0, 1, FAKE, FAKE, None,
                  big, None) == -3
