@@ -477,7 +477,7 @@ inline bool whole_rows(int64_t T, int64_t V, int dtype) {
 template <int kBf16>
 void launch_loss(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, float it,
                  float* loss, float* stats, void* ws, hipStream_t st) {
-    const int parts = row_parts(T, V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32);
+    const int parts = row_parts(T, V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32, kWhole);
     hipLaunchKernelGGL(k_distill_loss<kBf16>, dim3((unsigned)(T * parts)), dim3(kThreads), 0, st, z,
                        V, ld, parts, l, it, loss, stats, (float4*)ws);
     if (parts > 1)
@@ -512,7 +512,7 @@ void launch_row(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, 
 
 // The parts' statistics.
 inline size_t parts_ws(int64_t T, int64_t V) {
-    const int parts = row_parts(T, V, QUADS_OUT_F32);
+    const int parts = row_parts(T, V, QUADS_OUT_F32, kWhole);
     return parts > 1 ? (size_t)T * parts * 16 : 0;
 }
 

@@ -509,7 +509,8 @@ using namespace quads;
 // Statistics and candidates of the parts, as many as either type is split into.
 extern "C" size_t quads_token_logprob_ws(int64_t T, int64_t V, int32_t topk) {
     if (T < 1 || V < 1 || topk < 0) return 0;
-    const int parts = head::row_parts(T, V, QUADS_OUT_F32);
+    const int parts =
+        head::row_parts(T, V, QUADS_OUT_F32, topk > 0 ? head::kWholeTop : head::kWhole);
     return parts > 1 ? (size_t)T * parts * (16 + 8 * (size_t)topk) : 0;
 }
 
@@ -527,7 +528,7 @@ extern "C" int quads_token_logprob(const void* logits, int dtype, int64_t T, int
     if (topk > 0 && (!ok_ptr4(top_logp) || !ok_ptr4(top_id))) return QUADS_EINVAL;
     const size_t need = quads_token_logprob_ws(T, V, topk);
     if (ws_bytes < need || (need > 0 && !ok_ptr(ws))) return QUADS_EWORKSPACE;
-    const int parts = head::row_parts(T, V, dtype);
+    const int parts = head::row_parts(T, V, dtype, topk > 0 ? head::kWholeTop : head::kWhole);
     const head::Out o{ids, inv_temp, (int)topk, logp, entropy, stats, top_logp, top_id};
     const head::Parts p{(float4*)ws, (uint64_t*)((char*)ws + 16 * T * parts)};
     if (dtype == QUADS_OUT_BF16)
