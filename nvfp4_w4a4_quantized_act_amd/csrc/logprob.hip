@@ -196,10 +196,11 @@ __device__ __forceinline__ void finish(const Out& o, const Row<kBf16>& r, int64_
 // number.  The candidates are sorted once, at the end.  Where there were more
 // than there is room for (equal or rising entries) the part is read again,
 // 256 entries at a time, the candidates cut to the topk largest in between.
-template <int kBf16, bool kEntropy, bool kTop>
+template <int kBf16, bool kEntropy, bool kTop, int kVecs>
 __global__ __launch_bounds__(kThreads) void k_logprob(const void* z, int64_t V, int64_t ld,
                                                       int parts, Out o, Parts p) {
     constexpr int kPer = Row<kBf16>::kPer;
+    constexpr int kChunk = kThreads * kVecs;
     __shared__ Stat s_stat[kThreads / 64];
     __shared__ Cand c;
     const int64_t t = blockIdx.x / (unsigned)parts;
@@ -477,28 +478,43 @@ __global__ __launch_bounds__(kThreads) void k_logprob_bwd(const void* z, int64_t
     }
 }
 
+// Rows of one work-group each that leave the GPU half empty and are longer than
+// two chunks wait for each chunk's loads: their sums take four times the
+// vectors at once (in us, calls in turn, 4 / 16 vectors: 1 x 32768 fp32 top 20
+// 17.4 / 15.5, 400 x 30000 bf16 19.2 / 16.2, 800 x 30000 fp32 28.5 / 30.6; waited
+// for, 4 x 3000 bf16 29 / 34).
+constexpr int kVecsFew = 16;
+template <int kBf16>
+inline bool few_rows(int64_t T, int64_t V, int parts) {
+    return parts == 1 && T <= 512 && V > 2 * kChunk * (int64_t)Row<kBf16>::kPer;
+}
+
+template <int kBf16, bool kEntropy, bool kTop>
+void launch_rows(const void* z, int64_t T, int64_t V, int64_t ld, int parts, const Out& o,
+                 const Parts& p, hipStream_t st) {
+    const dim3 grid((unsigned)(T * parts)), block(kThreads);
+    if (few_rows<kBf16>(T, V, parts))
+        hipLaunchKernelGGL((k_logprob<kBf16, kEntropy, kTop, kVecsFew>), grid, block, 0, st, z, V,
+                           ld, parts, o, p);
+    else
+        hipLaunchKernelGGL((k_logprob<kBf16, kEntropy, kTop, kVecs>), grid, block, 0, st, z, V, ld,
+                           parts, o, p);
+}
+
 template <int kBf16>
 void launch_forward(const void* z, int64_t T, int64_t V, int64_t ld, int parts, const Out& o,
                     const Parts& p, hipStream_t st) {
-    const dim3 grid((unsigned)(T * parts)), block(kThreads);
-    if (o.topk > 0) {
-        if (o.entropy)
-            hipLaunchKernelGGL((k_logprob<kBf16, true, true>), grid, block, 0, st, z, V, ld, parts,
-                               o, p);
-        else
-            hipLaunchKernelGGL((k_logprob<kBf16, false, true>), grid, block, 0, st, z, V, ld,
-                               parts, o, p);
-    } else {
-        if (o.entropy)
-            hipLaunchKernelGGL((k_logprob<kBf16, true, false>), grid, block, 0, st, z, V, ld,
-                               parts, o, p);
-        else
-            hipLaunchKernelGGL((k_logprob<kBf16, false, false>), grid, block, 0, st, z, V, ld,
-                               parts, o, p);
-    }
+    if (o.topk > 0 && o.entropy)
+        launch_rows<kBf16, true, true>(z, T, V, ld, parts, o, p, st);
+    else if (o.topk > 0)
+        launch_rows<kBf16, false, true>(z, T, V, ld, parts, o, p, st);
+    else if (o.entropy)
+        launch_rows<kBf16, true, false>(z, T, V, ld, parts, o, p, st);
+    else
+        launch_rows<kBf16, false, false>(z, T, V, ld, parts, o, p, st);
     if (parts > 1)
-        hipLaunchKernelGGL((k_merge<kBf16>), dim3((unsigned)T), block, 0, st, z, V, ld, parts, o,
-                           p);
+        hipLaunchKernelGGL((k_merge<kBf16>), dim3((unsigned)T), dim3(kThreads), 0, st, z, V, ld,
+                           parts, o, p);
 }
 
 }  // namespace head
