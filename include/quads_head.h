@@ -55,7 +55,7 @@ extern "C" {
  *              quads_moe_w4a4_gemm (offsets may be NULL when E == 1)
  * Any number of rows is computed, with one read of an expert's weights per 16
  * or 32 of its rows: larger batches belong to a GEMM.
- * The error is below (176 + K / 1024) 2^-24 sum |x w| per output element plus
+ * The error is below (176 + K / 512) 2^-24 sum |x w| per output element plus
  * the rounding to bf16, and 2^-28 times the largest |x| of a row's 512-channel
  * block times sum |w| where a block spans more than 28 binary orders.
  * Workspace: quads_moe_w4a16_gemv_ws bytes (0: NULL is allowed).

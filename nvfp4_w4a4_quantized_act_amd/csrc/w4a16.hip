@@ -476,9 +476,9 @@ int launch(Args g, hipStream_t st) {
 // 4096 17.6 / 38.  64 rows were never better than both.
 template <int kEpi>
 int dispatch(const Args& g, hipStream_t st) {
-    const int64_t bytes = (int64_t)g.E * g.N * g.K / 16 * 9;
+    const double bytes = 0.5625 * g.E * g.N * g.K;
     const bool many = g.offsets ? g.rows / g.E >= 16 : g.rows > 16;
-    if (many && g.K <= 2048 && bytes > ((int64_t)32 << 20)) return launch<kEpi, 2>(g, st);
+    if (many && g.K <= 2048 && bytes > 32.0 * (1 << 20)) return launch<kEpi, 2>(g, st);
     return launch<kEpi, 1>(g, st);
 }
 

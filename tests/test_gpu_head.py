@@ -578,6 +578,38 @@ def test_other_stream(Q):
     assert all(torch.equal(got[k], want[k]) for k in want)
 
 
+def test_two_streams_at_once(Q):
+    """Calls that overlap in time (each with a workspace of its own) do not meet."""
+    zs = [make(40, 90001, "f32", seed=s)[0] for s in (3, 4)]
+    ids = torch.zeros(40, dtype=torch.int32, device=DEV)
+    want = [Q.quads_token_logprob(z, ids, 1.0, 30) for z in zs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [None, None]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = Q.quads_token_logprob(zs[i], ids, 1.0, 30)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(a[k], b[k]) for k in b)
+
+
+def test_bit_patterns(Q):
+    """bf16 as int16 or uint16 bits: the same results, gradients in the same type."""
+    z, zr = make(6, 700, "bf16", seed=3)
+    ids = torch.from_numpy(tokens(zr, 1)).to(DEV)
+    one = torch.ones(6, device=DEV)
+    want = Q.quads_token_logprob(z, ids, 1.0, 4)
+    dz = Q.quads_token_logprob_backward(z, ids, want["stats"], want["entropy"], one, one)
+    for dt in (torch.int16, torch.uint16):
+        got = Q.quads_token_logprob(z.view(dt), ids, 1.0, 4)
+        assert all(torch.equal(got[k], want[k]) for k in want)
+        d = Q.quads_token_logprob_backward(z.view(dt), ids, want["stats"], want["entropy"], one,
+                                           one)
+        assert d.dtype == dt and torch.equal(d.view(torch.int16), dz.view(torch.int16))
+
+
 @pytest.mark.parametrize("t,v", [(3, 70001), (300, 5000)])
 def test_graph_replays(Q, t, v):
     """Captured forward, backward and distillation, replayed on new inputs with eager work

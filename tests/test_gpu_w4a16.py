@@ -8,6 +8,8 @@ rounding, is rounded at most 128 + K / 1024 times, sums over the parts of K at
 most 16 times more, and the tensor scale once; 16 are left for an activation
 far below its row's largest.  Every rounding is at most 2^-24 of sum |x w|:
   |err| <= (176 + K / 1024) 2^-24 sum |x w|, plus half a step of the output.
+Chains of 512 channels and one addition per chain stay below that up to K =
+114688 (64 + K / 512 + 9 <= 176 + K / 1024).
 SwiGLU: |silu'| < 1.1, the hardware exponential and reciprocal to 2^-21."""
 
 import numpy as np
@@ -91,7 +93,9 @@ def check(Q, x, w, offsets=None, row_token=None, swiglu=False, bf16=False, out=N
 @pytest.mark.parametrize("rows,k,n", [(1, 16, 1), (1, 256, 128), (2, 48, 33), (3, 272, 1003),
                                       (5, 1040, 130), (16, 2048, 257), (17, 512, 64),
                                       (33, 1536, 96), (64, 4096, 320), (130, 144, 40),
-                                      (1, 8208, 70), (7, 2064, 4099)])
+                                      (1, 8208, 70), (7, 2064, 4099), (16, 8192, 48),
+                                      (3, 70000, 20), (40, 2048, 33000), (31, 1040, 60001),
+                                      (15, 4096, 600), (700, 64, 24)])
 def test_dense(Q, rows, k, n, bf16):
     check(Q, acts(rows + k, rows, k), codes(n, 1, n, k), bf16=bf16)
 
@@ -106,7 +110,8 @@ def test_dense_swiglu(Q, rows, k, n):
 @pytest.mark.parametrize("swiglu", [False, True])
 @pytest.mark.parametrize("t,e,topk,k,n", [(1, 4, 2, 256, 128), (9, 5, 2, 48, 62),
                                           (64, 128, 8, 512, 96), (3, 300, 9, 128, 34),
-                                          (40, 2, 1, 1040, 100), (2, 4096, 4, 32, 16)])
+                                          (40, 2, 1, 1040, 100), (2, 4096, 4, 32, 16),
+                                          (300, 64, 8, 1024, 1100), (600, 3, 2, 80, 50)])
 def test_experts(Q, t, e, topk, k, n, swiglu):
     """Experts without rows, with one, with more than a tile of them; tokens out of order."""
     rng = np.random.default_rng(t + e)
