@@ -125,16 +125,35 @@ __device__ __forceinline__ void stat_raise(Stat& a, float m, float c) {
     a.m = m;
 }
 
-// Sum over the 64 lanes of a wave, the same bits in every lane.
+// Sum and maximum over the 64 lanes of a wave (every lane active), the same bits
+// in every lane: DPP moves within the rows of 16 lanes and across them, then
+// one lane's value read as a scalar (lane shuffles, through LDS, took ten
+// times as long: a row of a loss has ten such reductions one after another).
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ float dpp_move(float old, float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+        (int)__float_as_uint(old), (int)__float_as_uint(v), kCtrl, kRowMask, 0xF, false));
+}
+__device__ __forceinline__ float last_lane(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+    v += dpp_move<0x111, 0xF>(0.0f, v);        // row_shr:1
+    v += dpp_move<0x112, 0xF>(0.0f, v);        // row_shr:2
+    v += dpp_move<0x114, 0xF>(0.0f, v);        // row_shr:4
+    v += dpp_move<0x118, 0xF>(0.0f, v);        // row_shr:8
+    v += dpp_move<0x142, 0xA>(0.0f, v);        // row_bcast:15 into rows 1 and 3
+    v += dpp_move<0x143, 0xC>(0.0f, v);        // row_bcast:31 into rows 2 and 3
+    return last_lane(v);
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-    return v;
+    v = fmaxf(v, dpp_move<0x111, 0xF>(v, v));
+    v = fmaxf(v, dpp_move<0x112, 0xF>(v, v));
+    v = fmaxf(v, dpp_move<0x114, 0xF>(v, v));
+    v = fmaxf(v, dpp_move<0x118, 0xF>(v, v));
+    v = fmaxf(v, dpp_move<0x142, 0xA>(v, v));
+    v = fmaxf(v, dpp_move<0x143, 0xC>(v, v));
+    return last_lane(v);
 }
 __device__ __forceinline__ Stat wave_stat(Stat a, float c) {
     stat_raise(a, wave_max(a.m), c);

@@ -65,6 +65,7 @@ constexpr int kBlk = 512;                      // channels per block
 constexpr int kStage = 4;                      // activation loads in flight per wave
 constexpr int kLds = 160 << 10;                // LDS bytes of a CU
 constexpr int kCus = 256;
+constexpr int kHeld = 4;                       // experts' offsets per lane kept in registers
 
 struct Args {
     const uint16_t* x; const int32_t* row_token; int rows; int K;
@@ -74,6 +75,7 @@ struct Args {
     int kw;                                    // waves per slot
     int slabs;                                 // work-groups per unit of rows
     int steps;                                 // of the largest slot
+    int step;                                  // features per step
     int sb;                                    // blocks of activations in LDS at once
     int rcap;                                  // rows of LDS
 };
@@ -156,29 +158,60 @@ __global__ __launch_bounds__(kThreads, 4) void k_w4a16(Args g) {
     const int slab = (int)(blockIdx.x % (unsigned)g.slabs);
     const int rank = (int)(blockIdx.x / (unsigned)g.slabs);
 
-    // the unit of this rank: kRows rows of an expert, in expert order
+    // the unit of this rank: kRows rows of an expert, in expert order.  Lane l
+    // counts the units of experts l*per .. l*per + per - 1, a scan finds the
+    // lane, the lane finds the expert.  Up to kHeld experts a lane keeps the
+    // offsets in registers, loaded together: the weights wait for them.
     int e = 0, p0 = kRows * rank, cnt = g.rows - p0;
     if (g.offsets) {
         const int per = (g.E + 63) / 64;
         const int e0 = lane * per < g.E ? lane * per : g.E;
         const int e1 = e0 + per < g.E ? e0 + per : g.E;
+        int held[kHeld + 1];
+#pragma unroll
+        for (int i = 0; i <= kHeld; ++i) held[i] = g.offsets[e0 + i < g.E ? e0 + i : g.E];
         int na = 0;
-        for (int x = e0; x < e1; ++x) na += (g.offsets[x + 1] - g.offsets[x] + kRows - 1) / kRows;
+        if (per <= kHeld) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i)
+                na += e0 + i < e1 ? (held[i + 1] - held[i] + kRows - 1) / kRows : 0;
+        } else {
+            for (int x = e0; x < e1; ++x)
+                na += (g.offsets[x + 1] - g.offsets[x] + kRows - 1) / kRows;
+        }
         const int inc = wave_incl_add(na);
         if (rank >= __builtin_amdgcn_readlane(inc, 63)) return;
-        int found = -1, part = 0;
-        if (rank >= inc - na && rank < inc) {
-            int rr = rank - (inc - na);
-            for (int x = e0; x < e1; ++x) {
-                const int u = (g.offsets[x + 1] - g.offsets[x] + kRows - 1) / kRows;
-                if (rr < u) { found = x; part = rr; break; }
-                rr -= u;
+        int found = -1, from = 0, to = 0;
+        int rr = rank - (inc - na);
+        if (rr >= 0 && rank < inc) {
+            if (per <= kHeld) {
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) {
+                    const int u = e0 + i < e1 ? (held[i + 1] - held[i] + kRows - 1) / kRows : 0;
+                    if (found < 0 && rr < u) {
+                        found = e0 + i;
+                        from = held[i] + kRows * rr;
+                        to = held[i + 1];
+                    }
+                    rr -= u;
+                }
+            } else {
+                for (int x = e0; x < e1; ++x) {
+                    const int u = (g.offsets[x + 1] - g.offsets[x] + kRows - 1) / kRows;
+                    if (rr < u) {
+                        found = x;
+                        from = g.offsets[x] + kRows * rr;
+                        to = g.offsets[x + 1];
+                        break;
+                    }
+                    rr -= u;
+                }
             }
         }
         const int src = __ffsll(__ballot(found >= 0)) - 1;
         e = __builtin_amdgcn_readlane(found, src);
-        p0 = g.offsets[e] + kRows * __builtin_amdgcn_readlane(part, src);
-        cnt = g.offsets[e + 1] - p0;
+        p0 = __builtin_amdgcn_readlane(from, src);
+        cnt = __builtin_amdgcn_readlane(to, src) - p0;
     }
     if (cnt <= 0) return;
     const int nr = cnt < kRows ? cnt : kRows;
@@ -186,8 +219,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_w4a16(Args g) {
     int token = 0;
     if (lane < nr) token = g.row_token ? g.row_token[p0 + lane] : p0 + lane;
 
-    // the slot's output features [lo, hi), taken kStep at a time
-    constexpr int kStep = swiglu ? 16 : 32;
+    // the slot's output features [lo, hi), taken g.step at a time
     const int nout = swiglu ? g.N / 2 : g.N;
     const int wk = wave % g.kw;
     const int slots = kWaves / g.kw;
@@ -197,12 +229,11 @@ __global__ __launch_bounds__(kThreads, 4) void k_w4a16(Args g) {
     const int hi =
         __builtin_amdgcn_readfirstlane(min(nout, (int)(4 * (quads_n * (slot + 1) / all))));
     const int nblk = (g.K + kBlk - 1) / kBlk;
-    // each tile's first feature (of the weight rows), kStep rows further per
-    // step, and how many features up to hi there are from it on; the lane's
-    // offset from it
+    // each tile's first feature (of the weight rows), g.step rows further per
+    // step, and how many of its features there are; the lane's offset from it
     const uint8_t* nib[2];
     const uint8_t* sc[2];
-    int left[2];
+    int left[2], most[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const int f = lo + (swiglu ? 0 : 16 * q);
@@ -210,16 +241,17 @@ __global__ __launch_bounds__(kThreads, 4) void k_w4a16(Args g) {
         nib[q] = g.w_nib + row * (g.K / 2);
         sc[q] = g.w_scale + row * (g.K / kBlock);
         left[q] = hi - f;
+        most[q] = g.step - (swiglu ? 0 : 16 * q);
     }
     const uint32_t nib_off = (uint32_t)r * (g.K / 2) + 16 * h, sc_off = (uint32_t)r * (g.K / kBlock);
-    const int64_t nib_step = (int64_t)kStep * (g.K / 2), sc_step = (int64_t)kStep * (g.K / kBlock);
+    const int64_t nib_step = (int64_t)g.step * (g.K / 2), sc_step = (int64_t)g.step * (g.K / kBlock);
 
     uint4 code[2][4];
     u32x2 scale[2];
     auto load = [&](int b) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const bool ok = r < left[q] && b < nblk;
+            const bool ok = r < min(left[q], most[q]) && b < nblk;
             scale[q] = load_scales(sc[q], sc_off, b, h, g.K, ok);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -336,7 +368,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_w4a16(Args g) {
                     if (turn) {
                         nib[q] += nib_step;
                         sc[q] += sc_step;
-                        left[q] -= kStep;
+                        left[q] -= g.step;
                     }
                 load(turn ? wk : b + g.kw);
                 __builtin_amdgcn_sched_barrier(0);
@@ -373,20 +405,21 @@ __global__ __launch_bounds__(kThreads, 4) void k_w4a16(Args g) {
         }
 
         // lane (r, h) holds row 16 t + r of features 4 h .. 4 h + 3 of each tile
+        const int end = min(hi, lo + (st + 1) * g.step);
 #pragma unroll
         for (int t = 0; t < kRt; ++t) {
             const bool have = 16 * t + r < nr;
             const int64_t o = (int64_t)(p0 + 16 * t + r) * nout;
 #pragma unroll
             for (int q = 0; q < (swiglu ? 1 : 2); ++q) {
-                const int n = lo + st * kStep + 16 * q + 4 * h;
+                const int n = lo + st * g.step + 16 * q + 4 * h;
                 float y[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     y[u] = tot[q][t][u] * ts;
                     if (swiglu) y[u] = silu_mul(y[u], tot[1][t][u] * ts);
                 }
-                if (!have || n >= hi) continue;
+                if (!have || n >= end) continue;
                 if (g.out_bf16) {
                     uint16_t* a = (uint16_t*)g.out + o + n;
                     const uint32_t p01 = v2::pk_bf16(y[0], y[1]), p23 = v2::pk_bf16(y[2], y[3]);
@@ -396,7 +429,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_w4a16(Args g) {
                         const uint32_t b4[4] = {p01, p01 >> 16, p23, p23 >> 16};
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            if (n + u < hi) a[u] = (uint16_t)b4[u];
+                            if (n + u < end) a[u] = (uint16_t)b4[u];
                     }
                 } else {
                     float* a = (float*)g.out + o + n;
@@ -405,7 +438,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_w4a16(Args g) {
                     } else {
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            if (n + u < hi) a[u] = y[u];
+                            if (n + u < end) a[u] = y[u];
                     }
                 }
             }
@@ -458,7 +491,9 @@ int launch(Args g, hipStream_t st) {
     if (slabs < 1) slabs = 1;
     g.slabs = (int)slabs;
     const int64_t quads_n = (nout + 3) / 4, share = (quads_n + slabs * slots - 1) / (slabs * slots);
+    // steps of equal size (multiples of 4 features)
     g.steps = (int)((4 * share + kStep - 1) / kStep);
+    g.step = (int)(4 * ((share + g.steps - 1) / g.steps));
     size_t bytes = (g.rcap * (16 + g.sb * row) + 15) & ~(size_t)15;
     if (g.kw > 1) bytes += (kWaves - 1) * part;
     hipLaunchKernelGGL((k_w4a16<kEpi, kRt>), dim3((unsigned)(slabs * units)), dim3(kThreads),
