@@ -35,7 +35,7 @@ __device__ __forceinline__ int key_index(uint64_t k) { return (int)(0xFFFFFFFFu 
 constexpr int kCand = 1024;                    // candidates kept at once
 
 struct __align__(16) Cand {
-    uint64_t key[kCand];
+    uint64_t key[kCand + 8];
     uint16_t top[2][kThreads];                 // upper halves of the threads' maxima's keys
     int n;
 };
@@ -46,28 +46,67 @@ __device__ __forceinline__ float next_up(float x) {
     return __uint_as_float((int32_t)b >= 0 ? b + 1u : b - 1u);
 }
 
-// A value that at least k of the work-group's values (key halves in `top`)
-// reach: the k-th largest half, rounded down.  Every wave finds it by itself,
-// one bit of the half at a time, counting with ballots.
-__device__ __forceinline__ float kth_bound(const uint16_t* top, int k) {
-    const uint2 w = reinterpret_cast<const uint2*>(top)[threadIdx.x & 63];
-    const uint32_t h[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
+// The k-th largest of the wave's values h (halves of keys, kPerLane a lane), 0
+// if there are fewer: one bit at a time, counted with ballots.
+template <int kPerLane>
+__device__ __forceinline__ uint32_t kth_half(const uint32_t* h, int k) {
     uint32_t t = 0;
 #pragma unroll
     for (int b = 15; b >= 0; --b) {
         const uint32_t x = t | (1u << b);
         int n = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) n += __popcll(__ballot(h[i] >= x));
+        for (int i = 0; i < kPerLane; ++i) n += __popcll(__ballot(h[i] >= x));
         if (n >= k) t = x;
     }
+    return t;
+}
+
+// A value that at least k of the work-group's values (key halves in `top`)
+// reach: the k-th largest half, rounded down.  Every wave finds it by itself.
+__device__ __forceinline__ float kth_bound(const uint16_t* top, int k) {
+    const uint2 w = reinterpret_cast<const uint2*>(top)[threadIdx.x & 63];
+    const uint32_t h[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
+    const uint32_t t = kth_half<4>(h, k);
     // the lowest value of that half (none below -inf)
     return t <= 0x007Fu ? -INFINITY : key_value((uint64_t)(t << 16) << 32);
 }
 
+// Drops the candidates whose half is below the k-th largest one.
+template <int kPerLane>
+__device__ __forceinline__ uint64_t kth_key(const Cand& c, int n, int k) {
+    uint32_t h[kPerLane];
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+        const int at = (int)(threadIdx.x & 63) + 64 * i;
+        h[i] = at < n ? (uint32_t)(c.key[at] >> 48) : 0;
+    }
+    return (uint64_t)kth_half<kPerLane>(h, k) << 48;
+}
+__device__ __forceinline__ int drop_low(Cand& c, int n, int k) {
+    uint64_t mine[kCand / kThreads];
+    __syncthreads();
+    const uint64_t low = n <= kThreads ? kth_key<4>(c, n, k) : kth_key<kCand / 64>(c, n, k);
+#pragma unroll
+    for (int i = 0; i < kCand / kThreads; ++i) {
+        const int at = threadIdx.x + i * kThreads;
+        mine[i] = at < n ? c.key[at] : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) c.n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kCand / kThreads; ++i)
+        if (mine[i] >= low && mine[i] != 0) c.key[atomicAdd(&c.n, 1)] = mine[i];
+    __syncthreads();
+    return c.n;
+}
+
 // Sorts the n candidates and keeps the k largest (c.n is set; barriers on
-// both sides).  Each entry's place is the number of larger ones.
+// both sides).  Each entry's place is the number of larger ones, eight read
+// at a time; candidates well beyond k are dropped before.
 __device__ __forceinline__ void keep_top(Cand& c, int n, int k) {
+    if (n > k + k / 2 + 16) n = drop_low(c, n, k);
     uint64_t mine[kCand / kThreads];
     int place[kCand / kThreads];
     __syncthreads();
@@ -77,13 +116,19 @@ __device__ __forceinline__ void keep_top(Cand& c, int n, int k) {
         mine[i] = at < n ? c.key[at] : 0;
         place[i] = 0;
     }
-    if (n <= kThreads) {
-        for (int j = 0; j < n; ++j) place[0] += c.key[j] > mine[0] ? 1 : 0;
-    } else {
-        for (int j = 0; j < n; ++j) {
-            const uint64_t x = c.key[j];
+    if (threadIdx.x < 8) c.key[n + threadIdx.x] = 0;       // smaller than any
+    __syncthreads();
+    for (int j = 0; j < n; j += 8) {
+        uint64_t x[8];
 #pragma unroll
-            for (int i = 0; i < kCand / kThreads; ++i) place[i] += x > mine[i] ? 1 : 0;
+        for (int b = 0; b < 8; ++b) x[b] = c.key[j + b];
+#pragma unroll
+        for (int b = 0; b < 8; ++b) place[0] += x[b] > mine[0] ? 1 : 0;
+        if (n > kThreads) {
+#pragma unroll
+            for (int i = 1; i < kCand / kThreads; ++i)
+#pragma unroll
+                for (int b = 0; b < 8; ++b) place[i] += x[b] > mine[i] ? 1 : 0;
         }
     }
     __syncthreads();
@@ -92,25 +137,6 @@ __device__ __forceinline__ void keep_top(Cand& c, int n, int k) {
         if (mine[i] != 0 && place[i] < k) c.key[place[i]] = mine[i];
     if (threadIdx.x == 0) c.n = n < k ? n : k;
     __syncthreads();
-}
-
-// Drops the candidates below `bound` (at least k are not).
-__device__ __forceinline__ int drop_below(Cand& c, int n, float bound) {
-    uint64_t mine[kCand / kThreads];
-    const uint64_t low = (uint64_t)value_key(bound) << 32;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kCand / kThreads; ++i) {
-        const int at = threadIdx.x + i * kThreads;
-        mine[i] = at < n ? c.key[at] : 0;
-    }
-    if (threadIdx.x == 0) c.n = 0;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kCand / kThreads; ++i)
-        if (mine[i] >= low && mine[i] != 0) c.key[atomicAdd(&c.n, 1)] = mine[i];
-    __syncthreads();
-    return c.n;
 }
 
 // ----------------------------------------------------------------- forward --
@@ -296,7 +322,6 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const void* z, int64_t V, 
         }
     }
 
-    const float top = a.m;
     a = group_stat<kThreads / 64>(a, cl, s_stat);
     int n = 0;
     if (kTop) {
@@ -333,10 +358,6 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const void* z, int64_t V, 
                     __syncthreads();
                 }
             }
-        } else if (n > topk + topk / 2 + 16) {
-            c.top[fresh ^ 1][threadIdx.x] = (uint16_t)(value_key(top) >> 16);
-            __syncthreads();
-            n = drop_below(c, n, kth_bound(c.top[fresh ^ 1], topk));
         }
         keep_top(c, n, topk);
         n = c.n;
