@@ -28,7 +28,8 @@ struct List {
 // A lane's two entries of a row's list: q = 0 and ln q = -inf where there is
 // none; Q over the wave.
 struct Teacher {
-    float q[2], lq[2], all;
+    double lq[2];
+    float q[2], all;
     int id[2];
 };
 struct Entries {
@@ -47,34 +48,32 @@ __device__ __forceinline__ Entries load_entries(const List& l, int64_t t) {
 }
 __device__ __forceinline__ Teacher teacher(const Entries& x, int V, float it, int renorm) {
     Teacher r;
+    float y[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         const bool have = x.id[b] >= 0 && x.id[b] < V;
         r.id[b] = have ? x.id[b] : -1;
-        r.lq[b] = have ? (renorm ? it * x.val[b] : x.val[b]) : -INFINITY;
+        r.lq[b] = have ? (renorm ? (double)it * (double)x.val[b] : (double)x.val[b]) : -INFINITY;
+        y[b] = (float)r.lq[b];
     }
     if (renorm) {
-        const float m = stat_base(wave_max(fmaxf(r.lq[0], r.lq[1])));
-        const float s = wave_sum(expf(r.lq[0] - m) + expf(r.lq[1] - m));
-        const float ls = logf(s);
+        const float m = stat_base(wave_max(fmaxf(y[0], y[1])));
 #pragma unroll
-        for (int b = 0; b < 2; ++b)            // an empty list has s = 0: nothing to normalise
-            r.lq[b] = r.id[b] < 0 || s == 0.0f ? -INFINITY : r.lq[b] - m - ls;
+        for (int b = 0; b < 2; ++b) r.q[b] = expf((float)(r.lq[b] - (double)m));
+        const float s = wave_sum(r.q[0] + r.q[1]);
+        const double ls = (double)m + ln_wide(s);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {          // an empty list has s = 0: nothing to normalise
+            const bool none = r.id[b] < 0 || s == 0.0f;
+            r.lq[b] = none ? -INFINITY : r.lq[b] - ls;
+            r.q[b] = none ? 0.0f : r.q[b] / s;
+        }
+    } else {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) r.q[b] = expf(y[b]);
     }
-#pragma unroll
-    for (int b = 0; b < 2; ++b) r.q[b] = expf(r.lq[b]);
     r.all = wave_sum(r.q[0] + r.q[1]);
     return r;
-}
-
-// sum_i q_i (ln q_i - ln p_i) over the wave, z the logits at the entries' ids.
-__device__ __forceinline__ float cross(const Teacher& a, const float z[2], float m, float ls,
-                                       float it) {
-    float y = 0.0f;
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-        if (!(a.q[b] == 0.0f)) y += a.q[b] * (a.lq[b] - ln_p(z[b], m, ls, it));
-    return wave_sum(y);
 }
 
 // The logits at a lane's entries (-inf where there is none).
@@ -84,34 +83,61 @@ __device__ __forceinline__ void gather(const Row<kBf16>& r, const Teacher& a, fl
     for (int b = 0; b < 2; ++b) z[b] = a.id[b] >= 0 ? r.entry(a.id[b]) : -INFINITY;
 }
 
-// Gradients at the list's ids: by (Q p - q), q summed over the entries with
-// the same id in the list's order, so that every one of them has the same
-// value.  One wave; the list and the gradients stay in LDS until the dense
-// ones are written.
+// A row's list, the logits at its ids and their gradients, in LDS while the row
+// is worked on (one wave writes and reads it; `all` is for every wave).
 struct Parked {
+    double lq[QUADS_TOP_MAX];
     int id[QUADS_TOP_MAX];
-    float q[QUADS_TOP_MAX], g[QUADS_TOP_MAX];
+    float q[QUADS_TOP_MAX], z[QUADS_TOP_MAX], g[QUADS_TOP_MAX];
+    float all;
 };
-__device__ __forceinline__ void at_entries(const Teacher& a, const float z[2], int topk, float by,
-                                           float m, float ls, float it, Parked& p) {
-    const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void park(const Teacher& a, const float z[2], Parked& p) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        p.id[lane + 64 * b] = a.id[b];
-        p.q[lane + 64 * b] = a.q[b];
+        const int i = (threadIdx.x & 63) + 64 * b;
+        p.lq[i] = a.lq[b];
+        p.id[i] = a.id[b];
+        p.q[i] = a.q[b];
+        p.z[i] = z[b];
     }
+    if ((threadIdx.x & 63) == 0) p.all = a.all;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// sum_i q_i (ln q_i - ln p_i) over the wave.
+__device__ __forceinline__ float cross(const Parked& p, float m, double ls, float it) {
+    float y = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int i = (threadIdx.x & 63) + 64 * b;
+        const float q = p.q[i];
+        if (!(q == 0.0f)) y += q * (float)(p.lq[i] - ln_p(p.z[i], m, ls, it));
+    }
+    return wave_sum(y);
+}
+
+// Probabilities of a row are 2^((z - base) cl - l2) inv: l2 = log2 of the sum
+// where only the stats are known, inv its reciprocal where it is at hand (then
+// l2 = 0: the logarithm's rounding does not enter the gradient).
+//
+// Gradients at the list's ids: by (Q p - q), q summed over the entries with
+// the same id in the list's order, so that every one of them has the same
+// value.  One wave; they stay in LDS until the dense ones are written.
+__device__ __forceinline__ void at_entries(Parked& p, int topk, float by, bool none, float base,
+                                           float cl, float l2, float inv) {
+    const int lane = threadIdx.x & 63;
+    const int id[2] = {p.id[lane], p.id[lane + 64]};
     float q[2] = {0.0f, 0.0f};
     for (int i = 0; i < topk; ++i)
 #pragma unroll
-        for (int b = 0; b < 2; ++b) q[b] += p.id[i] == a.id[b] ? p.q[i] : 0.0f;
-    const bool none = m == -INFINITY && ls == ls;
+        for (int b = 0; b < 2; ++b) q[b] += p.id[i] == id[b] ? p.q[i] : 0.0f;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        const float d = __builtin_fmaf(z[b] - stat_base(m), it * kLog2e, -ls * kLog2e);
-        p.g[lane + 64 * b] =
-            none ? 0.0f : by * __builtin_fmaf(a.all, __builtin_amdgcn_exp2f(d), -q[b]);
+        const int i = lane + 64 * b;
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(p.z[i] - base, cl, -l2)) * inv;
+        p.g[i] = none ? 0.0f : by * __builtin_fmaf(p.all, x, -q[b]);
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 template <int kBf16>
 __device__ __forceinline__ void patch(const Row<kBf16>& r, char* at, const Parked& p, int v0,
@@ -127,7 +153,7 @@ __device__ __forceinline__ void patch(const Row<kBf16>& r, char* at, const Parke
     }
 }
 
-// One vector's gradient by Q p (by Q = a): p = 2^((z - base) cl - l2).
+// One vector's gradient by Q p, a = by Q inv.
 template <int kBf16>
 __device__ __forceinline__ uint4 dense(const uint4& q, float base, float cl, float l2, float a) {
     float g[8];
@@ -163,16 +189,17 @@ __device__ __forceinline__ void pin(uint4& q) {
 template <int kBf16>
 __device__ __forceinline__ void finish_loss(const Row<kBf16>& r, int64_t t, const Stat& a,
                                             const List& l, float w, float it, float* loss,
-                                            float* stats) {
+                                            float* stats, Parked& p) {
     const Teacher q = teacher(load_entries(l, t), r.V, it, l.renorm);
     float z[2];
     gather<kBf16>(r, q, z);
-    const float ls = log_sum(a);
-    const float y = cross(q, z, a.m, ls, it);
+    park(q, z, p);
+    const double ls = log_sum(a);
+    const float y = cross(p, a.m, ls, it);
     if ((threadIdx.x & 63) == 0) {
         loss[t] = w * y;
         stats[2 * t] = a.m;
-        stats[2 * t + 1] = ls;
+        stats[2 * t + 1] = (float)ls;
     }
 }
 __device__ __forceinline__ void no_loss(int64_t t, float* loss, float* stats) {
@@ -187,6 +214,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_loss(const void* z, int64_
                                                            float* loss, float* stats,
                                                            float4* part_stat) {
     __shared__ Stat s_stat[kThreads / 64];
+    __shared__ Parked s_list;
     const int64_t t = blockIdx.x / (unsigned)parts;
     const int part = (int)(blockIdx.x % (unsigned)parts);
     const float w = l.weight ? l.weight[t] : 1.0f;
@@ -227,7 +255,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_loss(const void* z, int64_
     if (parts > 1) {
         if (threadIdx.x == 0) part_stat[blockIdx.x] = make_float4(a.m, a.s, 0.0f, 0.0f);
     } else if (threadIdx.x < 64) {
-        finish_loss<kBf16>(r, t, a, l, w, it, loss, stats);
+        finish_loss<kBf16>(r, t, a, l, w, it, loss, stats, s_list);
     }
 }
 
@@ -236,6 +264,7 @@ template <int kBf16>
 __global__ __launch_bounds__(64) void k_distill_join(const void* z, int64_t V, int64_t ld,
                                                      int parts, List l, float it, float* loss,
                                                      float* stats, const float4* part_stat) {
+    __shared__ Parked s_list;
     const int64_t t = blockIdx.x;
     const float w = l.weight ? l.weight[t] : 1.0f;
     if (w == 0.0f) {
@@ -248,7 +277,7 @@ __global__ __launch_bounds__(64) void k_distill_join(const void* z, int64_t V, i
         a = {q.x, q.y, q.z};
     }
     a = wave_stat(a, it * kLog2e);
-    finish_loss<kBf16>(Row<kBf16>(z, t, ld, V), t, a, l, w, it, loss, stats);
+    finish_loss<kBf16>(Row<kBf16>(z, t, ld, V), t, a, l, w, it, loss, stats, s_list);
 }
 
 template <int kBf16>
@@ -273,15 +302,17 @@ __global__ __launch_bounds__(kThreads) void k_distill_bwd(const void* z, int64_t
     const float m = stats[2 * t], ls = stats[2 * t + 1];
     const float by = w * it * (g ? g[t] : 1.0f);
     const Teacher q = teacher(load_entries(l, t), r.V, it, l.renorm);
+    const float base = stat_base(m), cl = it * kLog2e, l2 = ls * kLog2e;
     // the part's entries [v0, v1), their gradients parked before any store
     const int v0 = c0 ? r.index(c0 * kChunk, 0) : 0, v1 = r.index(c1 * kChunk, 0);
     if (threadIdx.x < 64) {
         float x[2];
         gather<kBf16>(r, q, x);
-        at_entries(q, x, l.topk, by, m, ls, it, s_list);
+        park(q, x, s_list);
+        at_entries(s_list, l.topk, by, m == -INFINITY && ls == ls, base, cl, l2, 1.0f);
     }
     __syncthreads();
-    const float base = stat_base(m), cl = it * kLog2e, l2 = ls * kLog2e, a = by * q.all;
+    const float a = by * q.all;
     for (int ch = c0; ch < c1; ++ch) {
         uint4 x[kVecs];
 #pragma unroll
@@ -378,10 +409,13 @@ __global__ __launch_bounds__(kThr, 4) void k_distill_row(const void* z, int64_t 
         const bool more = tn != t && wn != 0.0f;
         const int n = count(r), beyond = w != 0.0f ? n : 0, nn = more ? count(rn) : 0;
 
-        Teacher q = teacher(e, r.V, it, l.renorm);
-        if (w == 0.0f) q.id[0] = q.id[1] = -1;
-        float zq[2];
-        if (tid < 64) gather<kBf16>(r, q, zq);
+        if (tid < 64) {
+            Teacher q = teacher(e, r.V, it, l.renorm);
+            if (w == 0.0f) q.id[0] = q.id[1] = -1;
+            float zq[2];
+            gather<kBf16>(r, q, zq);
+            park(q, zq, s_list);
+        }
         // log-sum: the vectors in registers, then those beyond them
         Stat a = {vec_max<kBf16>(edge, -INFINITY), 0.0f, 0.0f};
 #pragma unroll
@@ -405,28 +439,29 @@ __global__ __launch_bounds__(kThr, 4) void k_distill_row(const void* z, int64_t 
             a.s = vec_sum<kBf16>(y, stat_base(a.m), cl, a.s);
         }
         a = group_stat<kThr / 64>(a, cl, s_stat);
-        const float ls = log_sum(a), by = w * it;
+        const bool none = a.m == -INFINITY && a.s == 0.0f;
+        base = stat_base(a.m);
+        const float by = w * it, inv = none ? 0.0f : 1.0f / a.s;
         if (tid < 64) {
-            const float y = cross(q, zq, a.m, ls, it);
+            const float y = cross(s_list, a.m, log_sum(a), it);
             if (tid == 0) loss[t] = w == 0.0f ? 0.0f : w * y;
-            at_entries(q, zq, l.topk, by, a.m, ls, it, s_list);
+            at_entries(s_list, l.topk, by, none, base, cl, 0.0f, inv);
         }
         // gradient
-        base = stat_base(a.m);
-        const float l2 = ls * kLog2e, f = w == 0.0f ? 0.0f : by * q.all;
+        const float f = w == 0.0f ? 0.0f : by * s_list.all * inv;
         for (int i = kNv * kThr + tid; kLong && i < n; i += kThr) {
             const int j = first(r) + i;
             uint4 y = masked;
             if (i < beyond) y = *r.vec(j);
-            st_stream16(out + 16 * (int64_t)j, dense<kBf16>(y, base, cl, l2, f));
+            st_stream16(out + 16 * (int64_t)j, dense<kBf16>(y, base, cl, 0.0f, f));
         }
         const int j = edge_at(r);
-        if (j >= 0) store_part<kBf16>(r, out, j, dense<kBf16>(edge, base, cl, l2, f));
+        if (j >= 0) store_part<kBf16>(r, out, j, dense<kBf16>(edge, base, cl, 0.0f, f));
         load_edge(rn, more);
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
             if (i * kThr < n) {
-                const uint4 y = dense<kBf16>(x[i], base, cl, l2, f);
+                const uint4 y = dense<kBf16>(x[i], base, cl, 0.0f, f);
                 char* to = out + 16 * (int64_t)(first(r) + i * kThr);
                 if (i * kThr + tid < n) {
                     if (kLong) st_stream16(to + lane16, y);

@@ -173,13 +173,22 @@ __device__ __forceinline__ Stat group_stat(Stat a, float c, Stat* s_stat) {
     return wave_stat(b, c);
 }
 
-// ln sum exp(it (z - m)): 0 for a row without an unmasked entry.
-__device__ __forceinline__ float log_sum(const Stat& a) {
-    return a.m == -INFINITY && a.s == 0.0f ? 0.0f : logf(a.s);
+// ln s to about 2^-24, however large it is: the exponent and the fp32 logarithm
+// of the mantissa, added in fp64 (an fp32 logarithm of 2^15 is off by four bits
+// of that, and fp64's own takes 30 registers that the kernels do not have).
+__device__ __forceinline__ double ln_wide(float s) {
+    const double e = (double)__builtin_amdgcn_frexp_expf(s);
+    return 0.69314718055994531 * (e + (double)__builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(s)));
+}
+// ln sum exp(it (z - m)): 0 for a row without an unmasked entry.  In fp64, as is
+// what is taken from it, once or a few times per row: a log-probability or a
+// small loss is a difference of such numbers.
+__device__ __forceinline__ double log_sum(const Stat& a) {
+    return a.m == -INFINITY && a.s == 0.0f ? 0.0 : ln_wide(a.s);
 }
 // ln p of an entry: -inf where it is masked (unless the row holds NaN or +inf).
-__device__ __forceinline__ float ln_p(float z, float m, float ls, float it) {
-    return z == -INFINITY && ls == ls ? z : (z - m) * it - ls;
+__device__ __forceinline__ double ln_p(float z, float m, double ls, float it) {
+    return z == -INFINITY && ls == ls ? (double)z : ((double)z - (double)m) * (double)it - ls;
 }
 
 // ------------------------------------------------------------------ host --

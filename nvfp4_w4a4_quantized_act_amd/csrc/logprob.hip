@@ -177,13 +177,16 @@ __device__ __forceinline__ Token load_token(const Out& o, const Row<kBf16>& r, i
 template <int kBf16>
 __device__ __forceinline__ void finish(const Out& o, const Row<kBf16>& r, int64_t t, const Stat& a,
                                        const Token& k, uint64_t* key, int n) {
-    const float ls = log_sum(a);
+    const double ls = log_sum(a);
     if (threadIdx.x == 0) {
         o.stats[2 * t] = a.m;
-        o.stats[2 * t + 1] = ls;
+        o.stats[2 * t + 1] = (float)ls;
         if (o.entropy)
-            o.entropy[t] = a.m == -INFINITY && a.s == 0.0f ? 0.0f : ls - kLn2 * a.u / a.s;
-        if (o.ids) o.logp[t] = k.id >= 0 && k.id < r.V ? ln_p(k.z, a.m, ls, o.it) : 0.0f;
+            o.entropy[t] = a.m == -INFINITY && a.s == 0.0f
+                               ? 0.0f
+                               : (float)(ls - 0.69314718055994531 * (double)a.u / (double)a.s);
+        if (o.ids)
+            o.logp[t] = k.id >= 0 && k.id < r.V ? (float)ln_p(k.z, a.m, ls, o.it) : 0.0f;
     }
     if (o.topk == 0) return;
     const bool number = ls == ls;              // no NaN or +inf in the row
@@ -205,7 +208,7 @@ __device__ __forceinline__ void finish(const Out& o, const Row<kBf16>& r, int64_
         const int64_t at = t * o.topk + threadIdx.x;
         const bool have = n >= o.topk;         // else any indices
         o.top_id[at] = have ? key_index(key[threadIdx.x]) : (int)threadIdx.x;
-        o.top_logp[at] = have ? ln_p(key_value(key[threadIdx.x]), a.m, ls, o.it) : NAN;
+        o.top_logp[at] = have ? (float)ln_p(key_value(key[threadIdx.x]), a.m, ls, o.it) : NAN;
     }
 }
 
