@@ -116,15 +116,12 @@ __device__ __forceinline__ float cross(const Parked& p, float m, double ls, floa
     return wave_sum(y);
 }
 
-// Probabilities of a row are 2^((z - base) cl - l2) inv: l2 = log2 of the sum
-// where only the stats are known, inv its reciprocal where it is at hand (then
-// l2 = 0: the logarithm's rounding does not enter the gradient).
-//
-// Gradients at the list's ids: by (Q p - q), q summed over the entries with
+// Gradients at the list's ids: by (Q p - q), p = 2^((z - base) cl) inv with inv
+// the reciprocal of the row's sum, q summed over the entries with
 // the same id in the list's order, so that every one of them has the same
 // value.  One wave; they stay in LDS until the dense ones are written.
 __device__ __forceinline__ void at_entries(Parked& p, int topk, float by, bool none, float base,
-                                           float cl, float l2, float inv) {
+                                           float cl, float inv) {
     const int lane = threadIdx.x & 63;
     const int id[2] = {p.id[lane], p.id[lane + 64]};
     float q[2] = {0.0f, 0.0f};
@@ -134,7 +131,7 @@ __device__ __forceinline__ void at_entries(Parked& p, int topk, float by, bool n
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         const int i = lane + 64 * b;
-        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(p.z[i] - base, cl, -l2)) * inv;
+        const float x = __builtin_amdgcn_exp2f((p.z[i] - base) * cl) * inv;
         p.g[i] = none ? 0.0f : by * __builtin_fmaf(p.all, x, -q[b]);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -155,11 +152,11 @@ __device__ __forceinline__ void patch(const Row<kBf16>& r, char* at, const Parke
 
 // One vector's gradient by Q p, a = by Q inv.
 template <int kBf16>
-__device__ __forceinline__ uint4 dense(const uint4& q, float base, float cl, float l2, float a) {
+__device__ __forceinline__ uint4 dense(const uint4& q, float base, float cl, float a) {
     float g[8];
 #pragma unroll
     for (int e = 0; e < Row<kBf16>::kPer; ++e)
-        g[e] = a * __builtin_amdgcn_exp2f(__builtin_fmaf(get<kBf16>(q, e) - base, cl, -l2));
+        g[e] = a * __builtin_amdgcn_exp2f((get<kBf16>(q, e) - base) * cl);
     return put<kBf16>(g);
 }
 template <int kBf16>
@@ -302,17 +299,17 @@ __global__ __launch_bounds__(kThreads) void k_distill_bwd(const void* z, int64_t
     const float m = stats[2 * t], ls = stats[2 * t + 1];
     const float by = w * it * (g ? g[t] : 1.0f);
     const Teacher q = teacher(load_entries(l, t), r.V, it, l.renorm);
-    const float base = stat_base(m), cl = it * kLog2e, l2 = ls * kLog2e;
+    const float base = stat_base(m), cl = it * kLog2e, inv = recip_sum(ls);
     // the part's entries [v0, v1), their gradients parked before any store
     const int v0 = c0 ? r.index(c0 * kChunk, 0) : 0, v1 = r.index(c1 * kChunk, 0);
     if (threadIdx.x < 64) {
         float x[2];
         gather<kBf16>(r, q, x);
         park(q, x, s_list);
-        at_entries(s_list, l.topk, by, m == -INFINITY && ls == ls, base, cl, l2, 1.0f);
+        at_entries(s_list, l.topk, by, m == -INFINITY && ls == ls, base, cl, inv);
     }
     __syncthreads();
-    const float a = by * q.all;
+    const float a = by * q.all * inv;
     for (int ch = c0; ch < c1; ++ch) {
         uint4 x[kVecs];
 #pragma unroll
@@ -324,7 +321,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_bwd(const void* z, int64_t
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             const int j = ch * kChunk + i * kThreads + threadIdx.x;
-            if (j < r.nvec) store_vec<kBf16>(r, out, j, dense<kBf16>(x[i], base, cl, l2, a));
+            if (j < r.nvec) store_vec<kBf16>(r, out, j, dense<kBf16>(x[i], base, cl, a));
         }
     }
     __syncthreads();
@@ -445,7 +442,7 @@ __global__ __launch_bounds__(kThr, 4) void k_distill_row(const void* z, int64_t 
         if (tid < 64) {
             const float y = cross(s_list, a.m, log_sum(a), it);
             if (tid == 0) loss[t] = w == 0.0f ? 0.0f : w * y;
-            at_entries(s_list, l.topk, by, none, base, cl, 0.0f, inv);
+            at_entries(s_list, l.topk, by, none, base, cl, inv);
         }
         // gradient
         const float f = w == 0.0f ? 0.0f : by * s_list.all * inv;
@@ -453,15 +450,15 @@ __global__ __launch_bounds__(kThr, 4) void k_distill_row(const void* z, int64_t 
             const int j = first(r) + i;
             uint4 y = masked;
             if (i < beyond) y = *r.vec(j);
-            st_stream16(out + 16 * (int64_t)j, dense<kBf16>(y, base, cl, 0.0f, f));
+            st_stream16(out + 16 * (int64_t)j, dense<kBf16>(y, base, cl, f));
         }
         const int j = edge_at(r);
-        if (j >= 0) store_part<kBf16>(r, out, j, dense<kBf16>(edge, base, cl, 0.0f, f));
+        if (j >= 0) store_part<kBf16>(r, out, j, dense<kBf16>(edge, base, cl, f));
         load_edge(rn, more);
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
             if (i * kThr < n) {
-                const uint4 y = dense<kBf16>(x[i], base, cl, 0.0f, f);
+                const uint4 y = dense<kBf16>(x[i], base, cl, f);
                 char* to = out + 16 * (int64_t)(first(r) + i * kThr);
                 if (i * kThr + tid < n) {
                     if (kLong) st_stream16(to + lane16, y);

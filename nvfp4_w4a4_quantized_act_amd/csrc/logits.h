@@ -186,6 +186,15 @@ __device__ __forceinline__ double ln_wide(float s) {
 __device__ __forceinline__ double log_sum(const Stat& a) {
     return a.m == -INFINITY && a.s == 0.0f ? 0.0 : ln_wide(a.s);
 }
+// 1 / sum exp(it (z - m)) from the fp32 log-sum a forward pass has left, with
+// no more error than ls has itself: ls log2(e) in two parts.  A probability is
+// then 2^((z - m) cl) times it, which for a large one is nearer than the power
+// of the difference.
+__device__ __forceinline__ float recip_sum(float ls) {
+    const float hi = ls * kLog2e;
+    const float lo = __builtin_fmaf(ls, kLog2e, -hi) + ls * 1.92596299e-8f;
+    return __builtin_amdgcn_exp2f(-hi) * __builtin_fmaf(-lo, kLn2, 1.0f);
+}
 // ln p of an entry: -inf where it is masked (unless the row holds NaN or +inf).
 __device__ __forceinline__ double ln_p(float z, float m, double ls, float it) {
     return z == -INFINITY && ls == ls ? (double)z : ((double)z - (double)m) * (double)it - ls;

@@ -464,11 +464,13 @@ __global__ __launch_bounds__(kThreads) void k_logprob_bwd(const void* z, int64_t
     const bool have = id >= 0 && id < r.V;
     const float gl = g_logp && have ? it * g_logp[t] : 0.0f;
     const float gh = g_entropy ? it * g_entropy[t] : 0.0f;
-    // with d = log2 p: dz = it g_lp 1[v = id] - p (f0 + f1 d)
-    const float f0 = g_entropy ? __builtin_fmaf(gh, entropy[t], gl) : gl;
-    const float f1 = gh * kLn2;
+    // with x = log2(p sum): dz = it g_lp 1[v = id] - 2^x (f0 + f1 x), both
+    // factors by 1 / sum
+    const float inv = recip_sum(ls);
+    const float f0 = (g_entropy ? __builtin_fmaf(gh, entropy[t] - ls, gl) : gl) * inv;
+    const float f1 = gh * kLn2 * inv;
     const bool none = m == -INFINITY && ls == ls;          // no unmasked entry: no gradient
-    const float cl = it * kLog2e, l2 = ls * kLog2e;
+    const float cl = it * kLog2e;
     const int idv = have ? (id + r.shift) / kPer : -1, ide = have ? (id + r.shift) % kPer : 0;
 
     for (int ch = c0; ch < c1; ++ch) {
@@ -486,8 +488,8 @@ __global__ __launch_bounds__(kThreads) void k_logprob_bwd(const void* z, int64_t
             float g[8];
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
-                const float d = __builtin_fmaf(get<kBf16>(q[i], e) - m, cl, -l2);
-                g[e] = -__builtin_amdgcn_exp2f(d) * __builtin_fmaf(f1, fmaxf(d, kNoTerm), f0);
+                const float x = (get<kBf16>(q[i], e) - m) * cl;
+                g[e] = -__builtin_amdgcn_exp2f(x) * __builtin_fmaf(f1, fmaxf(x, kNoTerm), f0);
             }
             if (j == idv) {
 #pragma unroll
