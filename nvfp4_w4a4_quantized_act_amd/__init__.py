@@ -597,9 +597,10 @@ def _scratch(nbytes, dev):
     return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
 
 
-def _logits(logits):
+def _logits(logits, ld_max=2**31 - 1):
     """(logits, dtype code, T, V, ld): a 2-D view with dense, 16-byte aligned rows; copied
-    if it is not one already.  A row stride above V (padded rows) needs no copy."""
+    if it is not one already.  A row stride above V (padded rows) up to ld_max needs no
+    copy."""
     _gpu("logits", logits)
     if logits.dtype == torch.float32:
         code = OUT_F32
@@ -611,22 +612,29 @@ def _logits(logits):
         raise ValueError("logits must be [T, V]")
     t, v = logits.shape
     z = logits
-    if t and v and (z.stride(1) != 1 or (t > 1 and z.stride(0) < v) or z.data_ptr() % 16):
+    if t and v and (z.stride(1) != 1 or (t > 1 and not v <= z.stride(0) <= ld_max)
+                    or z.data_ptr() % 16):
         z = z.detach().clone(memory_format=torch.contiguous_format)
     return z, code, t, v, (z.stride(0) if t > 1 else v)
 
 
-def _like_logits(z, t, v, ld, out):
-    """The gradient's tensor: `out`, checked, or a new one with the logits' row stride."""
+def _logits_and_grad(logits, out):
+    """_logits and the gradient's tensor: `out`, checked, or a new one with the logits' row
+    stride.  Rows far apart (the last positions of [B, S, V] logits) are copied then: their
+    gradient would take the whole batch's memory."""
+    far = out is None and isinstance(logits, torch.Tensor) and logits.dim() == 2
+    z, code, t, v, ld = _logits(logits, 2 * logits.shape[1] if far else 2**31 - 1)
     if out is None:
         if ld == v:
-            return torch.empty((t, v), dtype=z.dtype, device=z.device)
-        return torch.empty((t, ld), dtype=z.dtype, device=z.device)[:, :v]
+            out = torch.empty((t, v), dtype=z.dtype, device=z.device)
+        else:
+            out = torch.empty((t, ld), dtype=z.dtype, device=z.device)[:, :v]
+        return z, code, t, v, ld, out
     if out.dtype != z.dtype or tuple(out.shape) != (t, v) or out.device != z.device:
         raise ValueError("out must have the logits' type, shape and device")
     if t and v and (out.stride(1) != 1 or (t > 1 and out.stride(0) != ld) or out.data_ptr() % 16):
         raise ValueError("out must have the logits' row stride and be 16-byte aligned")
-    return out
+    return z, code, t, v, ld, out
 
 
 def quads_moe_w4a16_gemv(x, w, n, rows=None, offsets=None, row_token=None, epilogue=EPI_NONE,
@@ -694,14 +702,13 @@ def quads_token_logprob_backward(logits, ids, stats, entropy, g_logp, g_entropy=
                                  inv_temp=1.0, out=None):
     """Gradient of the logits from the gradients fp32 [T] of quads_token_logprob's logp and
     entropy (either may be None); stats and entropy are that call's.  out may be the logits."""
-    z, code, t, v, ld = _logits(logits)
+    z, code, t, v, ld, out = _logits_and_grad(logits, out)
     dev = z.device
     ids = _want("ids", ids, torch.int32, (t,), dev)
     stats = _want("stats", stats, torch.float32, (t, 2), dev)
     entropy = _want("entropy", entropy, torch.float32, (t,), dev)
     g_logp = _want("g_logp", g_logp, torch.float32, (t,), dev)
     g_entropy = _want("g_entropy", g_entropy, torch.float32, (t,), dev)
-    out = _like_logits(z, t, v, ld, out)
     _call("quads_token_logprob_backward", dev, _at(z), code, t, v, ld, _at(ids), inv_temp,
           _at(stats), _at(entropy), _at(g_logp), _at(g_entropy), _at(out))
     return out
@@ -735,12 +742,11 @@ def quads_topk_distill_backward(logits, t_val, t_id, stats, g, weight=None, inv_
                                 renorm=True, out=None):
     """Gradient of the logits from the gradient g fp32 [T] of quads_topk_distill's loss; stats
     are that call's.  out may be the logits."""
-    z, code, t, v, ld = _logits(logits)
+    z, code, t, v, ld, out = _logits_and_grad(logits, out)
     dev = z.device
     t_val, t_id, k, weight = _teacher(t_val, t_id, weight, t, dev)
     stats = _want("stats", stats, torch.float32, (t, 2), dev)
     g = _want("g", g, torch.float32, (t,), dev)
-    out = _like_logits(z, t, v, ld, out)
     _call("quads_topk_distill_backward", dev, _at(z), code, t, v, ld, _at(t_val), _at(t_id),
           k, _at(weight), inv_temp, int(renorm), _at(stats), _at(g), _at(out))
     return out
@@ -750,11 +756,10 @@ def quads_topk_distill_grad(logits, t_val, t_id, weight=None, inv_temp=1.0, reno
                             out=None):
     """The loss and the gradient of its sum in one call -> (loss fp32 [T], dlogits).  out may be
     the logits."""
-    z, code, t, v, ld = _logits(logits)
+    z, code, t, v, ld, out = _logits_and_grad(logits, out)
     dev = z.device
     t_val, t_id, k, weight = _teacher(t_val, t_id, weight, t, dev)
     loss = torch.empty(t, dtype=torch.float32, device=dev)
-    out = _like_logits(z, t, v, ld, out)
     nws = lib().quads_topk_distill_grad_ws(t, v, k)
     ws = _scratch(nws, dev)
     _call("quads_topk_distill_grad", dev, _at(z), code, t, v, ld, _at(t_val), _at(t_id), k,

@@ -526,6 +526,34 @@ def test_strides_and_alignment(Q):
     assert all(torch.equal(got[k], want[k][1:]) for k in want)
 
 
+def test_rows_far_apart(Q, qat):
+    """The last positions of [B, S, V] logits: read where they are, a dense gradient."""
+    z = make(12, 520, "f32", seed=4)[0].reshape(4, 3, 520)
+    last, dense = z[:, -1], z[:, -1].contiguous()
+    ids = torch.tensor([3, 519, -1, 0], dtype=torch.int32, device=DEV)
+    tv, ti = torch.zeros((4, 2), device=DEV), torch.tensor([[1, 9]] * 4, dtype=torch.int32,
+                                                           device=DEV)
+    one = torch.ones(4, device=DEV)
+
+    def calls(x):
+        r = Q.quads_token_logprob(x, ids, 1.0, 5)
+        loss, st = Q.quads_topk_distill(x, tv, ti)
+        grads = [Q.quads_token_logprob_backward(x, ids, r["stats"], r["entropy"], one, one),
+                 Q.quads_topk_distill_backward(x, tv, ti, st, one),
+                 Q.quads_topk_distill_grad(x, tv, ti)[1]]
+        assert all(g.is_contiguous() for g in grads)
+        return [*r.values(), loss, st, *grads]
+    assert all(torch.equal(a, b) for a, b in zip(calls(last), calls(dense)))
+    out = torch.full_like(z, 7.0)                            # in place of rows far apart
+    Q.quads_topk_distill_grad(last, tv, ti, out=out[:, -1])
+    assert torch.equal(out[:, -1], Q.quads_topk_distill_grad(dense, tv, ti)[1])
+    assert bool((out[:, :-1] == 7.0).all())
+    full = z.clone().requires_grad_()
+    lp, _ = qat.token_logprobs(full[:, -1], ids)
+    lp.sum().backward()
+    assert not bool(full.grad[:, :-1].any()) and bool(full.grad[0, -1].any())
+
+
 def test_empty_calls(Q):
     z = torch.empty((0, 100), device=DEV)
     r = Q.quads_token_logprob(z, torch.empty(0, dtype=torch.int32, device=DEV), 1.0, 3)
