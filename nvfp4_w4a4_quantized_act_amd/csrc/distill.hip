@@ -183,13 +183,9 @@ __device__ __forceinline__ void pin(uint4& q) {
 // ------------------------------------------------------------------ streaming --
 
 // Loss and stats of a row from its statistics (one wave).
-template <int kBf16>
-__device__ __forceinline__ void finish_loss(const Row<kBf16>& r, int64_t t, const Stat& a,
-                                            const List& l, float w, float it, float* loss,
+__device__ __forceinline__ void finish_loss(int64_t t, const Stat& a, const Teacher& q,
+                                            const float z[2], float w, float it, float* loss,
                                             float* stats, Parked& p) {
-    const Teacher q = teacher(load_entries(l, t), r.V, it, l.renorm);
-    float z[2];
-    gather<kBf16>(r, q, z);
     park(q, z, p);
     const double ls = log_sum(a);
     const float y = cross(p, a.m, ls, it);
@@ -205,12 +201,12 @@ __device__ __forceinline__ void no_loss(int64_t t, float* loss, float* stats) {
     stats[2 * t + 1] = 0.0f;
 }
 
-template <int kBf16>
-__global__ __launch_bounds__(kThreads) void k_distill_loss(const void* z, int64_t V, int64_t ld,
-                                                           int parts, List l, float it,
-                                                           float* loss, float* stats,
-                                                           float4* part_stat) {
-    __shared__ Stat s_stat[kThreads / 64];
+template <int kBf16, int kThr>
+__global__ __launch_bounds__(kThr) void k_distill_loss(const void* z, int64_t V, int64_t ld,
+                                                       int parts, List l, float it, float* loss,
+                                                       float* stats, float4* part_stat) {
+    constexpr int kChunk = kThr * kVecs;
+    __shared__ Stat s_stat[kThr / 64];
     __shared__ Parked s_list;
     const int64_t t = blockIdx.x / (unsigned)parts;
     const int part = (int)(blockIdx.x % (unsigned)parts);
@@ -228,14 +224,24 @@ __global__ __launch_bounds__(kThreads) void k_distill_loss(const void* z, int64_
         if (ch >= c1) return;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            const int j = ch * kChunk + i * kThreads + threadIdx.x;
+            const int j = ch * kChunk + i * kThr + threadIdx.x;
             if (r.whole(j)) q[i] = *r.vec(j);
             else q[i] = r.part(j);
         }
     };
     Stat a = {-INFINITY, 0.0f, 0.0f};
     uint4 q[kVecs], next[kVecs];
+    // the list and the logits at its ids come while the row is read
+    const bool first = parts == 1 && threadIdx.x < 64;
+    Entries x = {};
+    if (first) x = load_entries(l, t);
     load(next, c0);
+    Teacher list = {};
+    float zq[2] = {0.0f, 0.0f};
+    if (first) {
+        list = teacher(x, r.V, it, l.renorm);
+        gather<kBf16>(r, list, zq);
+    }
     for (int ch = c0; ch < c1; ++ch) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) q[i] = next[i];
@@ -248,11 +254,11 @@ __global__ __launch_bounds__(kThreads) void k_distill_loss(const void* z, int64_
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) a.s = vec_sum<kBf16>(q[i], base, cl, a.s);
     }
-    a = group_stat<kThreads / 64>(a, cl, s_stat);
+    a = group_stat<kThr / 64>(a, cl, s_stat);
     if (parts > 1) {
         if (threadIdx.x == 0) part_stat[blockIdx.x] = make_float4(a.m, a.s, 0.0f, 0.0f);
-    } else if (threadIdx.x < 64) {
-        finish_loss<kBf16>(r, t, a, l, w, it, loss, stats, s_list);
+    } else if (first) {
+        finish_loss(t, a, list, zq, w, it, loss, stats, s_list);
     }
 }
 
@@ -268,13 +274,18 @@ __global__ __launch_bounds__(64) void k_distill_join(const void* z, int64_t V, i
         if (threadIdx.x == 0) no_loss(t, loss, stats);
         return;
     }
+    const Row<kBf16> r(z, t, ld, V);
+    const Entries x = load_entries(l, t);
     Stat a = {-INFINITY, 0.0f, 0.0f};
     if ((int)threadIdx.x < parts) {
         const float4 q = part_stat[t * parts + threadIdx.x];
         a = {q.x, q.y, q.z};
     }
+    const Teacher list = teacher(x, r.V, it, l.renorm);
+    float zq[2];
+    gather<kBf16>(r, list, zq);
     a = wave_stat(a, it * kLog2e);
-    finish_loss<kBf16>(Row<kBf16>(z, t, ld, V), t, a, l, w, it, loss, stats, s_list);
+    finish_loss(t, a, list, zq, w, it, loss, stats, s_list);
 }
 
 template <int kBf16>
@@ -296,28 +307,34 @@ __global__ __launch_bounds__(kThreads) void k_distill_bwd(const void* z, int64_t
             store_vec<kBf16>(r, out, j, make_uint4(0, 0, 0, 0));
         return;
     }
-    const float m = stats[2 * t], ls = stats[2 * t + 1];
-    const float by = w * it * (g ? g[t] : 1.0f);
-    const Teacher q = teacher(load_entries(l, t), r.V, it, l.renorm);
-    const float base = stat_base(m), cl = it * kLog2e, inv = recip_sum(ls);
-    // the part's entries [v0, v1), their gradients parked before any store
-    const int v0 = c0 ? r.index(c0 * kChunk, 0) : 0, v1 = r.index(c1 * kChunk, 0);
-    if (threadIdx.x < 64) {
-        float x[2];
-        gather<kBf16>(r, q, x);
-        park(q, x, s_list);
-        at_entries(s_list, l.topk, by, m == -INFINITY && ls == ls, base, cl, inv);
-    }
-    __syncthreads();
-    const float a = by * q.all * inv;
-    for (int ch = c0; ch < c1; ++ch) {
-        uint4 x[kVecs];
+    // the first chunk comes while the list is worked on
+    uint4 x[kVecs];
+    auto load = [&](int ch) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             const int j = ch * kChunk + i * kThreads + threadIdx.x;
             if (r.whole(j)) x[i] = *r.vec(j);
             else x[i] = r.part(j);
         }
+    };
+    const Entries listed = load_entries(l, t);
+    const float m = stats[2 * t], ls = stats[2 * t + 1];
+    const float by = w * it * (g ? g[t] : 1.0f);
+    load(c0);
+    const Teacher q = teacher(listed, r.V, it, l.renorm);
+    const float base = stat_base(m), cl = it * kLog2e, inv = recip_sum(ls);
+    // the part's entries [v0, v1), their gradients parked before any store
+    const int v0 = c0 ? r.index(c0 * kChunk, 0) : 0, v1 = r.index(c1 * kChunk, 0);
+    if (threadIdx.x < 64) {
+        float zq[2];
+        gather<kBf16>(r, q, zq);
+        park(q, zq, s_list);
+        at_entries(s_list, l.topk, by, m == -INFINITY && ls == ls, base, cl, inv);
+    }
+    __syncthreads();
+    const float a = by * q.all * inv;
+    for (int ch = c0; ch < c1; ++ch) {
+        if (ch > c0) load(ch);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             const int j = ch * kChunk + i * kThreads + threadIdx.x;
@@ -510,8 +527,13 @@ template <int kBf16>
 void launch_loss(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, float it,
                  float* loss, float* stats, void* ws, hipStream_t st) {
     const int parts = row_parts(T, V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32, kWhole);
-    hipLaunchKernelGGL(k_distill_loss<kBf16>, dim3((unsigned)(T * parts)), dim3(kThreads), 0, st, z,
-                       V, ld, parts, l, it, loss, stats, (float4*)ws);
+    if (wide_rows<kBf16>(T, V, parts))
+        hipLaunchKernelGGL((k_distill_loss<kBf16, kWideThreads>), dim3((unsigned)T),
+                           dim3(kWideThreads), 0, st, z, V, ld, 1, l, it, loss, stats, (float4*)nullptr);
+    else
+        hipLaunchKernelGGL((k_distill_loss<kBf16, kThreads>), dim3((unsigned)(T * parts)),
+                           dim3(kThreads), 0, st, z, V, ld, parts, l, it, loss, stats,
+                           (float4*)ws);
     if (parts > 1)
         hipLaunchKernelGGL(k_distill_join<kBf16>, dim3((unsigned)T), dim3(64), 0, st, z, V, ld,
                            parts, l, it, loss, stats, (const float4*)ws);

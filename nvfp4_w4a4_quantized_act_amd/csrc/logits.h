@@ -229,6 +229,17 @@ inline int row_parts(int64_t T, int64_t V, int dtype, int whole) {
     const int p = split_row(T, V, dtype, kGroups);
     return p < kMaxParts ? p : kMaxParts;
 }
+// Rows of one work-group each, at most one per CU and longer than two chunks,
+// take a work-group of four times the threads for their sums (the
+// distillation's loss in us, calls in turn from a graph, 256 / 1024 threads:
+// 33 x 50001 fp32 12.2 / 8.9, 256 x 65536 22.4 / 16.0, 1 x 16000 5.4 / 4.5, 256
+// x 32000 bf16 7.7 / 7.2; not for 512 x 50001 bf16 15.5 / 17.7, 33 x 8000 4.6 /
+// 6.2).
+constexpr int kWideThreads = 1024;
+template <int kBf16>
+inline bool wide_rows(int64_t T, int64_t V, int parts) {
+    return parts == 1 && T <= 256 && V > 2 * kChunk * (int64_t)Row<kBf16>::kPer;
+}
 // Parts of a row for a gradient: nothing is joined, so that more of them are
 // better, up to what the GPU holds at once (1023 x 50001 fp32, both passes: 145
 // us with 1024 work-groups wanted, 141 with 2048, 137 with 4096, 150 with 8192).

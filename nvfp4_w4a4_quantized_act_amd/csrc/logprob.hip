@@ -225,12 +225,13 @@ __device__ __forceinline__ void finish(const Out& o, const Row<kBf16>& r, int64_
 // number.  The candidates are sorted once, at the end.  Where there were more
 // than there is room for (equal or rising entries) the part is read again,
 // 256 entries at a time, the candidates cut to the topk largest in between.
-template <int kBf16, bool kEntropy, bool kTop, int kVecs>
-__global__ __launch_bounds__(kThreads) void k_logprob(const void* z, int64_t V, int64_t ld,
-                                                      int parts, Out o, Parts p) {
+template <int kBf16, bool kEntropy, bool kTop, int kVecs, int kThr = kThreads>
+__global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int64_t ld, int parts,
+                                                  Out o, Parts p) {
+    static_assert(!kTop || kThr == kThreads, "the alternatives' steps are for kThreads threads");
     constexpr int kPer = Row<kBf16>::kPer;
-    constexpr int kChunk = kThreads * kVecs;
-    __shared__ Stat s_stat[kThreads / 64];
+    constexpr int kChunk = kThr * kVecs;
+    __shared__ Stat s_stat[kThr / 64];
     __shared__ Cand c;
     const int64_t t = blockIdx.x / (unsigned)parts;
     const int part = (int)(blockIdx.x % (unsigned)parts);
@@ -247,11 +248,11 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const void* z, int64_t V, 
         if (r.whole(j0) && r.whole(j0 + kChunk - 1)) {
             const uint4* a = r.vec(j0 + threadIdx.x);
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) q[i] = a[i * kThreads];
+            for (int i = 0; i < kVecs; ++i) q[i] = a[i * kThr];
         } else {
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const int j = j0 + i * kThreads + threadIdx.x;
+                const int j = j0 + i * kThr + threadIdx.x;
                 if (r.whole(j)) q[i] = *r.vec(j);
                 else q[i] = r.part(j);
             }
@@ -325,7 +326,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const void* z, int64_t V, 
         }
     }
 
-    a = group_stat<kThreads / 64>(a, cl, s_stat);
+    a = group_stat<kThr / 64>(a, cl, s_stat);
     int n = 0;
     if (kTop) {
         n = c.n;                               // (group_stat has a barrier)
@@ -519,7 +520,10 @@ template <int kBf16, bool kEntropy, bool kTop>
 void launch_rows(const void* z, int64_t T, int64_t V, int64_t ld, int parts, const Out& o,
                  const Parts& p, hipStream_t st) {
     const dim3 grid((unsigned)(T * parts)), block(kThreads);
-    if (few_rows<kBf16>(T, V, parts))
+    if (!kTop && wide_rows<kBf16>(T, V, parts))
+        hipLaunchKernelGGL((k_logprob<kBf16, kEntropy, false, kVecs, kWideThreads>), grid,
+                           dim3(kWideThreads), 0, st, z, V, ld, 1, o, p);
+    else if (few_rows<kBf16>(T, V, parts))
         hipLaunchKernelGGL((k_logprob<kBf16, kEntropy, kTop, kVecsFew>), grid, block, 0, st, z, V,
                            ld, parts, o, p);
     else
