@@ -230,11 +230,11 @@ inline int row_parts(int64_t T, int64_t V, int dtype, int whole) {
     return p < kMaxParts ? p : kMaxParts;
 }
 // Rows of one work-group each, at most one per CU and longer than two chunks,
-// take a work-group of four times the threads for their sums (the
-// distillation's loss in us, calls in turn from a graph, 256 / 1024 threads:
-// 33 x 50001 fp32 12.2 / 8.9, 256 x 65536 22.4 / 16.0, 1 x 16000 5.4 / 4.5, 256
-// x 32000 bf16 7.7 / 7.2; not for 512 x 50001 bf16 15.5 / 17.7, 33 x 8000 4.6 /
-// 6.2).
+// take a work-group of four times the threads for their sums (in us, calls in
+// turn from a graph, 256 / 1024 threads: the distillation's loss 33 x 50001 fp32
+// 12.2 / 8.9, 256 x 65536 22.4 / 16.0, 1 x 16000 5.4 / 4.5, 256 x 32000 bf16 7.7
+// / 7.2, not for 512 x 50001 bf16 15.5 / 17.7, 33 x 8000 4.6 / 6.2; with the top
+// 20 alternatives 128 x 16000 fp32 12.4 / 10.1, 1 x 20000 bf16 11.3 / 10.1).
 constexpr int kWideThreads = 1024;
 template <int kBf16>
 inline bool wide_rows(int64_t T, int64_t V, int parts) {

@@ -72,6 +72,18 @@ __device__ __forceinline__ float kth_bound(const uint16_t* top, int k) {
     return t <= 0x007Fu ? -INFINITY : key_value((uint64_t)(t << 16) << 32);
 }
 
+// A thread's maximum, or that of kThr / kThreads neighbours, into `top`.
+template <int kThr>
+__device__ __forceinline__ void set_top(uint16_t* top, float m) {
+    constexpr int kOf = kThr / kThreads;
+    static_assert(kOf == 1 || kOf == 4, "one thread's or four neighbours' maximum");
+    if (kOf == 4) {
+        m = fmaxf(m, dpp_move<0xB1, 0xF>(m, m));           // quad_perm:[1,0,3,2]
+        m = fmaxf(m, dpp_move<0x4E, 0xF>(m, m));           // quad_perm:[2,3,0,1]
+    }
+    if (threadIdx.x % kOf == 0) top[threadIdx.x / kOf] = (uint16_t)(value_key(m) >> 16);
+}
+
 // Drops the candidates whose half is below the k-th largest one.
 template <int kPerLane>
 __device__ __forceinline__ uint64_t kth_key(const Cand& c, int n, int k) {
@@ -83,20 +95,21 @@ __device__ __forceinline__ uint64_t kth_key(const Cand& c, int n, int k) {
     }
     return (uint64_t)kth_half<kPerLane>(h, k) << 48;
 }
+template <int kThr>
 __device__ __forceinline__ int drop_low(Cand& c, int n, int k) {
-    uint64_t mine[kCand / kThreads];
+    uint64_t mine[kCand / kThr];
     __syncthreads();
-    const uint64_t low = n <= kThreads ? kth_key<4>(c, n, k) : kth_key<kCand / 64>(c, n, k);
+    const uint64_t low = n <= 256 ? kth_key<4>(c, n, k) : kth_key<kCand / 64>(c, n, k);
 #pragma unroll
-    for (int i = 0; i < kCand / kThreads; ++i) {
-        const int at = threadIdx.x + i * kThreads;
+    for (int i = 0; i < kCand / kThr; ++i) {
+        const int at = threadIdx.x + i * kThr;
         mine[i] = at < n ? c.key[at] : 0;
     }
     __syncthreads();
     if (threadIdx.x == 0) c.n = 0;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kCand / kThreads; ++i)
+    for (int i = 0; i < kCand / kThr; ++i)
         if (mine[i] >= low && mine[i] != 0) c.key[atomicAdd(&c.n, 1)] = mine[i];
     __syncthreads();
     return c.n;
@@ -105,14 +118,15 @@ __device__ __forceinline__ int drop_low(Cand& c, int n, int k) {
 // Sorts the n candidates and keeps the k largest (c.n is set; barriers on
 // both sides).  Each entry's place is the number of larger ones, eight read
 // at a time; candidates well beyond k are dropped before.
+template <int kThr>
 __device__ __forceinline__ void keep_top(Cand& c, int n, int k) {
-    if (n > k + k / 2 + 16) n = drop_low(c, n, k);
-    uint64_t mine[kCand / kThreads];
-    int place[kCand / kThreads];
+    if (n > k + k / 2 + 16) n = drop_low<kThr>(c, n, k);
+    uint64_t mine[kCand / kThr];
+    int place[kCand / kThr];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kCand / kThreads; ++i) {
-        const int at = threadIdx.x + i * kThreads;
+    for (int i = 0; i < kCand / kThr; ++i) {
+        const int at = threadIdx.x + i * kThr;
         mine[i] = at < n ? c.key[at] : 0;
         place[i] = 0;
     }
@@ -124,16 +138,16 @@ __device__ __forceinline__ void keep_top(Cand& c, int n, int k) {
         for (int b = 0; b < 8; ++b) x[b] = c.key[j + b];
 #pragma unroll
         for (int b = 0; b < 8; ++b) place[0] += x[b] > mine[0] ? 1 : 0;
-        if (n > kThreads) {
+        if (n > kThr) {
 #pragma unroll
-            for (int i = 1; i < kCand / kThreads; ++i)
+            for (int i = 1; i < kCand / kThr; ++i)
 #pragma unroll
                 for (int b = 0; b < 8; ++b) place[i] += x[b] > mine[i] ? 1 : 0;
         }
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kCand / kThreads; ++i)
+    for (int i = 0; i < kCand / kThr; ++i)
         if (mine[i] != 0 && place[i] < k) c.key[place[i]] = mine[i];
     if (threadIdx.x == 0) c.n = n < k ? n : k;
     __syncthreads();
@@ -228,7 +242,6 @@ __device__ __forceinline__ void finish(const Out& o, const Row<kBf16>& r, int64_
 template <int kBf16, bool kEntropy, bool kTop, int kVecs, int kThr = kThreads>
 __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int64_t ld, int parts,
                                                   Out o, Parts p) {
-    static_assert(!kTop || kThr == kThreads, "the alternatives' steps are for kThreads threads");
     constexpr int kPer = Row<kBf16>::kPer;
     constexpr int kChunk = kThr * kVecs;
     __shared__ Stat s_stat[kThr / 64];
@@ -295,7 +308,7 @@ __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int6
         if (kTop) {
             const int nth = ch - c0;
             if (nth == 0) {
-                c.top[0][threadIdx.x] = (uint16_t)(value_key(m) >> 16);
+                set_top<kThr>(c.top[0], m);
                 __syncthreads();
                 bound = kth_bound(c.top[0], topk);
             }
@@ -308,7 +321,7 @@ __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int6
                         const float x = get<kBf16>(q[i], e);
                         if (x >= reach) {
                             const int at = atomicAdd(&c.n, 1);
-                            const int v = r.index(ch * kChunk + i * kThreads + threadIdx.x, e);
+                            const int v = r.index(ch * kChunk + i * kThr + threadIdx.x, e);
                             if (at < kCand) c.key[at] = rank_key(x, (uint32_t)v);
                         }
                     }
@@ -319,7 +332,7 @@ __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int6
                 // (two sets of maxima in turn: a wave writes the second next
                 // one only after all have read this one)
                 fresh ^= 1;
-                c.top[fresh][threadIdx.x] = (uint16_t)(value_key(m) >> 16);
+                set_top<kThr>(c.top[fresh], m);
                 __syncthreads();
                 bound = fmaxf(bound, next_up(kth_bound(c.top[fresh], topk)));
             }
@@ -344,7 +357,8 @@ __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int6
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int at = v + i * kThreads + (int)threadIdx.x;
-                    const float x = at < v1 ? r.entry(at) : -INFINITY;
+                    const bool mine = kThr == kThreads || threadIdx.x < kThreads;
+                    const float x = mine && at < v1 ? r.entry(at) : -INFINITY;
                     k[i] = x > -INFINITY ? rank_key(x, (uint32_t)at) : 0;
                     any = any || k[i] > over;
                 }
@@ -352,7 +366,7 @@ __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int6
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     if (n + kThreads > kCand) {
-                        keep_top(c, n, topk);
+                        keep_top<kThr>(c, n, topk);
                         over = c.n == topk ? c.key[topk - 1] : 0;
                         __syncthreads();
                     }
@@ -363,7 +377,7 @@ __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int6
                 }
             }
         }
-        keep_top(c, n, topk);
+        keep_top<kThr>(c, n, topk);
         n = c.n;
     }
     if (parts == 1) {
@@ -420,7 +434,7 @@ __global__ __launch_bounds__(kThreads) void k_merge(const void* z, int64_t V, in
             uint64_t over = 0;
             for (int b = 0; b < all; b += kThreads) {
                 if (n + kThreads > kCand) {
-                    keep_top(c, n, o.topk);
+                    keep_top<kThreads>(c, n, o.topk);
                     over = c.n == o.topk ? c.key[o.topk - 1] : 0;
                     __syncthreads();
                 }
@@ -432,7 +446,7 @@ __global__ __launch_bounds__(kThreads) void k_merge(const void* z, int64_t V, in
                 __syncthreads();
             }
         }
-        keep_top(c, n, o.topk);
+        keep_top<kThreads>(c, n, o.topk);
         n = c.n;
     }
     a = wave_stat(a, o.it * kLog2e);
@@ -505,11 +519,10 @@ __global__ __launch_bounds__(kThreads) void k_logprob_bwd(const void* z, int64_t
     }
 }
 
-// Rows of one work-group each that leave the GPU half empty and are longer than
-// two chunks wait for each chunk's loads: their sums take four times the
-// vectors at once (in us, calls in turn, 4 / 16 vectors: 1 x 32768 fp32 top 20
-// 17.4 / 15.5, 400 x 30000 bf16 19.2 / 16.2, 800 x 30000 fp32 28.5 / 30.6; waited
-// for, 4 x 3000 bf16 29 / 34).
+// Rows of one work-group each that leave the GPU half empty, too many for wide
+// ones (wide_rows), and longer than two chunks wait for each chunk's loads:
+// their sums take four times the vectors at once (in us, calls in turn, 4 / 16
+// vectors: 400 x 30000 bf16 19.2 / 16.2; not for 800 x 30000 fp32 28.5 / 30.6).
 constexpr int kVecsFew = 16;
 template <int kBf16>
 inline bool few_rows(int64_t T, int64_t V, int parts) {
@@ -520,8 +533,8 @@ template <int kBf16, bool kEntropy, bool kTop>
 void launch_rows(const void* z, int64_t T, int64_t V, int64_t ld, int parts, const Out& o,
                  const Parts& p, hipStream_t st) {
     const dim3 grid((unsigned)(T * parts)), block(kThreads);
-    if (!kTop && wide_rows<kBf16>(T, V, parts))
-        hipLaunchKernelGGL((k_logprob<kBf16, kEntropy, false, kVecs, kWideThreads>), grid,
+    if (wide_rows<kBf16>(T, V, parts))
+        hipLaunchKernelGGL((k_logprob<kBf16, kEntropy, kTop, kVecs, kWideThreads>), grid,
                            dim3(kWideThreads), 0, st, z, V, ld, 1, o, p);
     else if (few_rows<kBf16>(T, V, parts))
         hipLaunchKernelGGL((k_logprob<kBf16, kEntropy, kTop, kVecsFew>), grid, block, 0, st, z, V,
