@@ -552,7 +552,8 @@ def quads_moe_mx_rac_gemm(a, r, sel, w, n, rows=None, offsets=None, row_token=No
 
 # ---- the output head (include/quads_head.h) ----------------------------------
 # Unlike the calls above, these check the tensors they are given (type, shape,
-# device) before the library sees a pointer, and run on the inputs' device.
+# device) before the library sees a pointer, and run on the inputs' device.  (torch.empty with
+# the sizes as arguments, not as a tuple: 1.3 us instead of 1.6, a call has up to five.)
 
 def _want(name, t, dtype, shape, dev):
     """`t` dense on `dev`, checked; None stays None."""
@@ -626,9 +627,9 @@ def _logits_and_grad(logits, out):
     z, code, t, v, ld = _logits(logits, 2 * logits.shape[1] if far else 2**31 - 1)
     if out is None:
         if ld == v:
-            out = torch.empty((t, v), dtype=z.dtype, device=z.device)
+            out = torch.empty(t, v, dtype=z.dtype, device=z.device)
         else:
-            out = torch.empty((t, ld), dtype=z.dtype, device=z.device)[:, :v]
+            out = torch.empty(t, ld, dtype=z.dtype, device=z.device)[:, :v]
         return z, code, t, v, ld, out
     if out.dtype != z.dtype or tuple(out.shape) != (t, v) or out.device != z.device:
         raise ValueError("out must have the logits' type, shape and device")
@@ -662,7 +663,7 @@ def quads_moe_w4a16_gemv(x, w, n, rows=None, offsets=None, row_token=None, epilo
     ncols = n // 2 if epilogue == EPI_SWIGLU else n
     dt = torch.float32 if out_dtype == OUT_F32 else torch.int16
     if out is None:
-        out = torch.empty((rows, ncols), dtype=dt, device=dev)
+        out = torch.empty(rows, ncols, dtype=dt, device=dev)
     elif (out.dtype not in ((dt,) if out_dtype == OUT_F32 else (torch.int16, torch.bfloat16))
           or tuple(out.shape) != (rows, ncols) or out.device != dev or not out.is_contiguous()):
         raise ValueError("out must be a dense tensor of the call's type, shape and device")
@@ -686,10 +687,10 @@ def quads_token_logprob(logits, ids=None, inv_temp=1.0, topk=0, want_entropy=Tru
         out["logp"] = torch.empty(t, dtype=torch.float32, device=dev)
     if want_entropy:
         out["entropy"] = torch.empty(t, dtype=torch.float32, device=dev)
-    out["stats"] = torch.empty((t, 2), dtype=torch.float32, device=dev)
+    out["stats"] = torch.empty(t, 2, dtype=torch.float32, device=dev)
     if topk > 0:
-        out["top_logp"] = torch.empty((t, topk), dtype=torch.float32, device=dev)
-        out["top_id"] = torch.empty((t, topk), dtype=torch.int32, device=dev)
+        out["top_logp"] = torch.empty(t, topk, dtype=torch.float32, device=dev)
+        out["top_id"] = torch.empty(t, topk, dtype=torch.int32, device=dev)
     nws = lib().quads_token_logprob_ws(t, v, topk)
     ws = _scratch(nws, dev)
     _call("quads_token_logprob", dev, _at(z), code, t, v, ld, _at(ids), inv_temp, topk,
@@ -730,7 +731,7 @@ def quads_topk_distill(logits, t_val, t_id, weight=None, inv_temp=1.0, renorm=Tr
     dev = z.device
     t_val, t_id, k, weight = _teacher(t_val, t_id, weight, t, dev)
     loss = torch.empty(t, dtype=torch.float32, device=dev)
-    stats = torch.empty((t, 2), dtype=torch.float32, device=dev)
+    stats = torch.empty(t, 2, dtype=torch.float32, device=dev)
     nws = lib().quads_topk_distill_ws(t, v, k)
     ws = _scratch(nws, dev)
     _call("quads_topk_distill", dev, _at(z), code, t, v, ld, _at(t_val), _at(t_id), k,
