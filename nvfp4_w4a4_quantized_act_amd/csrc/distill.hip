@@ -288,11 +288,12 @@ __global__ __launch_bounds__(64) void k_distill_join(const void* z, int64_t V, i
     finish_loss(t, a, list, zq, w, it, loss, stats, s_list);
 }
 
-template <int kBf16>
-__global__ __launch_bounds__(kThreads) void k_distill_bwd(const void* z, int64_t V, int64_t ld,
-                                                          int parts, List l, float it,
-                                                          const float* stats, const float* g,
-                                                          void* dz) {
+template <int kBf16, int kThr>
+__global__ __launch_bounds__(kThr) void k_distill_bwd(const void* z, int64_t V, int64_t ld,
+                                                      int parts, List l, float it,
+                                                      const float* stats, const float* g,
+                                                      void* dz) {
+    constexpr int kChunk = kThr * kVecs;
     __shared__ Parked s_list;
     const int64_t t = blockIdx.x / (unsigned)parts;
     const int part = (int)(blockIdx.x % (unsigned)parts);
@@ -303,7 +304,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_bwd(const void* z, int64_t
     const int c1 = (int)((int64_t)chunks * (part + 1) / parts);
     const float w = l.weight ? l.weight[t] : 1.0f;
     if (w == 0.0f) {
-        for (int j = c0 * kChunk + threadIdx.x; j < c1 * kChunk && j < r.nvec; j += kThreads)
+        for (int j = c0 * kChunk + threadIdx.x; j < c1 * kChunk && j < r.nvec; j += kThr)
             store_vec<kBf16>(r, out, j, make_uint4(0, 0, 0, 0));
         return;
     }
@@ -312,7 +313,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_bwd(const void* z, int64_t
     auto load = [&](int ch) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            const int j = ch * kChunk + i * kThreads + threadIdx.x;
+            const int j = ch * kChunk + i * kThr + threadIdx.x;
             if (r.whole(j)) x[i] = *r.vec(j);
             else x[i] = r.part(j);
         }
@@ -337,7 +338,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_bwd(const void* z, int64_t
         if (ch > c0) load(ch);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            const int j = ch * kChunk + i * kThreads + threadIdx.x;
+            const int j = ch * kChunk + i * kThr + threadIdx.x;
             if (j < r.nvec) store_vec<kBf16>(r, out, j, dense<kBf16>(x[i], base, cl, a));
         }
     }
@@ -523,11 +524,22 @@ inline bool whole_rows(int64_t T, int64_t V, int dtype) {
     return T >= 64 || row_vectors(V, dtype) <= kRowVecs * 1024;
 }
 
+// Many short rows take a wave each: their lists are most of the work, and one
+// wave's (in us, calls in turn from a graph, 256 / 64 threads; loss: 4096 x 1227
+// fp32 14.0 / 10.3, 4096 x 4000 17.9 / 16.5, 4096 x 2000 bf16 17.7 / 9.2, not for
+// 1024 x 4000 fp32 7.1 / 7.5; gradient: 4096 x 300 fp32 16.5 / 9.6, 4096 x 2000
+// bf16 20.9 / 15.4, not for 4096 x 2000 fp32 22.7 / 25.6).
+constexpr int kShortLoss = 1024, kShortGrad = 256;         // vectors
+inline bool short_rows(int64_t T, int64_t nvec, int most) { return T >= 2048 && nvec <= most; }
+
 template <int kBf16>
 void launch_loss(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, float it,
                  float* loss, float* stats, void* ws, hipStream_t st) {
     const int parts = row_parts(T, V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32, kWhole);
-    if (wide_rows<kBf16>(T, V, parts))
+    if (short_rows(T, row_vectors(V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32), kShortLoss))
+        hipLaunchKernelGGL((k_distill_loss<kBf16, 64>), dim3((unsigned)T), dim3(64), 0, st, z, V,
+                           ld, 1, l, it, loss, stats, (float4*)nullptr);
+    else if (wide_rows<kBf16>(T, V, parts))
         hipLaunchKernelGGL((k_distill_loss<kBf16, kWideThreads>), dim3((unsigned)T),
                            dim3(kWideThreads), 0, st, z, V, ld, 1, l, it, loss, stats, (float4*)nullptr);
     else
@@ -542,8 +554,12 @@ template <int kBf16>
 void launch_bwd(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, float it,
                 const float* stats, const float* g, void* dz, hipStream_t st) {
     const int parts = grad_parts(T, V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32);
-    hipLaunchKernelGGL(k_distill_bwd<kBf16>, dim3((unsigned)(T * parts)), dim3(kThreads), 0, st, z,
-                       V, ld, parts, l, it, stats, g, dz);
+    if (short_rows(T, row_vectors(V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32), kShortGrad))
+        hipLaunchKernelGGL((k_distill_bwd<kBf16, 64>), dim3((unsigned)T), dim3(64), 0, st, z, V, ld,
+                           1, l, it, stats, g, dz);
+    else
+        hipLaunchKernelGGL((k_distill_bwd<kBf16, kThreads>), dim3((unsigned)(T * parts)),
+                           dim3(kThreads), 0, st, z, V, ld, parts, l, it, stats, g, dz);
 }
 template <int kBf16>
 void launch_row(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, float it,

@@ -361,7 +361,8 @@ def test_distill(Q, t, v, ld, k, renorm, dtype):
     (2049, 17, 24, "bf16", 17), (2100, 700, None, "bf16", 5), (2053, 1025, 1032, "f32", 70), (2048, 16383, None, "f32", 9),
     (1030, 32771, 32776, "bf16", 20), (1025, 16405, None, "f32", 4), (515, 65539, None, "bf16", 64),
     (4200, 1027, None, "f32", 11), (4097, 8200, None, "bf16", 20), (2049, 8203, 8204, "f32", 6),
-    (513, 65537, None, "f32", 33), (512, 131081, None, "bf16", 128)])
+    (513, 65537, None, "f32", 33), (512, 131081, None, "bf16", 128),
+    (2048, 1024, None, "f32", 36), (2200, 2041, None, "bf16", 40), (2300, 4096, None, "f32", 8)])
 def test_distill_many_rows(Q, t, v, ld, dtype, k):
     """Loss and gradient of many rows in one call: rows held by each size of work-group, rows
     longer than its registers, partial vectors at both ends, rows of weight 0 in between, lists
