@@ -512,10 +512,6 @@ inline int row_threads(int64_t nvec) {
     return n;
 }
 inline int64_t row_slots(int64_t nvec) { return (int64_t)kCus * (1024 / row_threads(nvec)); }
-inline int64_t row_vectors(int64_t V, int dtype) {
-    const int per = dtype == QUADS_OUT_BF16 ? 8 : 4;
-    return (V + per - 1) / per;
-}
 // Whether loss and gradient take k_distill_row: always, but for a few rows that
 // are longer than a work-group's registers, which are split (in us, row by row
 // / split: 1 x 20000 bf16 13 / 20, 64 x 131072 bf16 22 / 21, 300 x 131072 55 /
@@ -524,13 +520,12 @@ inline bool whole_rows(int64_t T, int64_t V, int dtype) {
     return T >= 64 || row_vectors(V, dtype) <= kRowVecs * 1024;
 }
 
-// Many short rows take a wave each: their lists are most of the work, and one
-// wave's (in us, calls in turn from a graph, 256 / 64 threads; loss: 4096 x 1227
-// fp32 14.0 / 10.3, 4096 x 4000 17.9 / 16.5, 4096 x 2000 bf16 17.7 / 9.2, not for
-// 1024 x 4000 fp32 7.1 / 7.5; gradient: 4096 x 300 fp32 16.5 / 9.6, 4096 x 2000
-// bf16 20.9 / 15.4, not for 4096 x 2000 fp32 22.7 / 25.6).
-constexpr int kShortLoss = 1024, kShortGrad = 256;         // vectors
-inline bool short_rows(int64_t T, int64_t nvec, int most) { return T >= 2048 && nvec <= most; }
+// Vectors of a row that a wave takes alone (short_rows; in us, calls in turn
+// from a graph, 256 / 64 threads; loss: 4096 x 1227 fp32 14.0 / 10.3, 4096 x 4000
+// 17.9 / 16.5, 4096 x 2000 bf16 17.7 / 9.2, not for 1024 x 4000 fp32 7.1 / 7.5;
+// gradient: 4096 x 300 fp32 16.5 / 9.6, 4096 x 2000 bf16 20.9 / 15.4, not for
+// 4096 x 2000 fp32 22.7 / 25.6).
+constexpr int kShortLoss = 1024, kShortGrad = 256;
 
 template <int kBf16>
 void launch_loss(const void* z, int64_t T, int64_t V, int64_t ld, const List& l, float it,

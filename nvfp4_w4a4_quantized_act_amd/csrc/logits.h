@@ -240,6 +240,13 @@ template <int kBf16>
 inline bool wide_rows(int64_t T, int64_t V, int parts) {
     return parts == 1 && T <= 256 && V > 2 * kChunk * (int64_t)Row<kBf16>::kPer;
 }
+// Many short rows take a wave each: what is done once per row is most of the
+// work, and three of four waves would wait for it.
+inline int64_t row_vectors(int64_t V, int dtype) {
+    const int per = dtype == QUADS_OUT_BF16 ? 8 : 4;
+    return (V + per - 1) / per;
+}
+inline bool short_rows(int64_t T, int64_t nvec, int most) { return T >= 2048 && nvec <= most; }
 // Parts of a row for a gradient: nothing is joined, so that more of them are
 // better, up to what the GPU holds at once (1023 x 50001 fp32, both passes: 145
 // us with 1024 work-groups wanted, 141 with 2048, 137 with 4096, 150 with 8192).

@@ -62,14 +62,23 @@ __device__ __forceinline__ uint32_t kth_half(const uint32_t* h, int k) {
     return t;
 }
 
+// The lowest value of a half (none below -inf).
+__device__ __forceinline__ float half_bound(uint32_t t) {
+    return t <= 0x007Fu ? -INFINITY : key_value((uint64_t)(t << 16) << 32);
+}
 // A value that at least k of the work-group's values (key halves in `top`)
 // reach: the k-th largest half, rounded down.  Every wave finds it by itself.
 __device__ __forceinline__ float kth_bound(const uint16_t* top, int k) {
     const uint2 w = reinterpret_cast<const uint2*>(top)[threadIdx.x & 63];
     const uint32_t h[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
-    const uint32_t t = kth_half<4>(h, k);
-    // the lowest value of that half (none below -inf)
-    return t <= 0x007Fu ? -INFINITY : key_value((uint64_t)(t << 16) << 32);
+    return half_bound(kth_half<4>(h, k));
+}
+// The same from one wave's values in registers.
+__device__ __forceinline__ float kth_bound(const float (&m)[4], int k) {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = value_key(m[i]) >> 16;
+    return half_bound(kth_half<4>(h, k));
 }
 
 // A thread's maximum, or that of kThr / kThreads neighbours, into `top`.
@@ -141,8 +150,10 @@ __device__ __forceinline__ void keep_top(Cand& c, int n, int k) {
         if (n > kThr) {
 #pragma unroll
             for (int i = 1; i < kCand / kThr; ++i)
+                if (kThr >= 256 || i * kThr < n) {
 #pragma unroll
-                for (int b = 0; b < 8; ++b) place[i] += x[b] > mine[i] ? 1 : 0;
+                    for (int b = 0; b < 8; ++b) place[i] += x[b] > mine[i] ? 1 : 0;
+                }
         }
     }
     __syncthreads();
@@ -186,7 +197,7 @@ __device__ __forceinline__ Token load_token(const Out& o, const Row<kBf16>& r, i
 }
 
 // The outputs of row t from its statistics and its n largest entries (thread
-// 0 and the first topk; key in LDS, sorted).  n < topk: no further entry is
+// 0, and all for the alternatives; key in LDS, sorted).  n < topk: no further entry is
 // above -inf, so that the masked ones of lowest index follow.
 template <int kBf16>
 __device__ __forceinline__ void finish(const Out& o, const Row<kBf16>& r, int64_t t, const Stat& a,
@@ -218,11 +229,11 @@ __device__ __forceinline__ void finish(const Out& o, const Row<kBf16>& r, int64_
         __syncthreads();
         n = o.topk;
     }
-    if ((int)threadIdx.x < o.topk) {
-        const int64_t at = t * o.topk + threadIdx.x;
+    for (int i = threadIdx.x; i < o.topk; i += blockDim.x) {
+        const int64_t at = t * o.topk + i;
         const bool have = n >= o.topk;         // else any indices
-        o.top_id[at] = have ? key_index(key[threadIdx.x]) : (int)threadIdx.x;
-        o.top_logp[at] = have ? (float)ln_p(key_value(key[threadIdx.x]), a.m, ls, o.it) : NAN;
+        o.top_id[at] = have ? key_index(key[i]) : i;
+        o.top_logp[at] = have ? (float)ln_p(key_value(key[i]), a.m, ls, o.it) : NAN;
     }
 }
 
@@ -236,16 +247,21 @@ __device__ __forceinline__ void finish(const Out& o, const Row<kBf16>& r, int64_
 // (entries of the first chunk count from the bound on, later ones only above
 // it, as their indices are higher), so that a random row yields about topk (1
 // + log2 of the chunks) candidates and most vectors are compared with one
-// number.  The candidates are sorted once, at the end.  Where there were more
+// number (256 maxima: one a thread, one of four threads in a wide work-group,
+// four a thread, in registers, in a single wave).  The candidates are sorted
+// once, at the end.  Where there were more
 // than there is room for (equal or rising entries) the part is read again,
-// 256 entries at a time, the candidates cut to the topk largest in between.
+// up to 256 entries at a time, the candidates cut to the topk largest in between.
 template <int kBf16, bool kEntropy, bool kTop, int kVecs, int kThr = kThreads>
 __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int64_t ld, int parts,
                                                   Out o, Parts p) {
     constexpr int kPer = Row<kBf16>::kPer;
     constexpr int kChunk = kThr * kVecs;
+    constexpr bool kOneWave = kThr == 64;
+    constexpr int kRead = kThr < kThreads ? kThr : kThreads;
     __shared__ Stat s_stat[kThr / 64];
-    __shared__ Cand c;
+    __shared__ __align__(16) char s_cand[kTop ? sizeof(Cand) : 16];
+    Cand& c = *reinterpret_cast<Cand*>(s_cand);
     const int64_t t = blockIdx.x / (unsigned)parts;
     const int part = (int)(blockIdx.x % (unsigned)parts);
     const Row<kBf16> r(z, t, ld, V);
@@ -278,6 +294,9 @@ __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int6
     Stat a = {-INFINITY, 0.0f, 0.0f};
     float bound = -INFINITY;                   // candidates reach it
     int fresh = 0;
+    float most[kVecs];                         // one wave: maxima of its vectors
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) most[i] = -INFINITY;
     if (kTop) {
         if (threadIdx.x == 0) c.n = 0;
         __syncthreads();
@@ -307,7 +326,11 @@ __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int6
             }
         if (kTop) {
             const int nth = ch - c0;
-            if (nth == 0) {
+            if constexpr (kOneWave) {
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) most[i] = fmaxf(most[i], vm[i]);
+                if (nth == 0) bound = kth_bound(most, topk);
+            } else if (nth == 0) {
                 set_top<kThr>(c.top[0], m);
                 __syncthreads();
                 bound = kth_bound(c.top[0], topk);
@@ -331,10 +354,14 @@ __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int6
             } else if ((nth & (nth + 1)) == 0 && ch + 1 < c1) {
                 // (two sets of maxima in turn: a wave writes the second next
                 // one only after all have read this one)
-                fresh ^= 1;
-                set_top<kThr>(c.top[fresh], m);
-                __syncthreads();
-                bound = fmaxf(bound, next_up(kth_bound(c.top[fresh], topk)));
+                if constexpr (kOneWave) {
+                    bound = fmaxf(bound, next_up(kth_bound(most, topk)));
+                } else {
+                    fresh ^= 1;
+                    set_top<kThr>(c.top[fresh], m);
+                    __syncthreads();
+                    bound = fmaxf(bound, next_up(kth_bound(c.top[fresh], topk)));
+                }
             }
         }
     }
@@ -351,13 +378,13 @@ __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int6
             uint64_t over = 0;                 // the topk-th candidate, once cut
             const int v0 = max(r.index(c0 * kChunk, 0), 0);
             const int v1 = min((int64_t)r.V, (int64_t)c1 * kChunk * kPer - r.shift);
-            for (int v = v0; v < v1; v += kThreads * 8) {
+            for (int v = v0; v < v1; v += kRead * 8) {
                 uint64_t k[8];
                 bool any = false;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int at = v + i * kThreads + (int)threadIdx.x;
-                    const bool mine = kThr == kThreads || threadIdx.x < kThreads;
+                    const int at = v + i * kRead + (int)threadIdx.x;
+                    const bool mine = kThr == kRead || threadIdx.x < kRead;
                     const float x = mine && at < v1 ? r.entry(at) : -INFINITY;
                     k[i] = x > -INFINITY ? rank_key(x, (uint32_t)at) : 0;
                     any = any || k[i] > over;
@@ -365,7 +392,7 @@ __global__ __launch_bounds__(kThr) void k_logprob(const void* z, int64_t V, int6
                 if (!__syncthreads_or(any)) continue;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    if (n + kThreads > kCand) {
+                    if (n + kRead > kCand) {
                         keep_top<kThr>(c, n, topk);
                         over = c.n == topk ? c.key[topk - 1] : 0;
                         __syncthreads();
@@ -524,6 +551,12 @@ __global__ __launch_bounds__(kThreads) void k_logprob_bwd(const void* z, int64_t
 // their sums take four times the vectors at once (in us, calls in turn, 4 / 16
 // vectors: 400 x 30000 bf16 19.2 / 16.2; not for 800 x 30000 fp32 28.5 / 30.6).
 constexpr int kVecsFew = 16;
+// Vectors of a row that a wave takes alone (short_rows; in us, calls in turn
+// from a graph, 256 / 64 threads; no alternatives: 4096 x 2000 fp32 13.9 / 9.9,
+// 4096 x 300 bf16 18.1 / 8.2, not for 4096 x 4000 fp32 15.0 / 15.7; top 8: 4096 x
+// 2000 fp32 23.6 / 17.2, 2048 x 2000 bf16 16.7 / 10.1; top 128: 4096 x 2000 fp32
+// 34.8 / 31.3, not for 2048 rows 20.7 / 24.3).
+constexpr int kShortSum = 512;
 template <int kBf16>
 inline bool few_rows(int64_t T, int64_t V, int parts) {
     return parts == 1 && T <= 512 && V > 2 * kChunk * (int64_t)Row<kBf16>::kPer;
@@ -533,7 +566,11 @@ template <int kBf16, bool kEntropy, bool kTop>
 void launch_rows(const void* z, int64_t T, int64_t V, int64_t ld, int parts, const Out& o,
                  const Parts& p, hipStream_t st) {
     const dim3 grid((unsigned)(T * parts)), block(kThreads);
-    if (wide_rows<kBf16>(T, V, parts))
+    if (short_rows(o.topk > 64 ? T / 2 : T,
+                   row_vectors(V, kBf16 ? QUADS_OUT_BF16 : QUADS_OUT_F32), kShortSum))
+        hipLaunchKernelGGL((k_logprob<kBf16, kEntropy, kTop, kVecs, 64>), grid, dim3(64), 0, st, z,
+                           V, ld, 1, o, p);
+    else if (wide_rows<kBf16>(T, V, parts))
         hipLaunchKernelGGL((k_logprob<kBf16, kEntropy, kTop, kVecs, kWideThreads>), grid,
                            dim3(kWideThreads), 0, st, z, V, ld, 1, o, p);
     else if (few_rows<kBf16>(T, V, parts))

@@ -154,7 +154,8 @@ def check_grad(Q, z, zr, it, ids, r, e, b, dtype, which="both", out=None):
 
 SHAPES = [(1, 1, None), (1, 7, None), (7, 64, None), (6, 257, 264), (9, 1000, None),
           (6, 4097, None), (300, 515, None), (2, 16385, 16392), (33, 32768, None),
-          (3, 50001, None), (2, 131072, None), (1, 300001, None)]
+          (3, 50001, None), (2, 131072, None), (1, 300001, None),
+          (2050, 515, 520), (2048, 2048, None), (4100, 37, None)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -171,7 +172,8 @@ def test_logprob_and_gradient(Q, t, v, ld, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("t,v,masked", [(8, 1000, 0.5), (6, 20000, 0.999), (9, 70001, 0.3)])
+@pytest.mark.parametrize("t,v,masked", [(8, 1000, 0.5), (6, 20000, 0.999), (9, 70001, 0.3),
+                                        (2100, 1001, 0.97)])
 def test_masked_rows(Q, t, v, masked, dtype):
     """-inf entries, rows with fewer unmasked entries than alternatives, rows with none."""
     z, zr = make(t, v, dtype, seed=4, masked=masked, empty=(0, 5))
@@ -189,7 +191,8 @@ def test_one_gradient_and_in_place(Q, which):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("t,v", [(1, 40000), (300, 40000), (3, 200000), (5, 30000), (600, 20000)])
+@pytest.mark.parametrize("t,v", [(1, 40000), (300, 40000), (3, 200000), (5, 30000), (600, 20000),
+                                 (4096, 2000)])
 @pytest.mark.parametrize("kind", ["constant", "two", "rising", "falling", "zeros", "late"])
 def test_alternatives_in_hard_rows(Q, kind, t, v, dtype):
     """Ties by index (signed zeros are equal), ordered rows, the largest entries last."""
@@ -214,7 +217,7 @@ def test_alternatives_in_hard_rows(Q, kind, t, v, dtype):
 
 @pytest.mark.parametrize("k", [1, 2, 3, 31, 64, 65, 128])
 def test_counts_of_alternatives(Q, k):
-    for t, v in ((2, 9000), (2, k), (400, 2049)):
+    for t, v in ((2, 9000), (2, k), (400, 2049), (4096, 2000)):
         z, zr = make(t, v, "bf16", seed=k, scale=1.0)
         check_logprob(Q, z, zr, 1.0, k, want_entropy=False)
 
@@ -237,7 +240,7 @@ def test_large_and_small_logits(Q):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_that_are_not_numbers(Q, bad, dtype):
     """NaN or +inf spoils its own row only; alternatives stay distinct indices of the row."""
-    for t, v in ((3, 700), (3, 70001), (300, 5000), (5, 30000)):
+    for t, v in ((3, 700), (3, 70001), (300, 5000), (5, 30000), (2048, 1500)):
         z, zr = make(t, v, dtype, seed=3)
         z[1, v // 2] = bad
         ids = torch.zeros(t, dtype=torch.int32, device=DEV)
