@@ -19,6 +19,11 @@ runs in the library, and so do the losses on its logits: the log-probabilities
 of the rollout's tokens with the entropy (`token_logprobs`, the quantity that
 the method aligns between rollout and learner) and the distillation from
 another model's top alternatives (`distill_loss`).
+
+Forward and backward of the losses may be captured into a HIP graph.  As with
+any of torch's operators, take the captured gradients with torch.autograd.grad,
+or call .backward() only while no eager result of the same leaves is alive:
+torch would wait, inside the capture, for the stream of the eager one.
 """
 
 import torch

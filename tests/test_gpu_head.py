@@ -672,3 +672,35 @@ def test_graph_replays(Q, t, v):
         want = step(new)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_autograd_in_a_graph(Q, qat):
+    """Forward and gradient of the autograd functions captured on leaves of their own, replayed
+    on new logits with eager work between the replays."""
+    t, v = 40, 9001
+    ids = torch.arange(t, dtype=torch.int32, device=DEV)
+    tv = torch.zeros((t, 4), device=DEV)
+    ti = torch.randint(0, v, (t, 4), generator=torch.Generator().manual_seed(1)).int().to(DEV)
+    g = torch.linspace(-1, 1, t, device=DEV)
+
+    def step(x):
+        lp, h = qat.token_logprobs(x, ids, 0.9)
+        loss = qat.distill_loss(x, tv, ti)
+        return [lp.detach(), h.detach(), loss.detach(),
+                *torch.autograd.grad([lp, h, loss], [x], [g, 0.5 * g, g])]
+    step(make(t, v, "f32", seed=1)[0].requires_grad_())
+    z = make(t, v, "f32", seed=2)[0].requires_grad_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(z)
+    for seed in (5, 6, 7):
+        new = make(t, v, "f32", seed=seed)[0]
+        with torch.no_grad():
+            z.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [a.clone() for a in held]
+        want = step(new.requires_grad_())
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
