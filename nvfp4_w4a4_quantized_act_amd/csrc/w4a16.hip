@@ -541,8 +541,9 @@ extern "C" int quads_moe_w4a16_gemv(const uint16_t* x, const int32_t* row_token,
     if (epilogue == QUADS_EPI_SWIGLU && N % 2) return QUADS_ESHAPE;
     if (offsets == nullptr && E != 1) return QUADS_EINVAL;
     if (rows == 0) return QUADS_OK;
-    if (!ok_opt_ptr(offsets) || !ok_opt_ptr(row_token)) return QUADS_EINVAL;
-    if (!ok_ptr(x) || !ok_ptr(w_nib) || !ok_ptr(w_scale) || !ok_ptr(w_ts) || !ok_ptr(out))
+    if ((offsets != nullptr && !ok_ptr4(offsets)) || (row_token != nullptr && !ok_ptr4(row_token)))
+        return QUADS_EINVAL;
+    if (!ok_ptr(x) || !ok_ptr(w_nib) || !ok_ptr(w_scale) || !ok_ptr4(w_ts) || !ok_ptr(out))
         return QUADS_EINVAL;
     const size_t need = quads_moe_w4a16_gemv_ws(rows, K, E, N);
     if (ws_bytes < need || (need > 0 && !ok_ptr(ws))) return QUADS_EWORKSPACE;
