@@ -58,7 +58,7 @@ extern "C" {
  * The error is below (176 + K / 512) 2^-24 sum |x w| per output element plus
  * the rounding to bf16, and 2^-28 times the largest |x| of a row's 512-channel
  * block times sum |w| where a block spans more than 28 binary orders.
- * Workspace: quads_moe_w4a16_gemv_ws bytes (0: NULL is allowed).
+ * Workspace: none (quads_moe_w4a16_gemv_ws is 0 for every size, ws is not used).
  */
 size_t quads_moe_w4a16_gemv_ws(int64_t rows, int64_t K, int32_t E, int64_t N);
 int quads_moe_w4a16_gemv(const uint16_t* x, const int32_t* row_token, int64_t rows, int64_t K,

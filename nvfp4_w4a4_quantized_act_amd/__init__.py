@@ -667,11 +667,8 @@ def quads_moe_w4a16_gemv(x, w, n, rows=None, offsets=None, row_token=None, epilo
     elif (out.dtype not in ((dt,) if out_dtype == OUT_F32 else (torch.int16, torch.bfloat16))
           or tuple(out.shape) != (rows, ncols) or out.device != dev or not out.is_contiguous()):
         raise ValueError("out must be a dense tensor of the call's type, shape and device")
-    nws = lib().quads_moe_w4a16_gemv_ws(rows, kd, e, n)
-    ws = _scratch(nws, dev)
     _call("quads_moe_w4a16_gemv", dev, _at(x), _at(row_token), rows, kd, _at(w_nib),
-          _at(w_scale), _at(w_ts), _at(offsets), e, n, epilogue, out_dtype, _at(out),
-          _at(ws), nws)
+          _at(w_scale), _at(w_ts), _at(offsets), e, n, epilogue, out_dtype, _at(out), None, 0)
     return out
 
 
