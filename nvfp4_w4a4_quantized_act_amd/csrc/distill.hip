@@ -329,7 +329,9 @@ __global__ __launch_bounds__(kThr) void k_distill_bwd(const void* z, int64_t V, 
     load(c0);
     const Teacher q = teacher(listed, r.V, it, l.renorm);
     const float base = stat_base(m), cl = it * kLog2e, inv = recip_sum(ls);
-    // the part's entries [v0, v1), their gradients parked before any store
+    // the part's entries [v0, v1), their gradients parked before any store.  In
+    // place, a logit that lies in another part may already be its gradient: what
+    // is worked out from it is not used (patch), and nothing else reads it.
     const int v0 = c0 ? r.index(c0 * kChunk, 0) : 0, v1 = r.index(c1 * kChunk, 0);
     if (threadIdx.x < 64) {
         float zq[2];
@@ -365,6 +367,9 @@ __device__ __forceinline__ void st_stream16(char* p, const uint4& q) {
 // of the one whose gradient was just stored, so that loads, stores and
 // arithmetic overlap although a CU holds one row at a time.  The partial
 // vectors at a row's ends are in one more register vector of threads 0 and 1.
+// With 1024 threads the compiler spills up to 5 of 128 registers (24 bytes of
+// scratch a lane): stored before the loop over the rows, read back once or twice
+// per row in the joins and the list's work, not in the passes over the vectors.
 //
 // kLong (rows beyond the registers): what is read or written once is marked
 // as not to be kept, so that the cache keeps the part that is read again (1000
@@ -518,9 +523,14 @@ inline int row_threads(int64_t nvec) {
 }
 inline int64_t row_slots(int64_t nvec) { return (int64_t)kCus * (1024 / row_threads(nvec)); }
 // Whether loss and gradient take k_distill_row: always, but for a few rows that
-// are longer than a work-group's registers, which are split (in us, row by row
-// / split: 1 x 20000 bf16 13 / 20, 64 x 131072 bf16 22 / 21, 300 x 131072 55 /
-// 49, 600 x 131072 84 / 101, 64 x 100001 fp32 23 / 25).
+// are longer than a work-group's registers, which are split.  In us, row by row
+// / split: 1 x 20000 bf16 13 / 20, 64 x 100001 fp32 23 / 25, 64 x 140001 30 / 37,
+// 300 x 140001 99 / 119, 600 x 300001 410 / 485; bf16 64 x 140001 30 / 26, 300 x
+// 140001 70 / 68, 600 x 140001 109 / 119.  A row by row form with fewer rows than
+// CUs leaves CUs without one, and reads what is beyond the registers twice: from
+// about 300000 entries on the split would be the better one (fp32 64 x 300001 86
+// / 62, 64 x 1000003 300 / 183, 300 x 1000003 894 / 802; bf16 128 x 1000003 207 /
+// 170), which the rule, made for vocabularies up to 131072, does not see.
 inline bool whole_rows(int64_t T, int64_t V, int dtype) {
     return T >= 64 || row_vectors(V, dtype) <= kRowVecs * 1024;
 }

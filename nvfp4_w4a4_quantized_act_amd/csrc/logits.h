@@ -219,10 +219,16 @@ inline int split_row(int64_t T, int64_t V, int dtype, int64_t groups) {
     return p < 1 ? 1 : (int)p;
 }
 // Parts of a row for sums, which a second kernel joins: not for rows of up to
-// `whole` entries, whose work-group is done before a second launch would be
-// (in us with one work-group a row / split, calls in turn: 100 x 65536 fp32 12
-// / 17; with alternatives 1 x 32768 fp32 17.5 / 20, 1 x 65536 bf16 21 / 20, 1 x
-// 131072 30 / 20).
+// `whole` entries, whose work-group is done before the host has made a second
+// launch.  In us with one work-group a row (wide_rows) / split, calls in turn,
+// and in brackets device time from a graph, fp32: no alternatives 1 x 65536
+// 11.6 / 16.5 (7.9 / 4.7), 64 x 65536 11.9 / 16.8 (8.7 / 8.3), 1 x 131072 12.5 /
+// 16.7 (12.4 / 4.8), 64 x 131072 15.0 / 16.8 (15.0 / 11.2); top 20, 1 x 32768
+// 15.0 / 20.0 (10.6 / 9.9), 1 x 50001 17.7 / 19.5 (17.1 / 10.3), 64 x 65536 18.2
+// / 19.9 (17.9 / 15.3), 64 x 131072 26.8 / 21.0 (26.6 / 20.6).  From a graph
+// fewer rows than about 64 gain by a split from 32768 entries on, and 256 rows
+// lose by it at any length (65536 with top 20 22 / 26, 131072 without 27 / 30):
+// the rule looks at neither.
 constexpr int kWhole = 65536, kWholeTop = 32768;
 inline int row_parts(int64_t T, int64_t V, int dtype, int whole) {
     if (V <= whole) return 1;

@@ -35,8 +35,11 @@
 // loads the 8 of chunk h, and the four lanes of a feature exchange them in
 // registers (row swaps), so that each has its two of every chunk.
 //   The activations, few and read by every wave, are in LDS: all of a unit's
-// channels, brought once, where they fit, else as many blocks as do, again for
-// every step.
+// channels, brought once, where they fit (K <= 4608 for 16 rows, 9216 for 8), else
+// as many blocks as do, again for every step.  A wave then takes its features
+// alone, and there are at most outputs / 128 work-groups, too few for the GPU at
+// ordinary N: 16 x 4608 x 4096 takes 16.5 us and 16 x 5120 x 4096 35, 9 x 8192 x
+// 4096 19 and 10 x 8192 x 4096 50, 16 x 7168 x 7168 48 (0.6 TB/s).
 //
 // Work-groups are resident ones, as many as the GPU holds: a unit (up to 16 kRt
 // rows of an expert) has `slabs` of them, and each takes an equal range of its
@@ -508,7 +511,11 @@ int launch(Args g, hipStream_t st) {
 // otherwise serves the second read.  In us with 16 / 32 rows: 40 x 2048 x
 // 32768 30.6 / 28.0; gate/up of 128 experts of 1536 x 2048, top 8, 256 tokens
 // 71 / 62, 128 tokens 52 / 60; 16 such experts, 64 tokens 29 / 36; 64 x 4096 x
-// 4096 17.6 / 38.  64 rows were never better than both.
+// 4096 17.6 / 38.  64 rows were never better than both.  (The form of 32 rows
+// spills 5 registers, with SwiGLU 1: stored before the loop over the steps, read
+// back at a step's results.)  Either way a unit of rows decodes the weights for
+// itself after it has brought all of its activations, so that 17 to 64 rows of a
+// matrix take 3 to 9 times what their bytes do.
 template <int kEpi>
 int dispatch(const Args& g, hipStream_t st) {
     const double bytes = 0.5625 * g.E * g.N * g.K;
