@@ -110,7 +110,10 @@ __device__ __forceinline__ void store_vec(const Row<kBf16>& r, char* at, int j, 
 // Running statistics of some entries: m = max z, and with d = c (z - m),
 // c = it log2(e):  s = sum 2^d, u = sum 2^d d.  Rescaled when m rises, one
 // pass over the data.  Entries of -inf add nothing; m = -inf, s = 0 while
-// there is no other.
+// there is no other.  c is one fp32 number, up to 7e-8 off: every d is off by
+// that share of itself and ln s by at most that times sum p |d| (1e-8 of it at
+// it = 1, 3e-8 at 1.3).  The rest of c would be one more operation per entry of
+// kernels whose vector units are up to 89% busy.
 struct Stat {
     float m, s, u;
 };
