@@ -3,8 +3,10 @@
 Argument marshalling only: every step of the path runs in the library's HIP
 kernels.  PyTorch supplies device memory (outputs and workspace are torch
 tensors) and the current stream.  The functions carry the C ABI's names; see
-include/quads.h and include/quads_head.h (the output head: W4A16 product, token
-log-probabilities, distillation) for the exact contract of each call.
+include/quads.h, include/quads_head.h (the output head: W4A16 product, token
+log-probabilities, distillation) and include/quads_block.h (the layer around the
+experts: residual and norm, routing, tokens in expert order) for the exact
+contract of each call.
 
 bf16 tensors may be passed as torch.bfloat16, torch.int16 or torch.uint16
 (bit patterns).  Results are returned as torch tensors on the input's device.
@@ -26,11 +28,14 @@ __all__ = [
     "quads_mx_quantize", "quads_moe_mx_gemm",
     "quads_moe_w4a16_gemv", "quads_token_logprob", "quads_token_logprob_backward",
     "quads_topk_distill", "quads_topk_distill_backward", "quads_topk_distill_grad", "TOP_MAX",
-    "EPI_NONE", "EPI_SWIGLU", "OUT_F32", "OUT_BF16", "MX_FP8", "MX_FP4",
+    "quads_rmsnorm", "quads_rmsnorm_backward", "quads_rmsnorm_amax_groups", "quads_moe_route",
+    "quads_moe_route_backward", "quads_moe_sort", "quads_moe_unsort", "quads_moe_unsort_backward",
+    "EPI_NONE", "EPI_SWIGLU", "OUT_F32", "OUT_BF16", "OUT_MX_FP8", "MX_FP8", "MX_FP4",
 ]
 
 EPI_NONE, EPI_SWIGLU = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
+OUT_MX_FP8 = 2                                       # quads_rmsnorm only
 MX_FP8, MX_FP4 = 0, 4
 TOP_MAX = 128                                        # alternatives per row
 
@@ -43,6 +48,7 @@ _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
+_D = ctypes.c_double
 _INT = ctypes.c_int
 _SIGNATURES = {
     "quads_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -108,6 +114,19 @@ _SIGNATURES = {
     "quads_topk_distill_grad_ws": (_SZ, [_I64, _I64, _I32]),
     "quads_topk_distill_grad": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _I32, _P, _F, _INT,
                                        _P, _P, _P, _SZ, _P]),
+    "quads_rmsnorm_amax_groups": (_I64, [_I64, _I64]),
+    "quads_rmsnorm": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _INT, _I64, _P, _INT, _D, _P, _P,
+                             _INT, _P, _P, _I64, _P]),
+    "quads_rmsnorm_backward_ws": (_SZ, [_I64, _I64, _INT]),
+    "quads_rmsnorm_backward": (_INT, [_P, _INT, _P, _INT, _I64, _I64, _I64, _P, _INT, _D, _P, _P,
+                                      _INT, _P, _P, _P, _SZ, _P]),
+    "quads_moe_route": (_INT, [_P, _INT, _I64, _I32, _I64, _I32, _INT, _P, _P, _P]),
+    "quads_moe_route_backward": (_INT, [_P, _INT, _I64, _I32, _I64, _P, _P, _P, _I32, _INT, _P,
+                                        _P]),
+    "quads_moe_sort": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I32, _I64, _P, _P]),
+    "quads_moe_unsort": (_INT, [_P, _INT, _I64, _P, _P, _I64, _I32, _I64, _P, _INT, _P]),
+    "quads_moe_unsort_backward": (_INT, [_P, _INT, _P, _INT, _I64, _P, _P, _I64, _I32, _I64, _P,
+                                         _P, _P]),
 }
 
 
@@ -763,3 +782,240 @@ def quads_topk_distill_grad(logits, t_val, t_id, weight=None, inv_temp=1.0, reno
     _call("quads_topk_distill_grad", dev, _at(z), code, t, v, ld, _at(t_val), _at(t_id), k,
           _at(weight), inv_temp, int(renorm), _at(loss), _at(out), _at(ws), nws)
     return loss, out
+
+
+# ---- the layer around the experts (include/quads_block.h) ---------------------
+# Checked as the output head's calls are.  bf16 inputs may be torch.bfloat16, int16 or uint16
+# bits; what is new is returned as torch.bfloat16, a gradient or a sum in its input's type.
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _rows(name, t, shape=None, dev=None):
+    """(t, dtype code, row stride) of a 2-D tensor with dense, 16-byte aligned rows; copied if
+    it is not one already.  Any row stride is taken as it is."""
+    if dev is None:
+        dev = _gpu(name, t)
+    elif not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype == torch.bfloat16:
+        code = OUT_BF16
+    elif t.dtype == torch.float32:
+        code = OUT_F32
+    elif t.dtype in (torch.int16, torch.uint16):
+        code = OUT_BF16
+    else:
+        raise TypeError(f"{name} must be float32 or bf16 (torch.bfloat16, int16 or uint16 bits)")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have the shape "
+                         f"{'[rows, channels]' if shape is None else tuple(shape)}, "
+                         f"not {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, not on {t.device}")
+    n, h = t.shape
+    if t.is_contiguous():
+        if t.data_ptr() % 16:
+            t = t.detach().clone(memory_format=torch.contiguous_format)
+        return t, code, h
+    if n and h and (t.stride(1) != 1 or (n > 1 and not h <= t.stride(0) < 2**31)
+                    or t.data_ptr() % 16):
+        t = t.detach().clone(memory_format=torch.contiguous_format)
+    return t, code, (t.stride(0) if n > 1 else h)
+
+
+def _dense(name, t, shape, dev):
+    """(t, dtype code) of dense rows."""
+    t, code, ld = _rows(name, t, shape, dev)
+    if ld != shape[1]:
+        t = t.detach().clone(memory_format=torch.contiguous_format)
+    return t, code
+
+
+def _weight(weight, h, dev):
+    if weight is None:
+        return None, OUT_F32
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in (
+            torch.float32, torch.bfloat16, torch.int16, torch.uint16):
+        raise TypeError("weight must be float32 or bf16 (torch.bfloat16, int16 or uint16 bits)")
+    w = _want("weight", weight, weight.dtype, (h,), dev)
+    if w.data_ptr() % 16:
+        w = w.detach().clone()
+    return w, OUT_F32 if w.dtype == torch.float32 else OUT_BF16
+
+
+def quads_rmsnorm_amax_groups(t, h):
+    """Partial-maximum slots of a quads_rmsnorm call of these sizes."""
+    return int(lib().quads_rmsnorm_amax_groups(t, h))
+
+
+def quads_rmsnorm(x, weight=None, eps=1e-6, residual=None, out_dtype=OUT_BF16, want_sum=True,
+                  want_amax=False):
+    """Residual addition and root-mean-square norm of the rows of x [T, H] -> dict of y (fp32 or
+    bf16), or codes uint8 [T, H] and scales uint8 [T, H/32] (OUT_MX_FP8); sum [T, H] in the
+    residual's type (with a residual, if wanted); amax_part int32 [groups] (OUT_BF16, if
+    wanted)."""
+    x, xt, ldx = _rows("x", x)
+    dev = x.device
+    t, h = x.shape
+    rt, ldr = OUT_F32, h
+    out = {}
+    total = None
+    if residual is not None:
+        residual, rt, ldr = _rows("residual", residual, x.shape, dev)
+        if want_sum:
+            total = out["sum"] = torch.empty(t, h, dtype=residual.dtype, device=dev)
+    weight, wt = _weight(weight, h, dev)
+    scales = part = None
+    groups = 0
+    if out_dtype == OUT_MX_FP8:
+        y = out["codes"] = torch.empty(t, h, dtype=torch.uint8, device=dev)
+        scales = out["scales"] = torch.empty(t, h // 32, dtype=torch.uint8, device=dev)
+    else:
+        y = out["y"] = torch.empty(t, h, dtype=_FLOATS[1 if out_dtype == OUT_BF16 else 0],
+                                   device=dev)
+    if want_amax:
+        groups = quads_rmsnorm_amax_groups(t, h)
+        part = out["amax_part"] = torch.empty(groups, dtype=torch.int32, device=dev)
+        if not groups:
+            part = None
+    _call("quads_rmsnorm", dev, _at(x), xt, t, h, ldx, _at(residual), rt, ldr, _at(weight), wt,
+          eps, _at(total), _at(y), out_dtype, _at(scales), _at(part), groups)
+    return out
+
+
+def quads_rmsnorm_backward(g, h, weight=None, eps=1e-6, g_sum=None, dx_dtype=None,
+                           want_dweight=True):
+    """Gradient of quads_rmsnorm from the gradient g [T, H] of its y and g_sum (or None) of its
+    sum -> (dx, dres, dweight).  h is the call's sum (x without a residual); dx has the type
+    dx_dtype (h's), dres is dx unless the types differ."""
+    h, ht, ldh = _rows("h", h)
+    dev = h.device
+    t, n = h.shape
+    g, gt = _dense("g", g, h.shape, dev)
+    weight, wt = _weight(weight, n, dev)
+    if g_sum is not None:
+        if not isinstance(g_sum, torch.Tensor) or g_sum.dtype != h.dtype:
+            raise TypeError("g_sum must be a tensor of h's type")
+        g_sum, _ = _dense("g_sum", g_sum, h.shape, dev)
+    if dx_dtype is None:
+        dx_dtype = h.dtype
+    elif dx_dtype not in (torch.float32, torch.bfloat16, torch.int16, torch.uint16):
+        raise TypeError("dx_dtype must be float32 or bf16")
+    dt = OUT_F32 if dx_dtype == torch.float32 else OUT_BF16
+    dx = torch.empty(t, n, dtype=dx_dtype, device=dev)
+    dres = torch.empty(t, n, dtype=h.dtype, device=dev) if dt != ht else None
+    dw = torch.empty_like(weight) if want_dweight and weight is not None else None
+    nws = lib().quads_rmsnorm_backward_ws(t, n, int(dw is not None))
+    ws = _scratch(nws, dev)
+    _call("quads_rmsnorm_backward", dev, _at(g), gt, _at(h), ht, t, n, ldh, _at(weight), wt, eps,
+          _at(g_sum), _at(dx), dt, _at(dres), _at(dw), _at(ws), nws)
+    return dx, (dx if dres is None else dres), dw
+
+
+def quads_moe_route(logits, topk, renorm=True):
+    """The topk experts with the largest logits [T, E] of each token -> (ids int32 [T, topk],
+    weights fp32 [T, topk]): softmax over all experts, or over the chosen ones (renorm)."""
+    z, code, ld = _rows("logits", logits)
+    t, e = z.shape
+    if not 1 <= topk <= e:
+        raise ValueError(f"topk must be in 1 .. {e}")
+    dev = z.device
+    ids = torch.empty(t, topk, dtype=torch.int32, device=dev)
+    w = torch.empty(t, topk, dtype=torch.float32, device=dev)
+    _call("quads_moe_route", dev, _at(z), code, t, e, ld, topk, int(renorm), _at(ids), _at(w))
+    return ids, w
+
+
+def quads_moe_route_backward(logits, ids, w, g, renorm=True):
+    """Gradient of the logits from the gradient g fp32 [T, topk] of quads_moe_route's weights;
+    ids and w are that call's."""
+    z, code, ld = _rows("logits", logits)
+    t, e = z.shape
+    dev = z.device
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be a tensor [T, topk]")
+    k = ids.shape[1]
+    ids = _want("ids", ids, torch.int32, (t, k), dev)
+    w = _want("w", w, torch.float32, (t, k), dev)
+    g = _want("g", g, torch.float32, (t, k), dev)
+    dz = torch.empty(t, e, dtype=z.dtype, device=dev)
+    _call("quads_moe_route_backward", dev, _at(z), code, t, e, ld, _at(ids), _at(w), _at(g), k,
+          int(renorm), _at(dz))
+    return dz
+
+
+def _slots(pos, topk, topk_w, dev):
+    """(pos, topk_w, T) of T tokens with topk slots each."""
+    if not isinstance(pos, torch.Tensor) or pos.dtype != torch.int32:
+        raise TypeError("pos must be an int32 tensor")
+    if not 1 <= topk <= 64:
+        raise ValueError("topk must be in 1 .. 64")
+    n = pos.numel()
+    if n % topk:
+        raise ValueError("pos must have topk entries per token")
+    pos = _want("pos", pos, torch.int32, pos.shape, dev)
+    return pos, _want("topk_w", topk_w, torch.float32, (n // topk, topk), dev), n // topk
+
+
+def _packed(rows, n, h, dtype, dev):
+    """The packed rows of a call that writes the rows which pos names: every one (rows None: pos
+    is a permutation of them), or some, and the others are 0."""
+    if rows is None:
+        return n, torch.empty(n, h, dtype=dtype, device=dev)
+    if rows < 0:
+        raise ValueError("rows must not be negative")
+    return rows, torch.zeros(rows, h, dtype=dtype, device=dev)
+
+
+def quads_moe_sort(x, pos, topk, rows=None):
+    """Tokens x [T, H] in packed order: out[pos[t * topk + s]] = x[t] -> [rows, H] in x's type.
+    rows None: T * topk, and pos a permutation of them, as quads_moe_pack writes it.  With rows
+    given, slots whose pos is outside [0, rows) are left out, and rows without a slot are 0."""
+    x, code, ldx = _rows("x", x)
+    dev = x.device
+    t, h = x.shape
+    pos, _, n = _slots(pos, topk, None, dev)
+    if n != t:
+        raise ValueError("pos must have topk entries per row of x")
+    rows, out = _packed(rows, t * topk, h, x.dtype, dev)
+    _call("quads_moe_sort", dev, _at(x), code, t, h, ldx, _at(pos), topk, rows, _at(out))
+    return out
+
+
+def quads_moe_unsort(y, pos, topk, topk_w=None, out_dtype=OUT_F32):
+    """Packed rows y [rows, H] back in token order: out[t] = sum over slots in order of
+    topk_w[t, s] * y[pos[t * topk + s]] (without the weights for None) -> [T, H].  Slots whose
+    pos is outside [0, rows) add nothing."""
+    dev = _gpu("y", y)
+    if y.dim() != 2:
+        raise ValueError("y must be [rows, H]")
+    y, code = _dense("y", y, y.shape, dev)
+    rows, h = y.shape
+    pos, topk_w, t = _slots(pos, topk, topk_w, dev)
+    out = torch.empty(t, h, dtype=_FLOATS[1 if out_dtype == OUT_BF16 else 0], device=dev)
+    _call("quads_moe_unsort", dev, _at(y), code, rows, _at(pos), _at(topk_w), t, topk, h,
+          _at(out), out_dtype)
+    return out
+
+
+def quads_moe_unsort_backward(g, y, pos, topk, topk_w, rows=None, want_dy=True, want_dw=True):
+    """Gradient of quads_moe_unsort(y, pos, topk, topk_w) from the gradient g [T, H] -> (dy in
+    y's type or None, dw fp32 [T, topk] or None).  rows as in quads_moe_sort: None says that pos
+    is a permutation of y's rows; otherwise it is y's number of rows, and rows of dy without a
+    slot are 0."""
+    dev = _gpu("y", y)
+    if y.dim() != 2:
+        raise ValueError("y must be [rows, H]")
+    y, yt = _dense("y", y, y.shape, dev)
+    n, h = y.shape
+    pos, topk_w, t = _slots(pos, topk, topk_w, dev)
+    g, gt = _dense("g", g, (t, h), dev)
+    if n != (t * topk if rows is None else rows):
+        raise ValueError("y must have T * topk rows, or as many as rows says")
+    dy = _packed(rows, n, h, y.dtype, dev)[1] if want_dy else None
+    dw = None
+    if want_dw and topk_w is not None:
+        dw = torch.empty(t, topk, dtype=torch.float32, device=dev)
+    _call("quads_moe_unsort_backward", dev, _at(g), gt, _at(y), yt, n, _at(pos), _at(topk_w), t,
+          topk, h, _at(dy), _at(dw))
+    return dy, dw

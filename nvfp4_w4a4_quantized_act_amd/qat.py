@@ -20,7 +20,7 @@ of the rollout's tokens with the entropy (`token_logprobs`, the quantity that
 the method aligns between rollout and learner) and the distillation from
 another model's top alternatives (`distill_loss`).
 
-Forward and backward of the losses may be captured into a HIP graph.  As with
+Forward and backward of these operators may be captured into a HIP graph.  As with
 any of torch's operators, take the captured gradients with torch.autograd.grad,
 or call .backward() only while no eager result of the same leaves is alive:
 torch would wait, inside the capture, for the stream of the eager one.
@@ -28,7 +28,9 @@ torch would wait, inside the capture, for the stream of the eager one.
 
 import torch
 
-from . import (quads_nvfp4_weight_qdq, quads_token_logprob, quads_token_logprob_backward,
+from . import (OUT_BF16, OUT_F32, quads_moe_route, quads_moe_route_backward, quads_moe_sort,
+               quads_moe_unsort, quads_moe_unsort_backward, quads_nvfp4_weight_qdq, quads_rmsnorm,
+               quads_rmsnorm_backward, quads_token_logprob, quads_token_logprob_backward,
                quads_topk_distill, quads_topk_distill_backward)
 
 
@@ -137,3 +139,134 @@ def distill_loss(logits, t_val, t_id, weight=None, inv_temp=1.0, renorm=True):
                              None if weight is None else weight.reshape(-1), float(inv_temp),
                              bool(renorm))
     return loss.reshape(lead)
+
+
+def _code(dtype):
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("the type must be torch.float32 or torch.bfloat16")
+    return OUT_BF16 if dtype == torch.bfloat16 else OUT_F32
+
+
+class RMSNorm(torch.autograd.Function):
+    """(y, h) of h = x + residual, y = h / sqrt(mean h^2 + eps) * weight, over rows."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, out_dtype):
+        r = quads_rmsnorm(x, weight, eps, residual, _code(out_dtype))
+        h = r.get("sum")
+        ctx.save_for_backward(x if h is None else h, weight)
+        ctx.eps, ctx.x_dtype, ctx.added = eps, x.dtype, h is not None
+        ctx.set_materialize_grads(False)
+        return r["y"], h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g, g_sum):
+        h, weight = ctx.saved_tensors
+        if g is None:
+            if g_sum is None:
+                return None, None, None, None, None
+            return g_sum.to(ctx.x_dtype), g_sum, None, None, None
+        dx, dres, dw = quads_rmsnorm_backward(g, h, weight, ctx.eps, g_sum, ctx.x_dtype,
+                                              ctx.needs_input_grad[2])
+        return dx, dres if ctx.added else None, dw, None, None
+
+
+def rms_norm(x, weight=None, eps=1e-6, residual=None, out_dtype=None):
+    """Root-mean-square norm over the last dimension of x [..., H] (float32 or bf16), times
+    weight [H].  With a residual of x's shape: (y, h), the norm of h = x + residual and h itself
+    in the residual's type, the next residual.  y has the type out_dtype (h's).  Differentiable
+    in x, residual and weight."""
+    for t in (x, weight, residual):
+        if t is not None:
+            _code(t.dtype)
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError("residual must have the shape of x")
+    if out_dtype is None:
+        out_dtype = x.dtype if residual is None else residual.dtype
+    n = x.shape[-1]
+    y, h = RMSNorm.apply(x.reshape(-1, n), None if residual is None else residual.reshape(-1, n),
+                         weight, float(eps), out_dtype)
+    return y.reshape(x.shape) if residual is None else (y.reshape(x.shape), h.reshape(x.shape))
+
+
+class Route(torch.autograd.Function):
+    """(weights, ids) of the topk experts of each row of logits; gradient for the logits."""
+
+    @staticmethod
+    def forward(ctx, logits, topk, renorm):
+        ids, w = quads_moe_route(logits, topk, renorm)
+        ctx.save_for_backward(logits, ids, w)
+        ctx.renorm = renorm
+        ctx.mark_non_differentiable(ids)
+        return w, ids
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g, _):
+        logits, ids, w = ctx.saved_tensors
+        return quads_moe_route_backward(logits, ids, w, g, ctx.renorm), None, None
+
+
+def route(logits, topk, renorm=True):
+    """Routing weights (fp32) and ids (int32) [..., topk] of the experts with the largest logits
+    [..., E] (float32 or bf16): softmax over all experts, or over the chosen ones (renorm).
+    Differentiable in the logits, through the weights of the chosen experts."""
+    _code(logits.dtype)
+    w, ids = Route.apply(logits.reshape(-1, logits.shape[-1]), int(topk), bool(renorm))
+    lead = logits.shape[:-1]
+    return w.reshape(*lead, -1), ids.reshape(*lead, -1)
+
+
+class SortTokens(torch.autograd.Function):
+    """Rows of x copied to the packed rows that pos names; the gradient adds them up again."""
+
+    @staticmethod
+    def forward(ctx, x, pos, topk, rows):
+        ctx.save_for_backward(pos)
+        ctx.topk, ctx.dtype = topk, x.dtype
+        return quads_moe_sort(x, pos, topk, rows)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        pos, = ctx.saved_tensors
+        return quads_moe_unsort(g, pos, ctx.topk, out_dtype=_code(ctx.dtype)), None, None, None
+
+
+def sort_tokens(x, pos, topk, rows=None):
+    """Tokens x [T, H] (float32 or bf16) in expert order [rows, H]: row pos[t * topk + s] is x[t].
+    rows None: pos is a permutation of the T * topk rows (`quads_moe_pack`'s).  With rows given,
+    slots whose pos is outside [0, rows) are left out and rows without a slot are 0.
+    Differentiable in x."""
+    _code(x.dtype)
+    return SortTokens.apply(x, pos, int(topk), rows)
+
+
+class UnsortTokens(torch.autograd.Function):
+    """Weighted sums of the packed rows that pos names; gradient for the rows and the weights."""
+
+    @staticmethod
+    def forward(ctx, y, pos, topk, topk_w, out_dtype, rows):
+        ctx.save_for_backward(y, pos, topk_w)
+        ctx.topk, ctx.rows = topk, rows
+        return quads_moe_unsort(y, pos, topk, topk_w, _code(out_dtype))
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        y, pos, topk_w = ctx.saved_tensors
+        dy, dw = quads_moe_unsort_backward(g, y, pos, ctx.topk, topk_w, ctx.rows,
+                                           ctx.needs_input_grad[0], ctx.needs_input_grad[3])
+        return dy, None, None, dw, None, None
+
+
+def unsort_tokens(y, pos, topk, topk_w=None, out_dtype=torch.float32, rows=None):
+    """Experts' rows y [rows, H] (float32 or bf16) back in token order [T, H]: the sum over a
+    token's slots of topk_w[t, s] * y[pos[t * topk + s]] (topk_w fp32 [T, topk], None: 1).  rows
+    as in sort_tokens: None says that pos is a permutation of y's rows; otherwise y's number of
+    rows, and rows without a slot get a zero gradient.  Differentiable in y and topk_w."""
+    _code(y.dtype)
+    if y.shape[0] != (pos.numel() if rows is None else rows):
+        raise ValueError("y must have T * topk rows, or as many as rows says")
+    return UnsortTokens.apply(y, pos, int(topk), topk_w, out_dtype, rows)

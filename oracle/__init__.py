@@ -28,6 +28,7 @@ Modules:
   moe     -- token packing, grouped W4A4 GEMM with compensation, SwiGLU,
              combine
   head    -- W4A16 product, token log-probabilities, distillation, gradients
+  block   -- residual and RMS norm, routing, tokens in expert order, gradients
 """
 
-from . import formats, nvfp4, rac, moe, head  # noqa: F401
+from . import formats, nvfp4, rac, moe, head, block  # noqa: F401
