@@ -17,17 +17,21 @@ using namespace block;
 
 constexpr int kNone = 2;                     // no residual
 
-// Sum over a work-group of up to 16 waves (one barrier), in every thread.  s_part: two
-// sets of one number per wave, taken in turn by calls that follow one another (`set`
-// 0, 1, 0, ..): a wave is past the barrier of the call between when it writes a set
-// again, and so every wave has read it.
+// Sum over n waves of a work-group, from wave `first` on (one barrier, of the whole
+// work-group), in every thread of theirs.  s_part: two sets of one number per wave, taken
+// in turn by calls that follow one another (`set` 0, 1, 0, ..): a wave is past the barrier
+// of the call between when it writes a set again, and so every wave has read it.
 constexpr int kMaxWaves = 16;
-__device__ __forceinline__ double group_sum(double v, double (*s_part)[kMaxWaves], int set) {
+__device__ __forceinline__ double group_sum(double v, double (*s_part)[kMaxWaves], int set,
+                                            int first, int n) {
     v = lanes_sum<64>(v);
     if ((threadIdx.x & 63) == 0) s_part[set][threadIdx.x >> 6] = v;
     __syncthreads();
     const int i = threadIdx.x & (kMaxWaves - 1);
-    return lanes_sum<kMaxWaves>(i < (int)(blockDim.x >> 6) ? s_part[set][i] : 0.0);
+    return lanes_sum<kMaxWaves>(i < n ? s_part[set][first + i] : 0.0);
+}
+__device__ __forceinline__ double group_sum(double v, double (*s_part)[kMaxWaves], int set) {
+    return group_sum(v, s_part, set, 0, (int)(blockDim.x >> 6));
 }
 
 // Eight channels of the weight in either type; 1 without one.
