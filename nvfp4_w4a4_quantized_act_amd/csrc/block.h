@@ -20,6 +20,17 @@ typedef words4 words4_at2 __attribute__((aligned(2)));
 typedef words4 words4_at4 __attribute__((aligned(4)));
 typedef uint32_t words2 __attribute__((ext_vector_type(2)));
 
+template <bool kOnce, typename T>
+__device__ __forceinline__ words4 read(const T* p) {
+    if (kOnce) return __builtin_nontemporal_load(p);
+    return *p;
+}
+template <bool kOnce, typename T>
+__device__ __forceinline__ void write(T* p, words4 v) {
+    if (kOnce) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
 // Eight channels as they stand in memory.
 template <int kBf16>
 struct Raw {
@@ -34,14 +45,15 @@ struct Raw {
 };
 
 // The eight channels from element `at` of a row that has n >= 1 left from there
-// (channels behind the row's end: 0).  kWhole: n is at least eight.
-template <int kBf16, bool kWhole = false>
+// (channels behind the row's end: 0).  kWhole: n is at least eight.  kOnce: rows that
+// nothing reads again soon (non-temporal, whole eights only).
+template <int kBf16, bool kWhole = false, bool kOnce = false>
 __device__ __forceinline__ Raw<kBf16> load(const void* row, int64_t at, int64_t n) {
     Raw<kBf16> r;
     if (kBf16) {
         const uint16_t* p = (const uint16_t*)row + at;
         if (kWhole || n >= kPer) {
-            r.q[0] = *reinterpret_cast<const words4_at2*>(p);
+            r.q[0] = read<kOnce>(reinterpret_cast<const words4_at2*>(p));
         } else {
             uint32_t v[kPer];
 #pragma unroll
@@ -52,8 +64,8 @@ __device__ __forceinline__ Raw<kBf16> load(const void* row, int64_t at, int64_t 
     } else {
         const uint32_t* p = (const uint32_t*)row + at;
         if (kWhole || n >= kPer) {
-            r.q[0] = *reinterpret_cast<const words4_at4*>(p);
-            r.q[1] = *reinterpret_cast<const words4_at4*>(p + 4);
+            r.q[0] = read<kOnce>(reinterpret_cast<const words4_at4*>(p));
+            r.q[1] = read<kOnce>(reinterpret_cast<const words4_at4*>(p + 4));
         } else {
 #pragma unroll
             for (int i = 0; i < kPer; ++i) r.q[i >> 2][i & 3] = i < n ? p[i] : 0u;
@@ -80,12 +92,12 @@ __device__ __forceinline__ Raw<kBf16> pack(const float* v) {
     }
     return r;
 }
-template <int kBf16, bool kWhole = false>
+template <int kBf16, bool kWhole = false, bool kOnce = false>
 __device__ __forceinline__ void store(void* row, int64_t at, int64_t n, const Raw<kBf16>& r) {
     if (kBf16) {
         uint16_t* p = (uint16_t*)row + at;
         if (kWhole || n >= kPer) {
-            *reinterpret_cast<words4_at2*>(p) = r.q[0];
+            write<kOnce>(reinterpret_cast<words4_at2*>(p), r.q[0]);
         } else {
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
@@ -94,8 +106,8 @@ __device__ __forceinline__ void store(void* row, int64_t at, int64_t n, const Ra
     } else {
         uint32_t* p = (uint32_t*)row + at;
         if (kWhole || n >= kPer) {
-            *reinterpret_cast<words4_at4*>(p) = r.q[0];
-            *reinterpret_cast<words4_at4*>(p + 4) = r.q[kBf16 ? 0 : 1];
+            write<kOnce>(reinterpret_cast<words4_at4*>(p), r.q[0]);
+            write<kOnce>(reinterpret_cast<words4_at4*>(p + 4), r.q[kBf16 ? 0 : 1]);
         } else {
 #pragma unroll
             for (int i = 0; i < kPer; ++i)

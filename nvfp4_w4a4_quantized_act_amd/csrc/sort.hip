@@ -14,7 +14,6 @@ namespace sorting {
 
 using namespace block;
 
-constexpr int kThreads = 256;
 constexpr int kMaxTopk = 64;
 
 struct Args {
@@ -22,91 +21,211 @@ struct Args {
     const void* y;                           // of the gradient
     void* out;                               // packed rows, token rows, or dy
     float* dw;
-    const int32_t* pos;
-    const float* w;
     int64_t T, H, ld, rows;
     int topk;
 };
 
-template <int kT>
-__global__ __launch_bounds__(kThreads) void k_sort(Args a) {
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const void* x = row_at<kT>(a.a, t * a.ld);
-        for (int64_t c = (int64_t)threadIdx.x * kPer; c < a.H; c += kThreads * kPer) {
-            const Raw<kT> r = load<kT>(x, c, a.H - c);
-            for (int s = 0; s < a.topk; ++s) {
-                const int64_t p = a.pos[t * a.topk + s];
-                if (p >= 0 && p < a.rows) store<kT>(row_at<kT>(a.out, p * a.H), c, a.H - c, r);
-            }
+// Which token and which eight channels a thread has.  kLanes threads to a token (8, 16,
+// 32), 256 / kLanes tokens to a work-group; 0: work-group (x, y) has channels
+// 8 * blockDim.x * y .. of token x.
+template <int kLanes, int kCut>
+struct Place {
+    int64_t t;
+    Piece p;
+    __device__ __forceinline__ explicit Place(const Args& a) {
+        int c;
+        if (kLanes) {
+            t = (int64_t)blockIdx.x * (256 / (kLanes ? kLanes : 1)) + threadIdx.x / (kLanes ? kLanes : 1);
+            c = threadIdx.x % (kLanes ? kLanes : 1);
+        } else {
+            t = blockIdx.x;
+            c = blockIdx.y * blockDim.x + threadIdx.x;
         }
+        p = piece<kCut>(c * kPer, (int)a.H);
+        if (t >= a.T) p.n = 0;
+    }
+};
+// Packed row of slot s, or -1.
+__device__ __forceinline__ int64_t slot_row(const int32_t* pos, int64_t at, int64_t rows) {
+    const int64_t p = pos[at];
+    return p >= 0 && p < rows ? p : -1;
+}
+
+constexpr int kBatch = 8;                    // slots whose rows are asked for together
+
+template <int kT, int kOnce, int kLanes, int kCut>
+__global__ __launch_bounds__(kLanes ? 256 : 1024) void k_sort(Args a,
+                                                              const int32_t* __restrict__ pos) {
+    const Place<kLanes, kCut> at(a);
+    if (at.p.n <= 0) return;
+    const Raw<kT> r = load<kT, kCut != kTiny>(row_at<kT>(a.a, at.t * a.ld), at.p.at, at.p.n);
+    for (int s = 0; s < a.topk; ++s) {
+        const int64_t p = slot_row(pos, at.t * a.topk + s, a.rows);
+        if (p >= 0) store<kT, kCut != kTiny, (kOnce & 2) && kCut == kEven>(row_at<kT>(a.out, p * a.H), at.p.at, at.p.n, r);
     }
 }
 
-template <int kY, int kOut>
-__global__ __launch_bounds__(kThreads) void k_unsort(Args a) {
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        for (int64_t c = (int64_t)threadIdx.x * kPer; c < a.H; c += kThreads * kPer) {
-            float acc[kPer] = {};
-            for (int s = 0; s < a.topk; ++s) {
-                const int64_t p = a.pos[t * a.topk + s];
-                if (p < 0 || p >= a.rows) continue;
-                const float w = a.w ? a.w[t * a.topk + s] : 1.0f;
-                const Raw<kY> r = load<kY>(row_at<kY>(a.a, p * a.H), c, a.H - c);
+template <int kY, int kOut, int kOnce, int kLanes, int kCut>
+__global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort(Args a,
+                                                                const int32_t* __restrict__ pos,
+                                                                const float* __restrict__ w) {
+    const Place<kLanes, kCut> at(a);
+    if (at.p.n <= 0) return;
+    float acc[kPer] = {};
+    for (int s0 = 0; s0 < a.topk; s0 += kBatch) {
+        Raw<kY> r[kBatch];
+        float by[kBatch];
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) acc[i] = fmaf(w, r.get(i), acc[i]);
+        for (int s = 0; s < kBatch; ++s) {
+            const int64_t slot = at.t * a.topk + s0 + s;
+            const int64_t p = s0 + s < a.topk ? slot_row(pos, slot, a.rows) : -1;
+            r[s] = Raw<kY>{};
+            by[s] = 0.0f;
+            if (p >= 0) {
+                r[s] = load<kY, kCut != kTiny, (kOnce & 1) != 0>(row_at<kY>(a.a, p * a.H), at.p.at, at.p.n);
+                by[s] = w ? w[slot] : 1.0f;
             }
-            store<kOut>(row_at<kOut>(a.out, t * a.H), c, a.H - c, pack<kOut>(acc));
+        }
+#pragma unroll
+        for (int s = 0; s < kBatch; ++s) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) acc[i] = fmaf(by[s], r[s].get(i), acc[i]);
         }
     }
+    store<kOut, kCut != kTiny>(row_at<kOut>(a.out, at.t * a.H), at.p.at, at.p.n, pack<kOut>(acc));
 }
 
-template <int kG, int kY>
-__global__ __launch_bounds__(kThreads) void k_unsort_grad(Args a) {
-    __shared__ float s_part[kMaxTopk][kThreads / 64];
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const void* g = row_at<kG>(a.a, t * a.H);
-        for (int s = 0; s < a.topk; ++s) {
-            const int64_t p = a.pos[t * a.topk + s];
-            const bool have = p >= 0 && p < a.rows;
-            float dot = 0.0f;
-            if (have) {
-                const float w = a.w ? a.w[t * a.topk + s] : 1.0f;
-                for (int64_t c = (int64_t)threadIdx.x * kPer; c < a.H; c += kThreads * kPer) {
-                    const int64_t n = a.H - c;
-                    const Raw<kG> gr = load<kG>(g, c, n);
-                    if (a.dw) {
-                        const Raw<kY> yr = load<kY>(row_at<kY>(a.y, p * a.H), c, n);
+// kLanes 0: a work-group per token, its threads over the row, again where it is longer.
+template <int kG, int kY, int kOnce, int kLanes, int kCut>
+__global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort_grad(
+    Args a, const int32_t* __restrict__ pos, const float* __restrict__ w) {
+    constexpr int kMaxWaves = kLanes ? 1 : 16;
+    __shared__ float s_dot[kLanes ? 1 : kMaxTopk][kMaxWaves];
+    const Place<kLanes, kCut> at(a);
+    const int step = kLanes ? 1 : (int)blockDim.x * kPer;
+    int c = kLanes ? 0 : (int)threadIdx.x * kPer;
+    for (int first = 1;; first = 0) {
+        const Piece p = kLanes ? at.p : piece<kCut>(c, (int)a.H);
+        Raw<kG> g = {};
+        if (p.n > 0) g = load<kG, kCut != kTiny>(row_at<kG>(a.a, at.t * a.H), p.at, p.n);
+        for (int s0 = 0; s0 < a.topk; s0 += kBatch) {
+            Raw<kY> y[kBatch];
+            int64_t row[kBatch];
 #pragma unroll
-                        for (int i = 0; i < kPer; ++i) dot = fmaf(gr.get(i), yr.get(i), dot);
-                    }
-                    if (a.out) {
-                        float d[kPer];
+            for (int s = 0; s < kBatch; ++s) {
+                const int64_t slot = at.t * a.topk + s0 + s;
+                row[s] = s0 + s < a.topk && (!kLanes || at.t < a.T) ? slot_row(pos, slot, a.rows)
+                                                                    : -1;
+                y[s] = Raw<kY>{};
+                if (a.dw && row[s] >= 0 && p.n > 0)
+                    y[s] = load<kY, kCut != kTiny, (kOnce & 1) != 0>(row_at<kY>(a.y, row[s] * a.H), p.at, p.n);
+            }
 #pragma unroll
-                        for (int i = 0; i < kPer; ++i) d[i] = w * gr.get(i);
-                        store<kY>(row_at<kY>(a.out, p * a.H), c, n, pack<kY>(d));
+            for (int s = 0; s < kBatch; ++s) {
+                if (s0 + s >= a.topk) break;
+                const int64_t slot = at.t * a.topk + s0 + s;
+                if (a.out && row[s] >= 0 && p.n > 0) {
+                    const float by = w ? w[slot] : 1.0f;
+                    float d[kPer];
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) d[i] = by * g.get(i);
+                    store<kY, kCut != kTiny, (kOnce & 2) && kCut == kEven>(row_at<kY>(a.out, row[s] * a.H), p.at, p.n, pack<kY>(d));
+                }
+                if (a.dw) {
+                    float dot = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i)
+                        if (kCut != kOdd || i >= p.from) dot = fmaf(g.get(i), y[s].get(i), dot);
+                    dot = lanes_sum<kLanes ? kLanes : 64>(dot);
+                    if (kLanes) {
+                        if (threadIdx.x % (kLanes ? kLanes : 1) == 0 && at.t < a.T) a.dw[slot] = dot;
+                    } else if ((threadIdx.x & 63) == 0) {
+                        float& all = s_dot[kLanes ? 0 : s0 + s][kLanes ? 0 : threadIdx.x >> 6];
+                        all = first ? dot : all + dot;
                     }
                 }
             }
-            if (a.dw) {
-#pragma unroll
-                for (int off = 32; off; off >>= 1) dot += __shfl_xor(dot, off, 64);
-                if ((threadIdx.x & 63) == 0) s_part[s][threadIdx.x >> 6] = dot;
-            }
         }
-        if (a.dw) {
-            __syncthreads();
-            for (int s = threadIdx.x; s < a.topk; s += kThreads) {
-                float v = 0.0f;
-                for (int i = 0; i < kThreads / 64; ++i) v += s_part[s][i];
-                a.dw[t * a.topk + s] = v;
-            }
-            __syncthreads();
-        }
+        if (kLanes) return;
+        c += step;
+        if (c - (int)threadIdx.x * kPer >= a.H) break;
+    }
+    if (kLanes || !a.dw) return;
+    __syncthreads();
+    for (int s = threadIdx.x; s < a.topk; s += blockDim.x) {
+        float v = s_dot[kLanes ? 0 : s][0];
+        for (int i = 1; i < (int)(blockDim.x >> 6); ++i) v += s_dot[kLanes ? 0 : s][kLanes ? 0 : i];
+        a.dw[at.t * a.topk + s] = v;
     }
 }
 
-constexpr int64_t kGroups = 1 << 20;         // work-groups of a call, at most
-inline dim3 grid(int64_t T) { return dim3((unsigned)(T < kGroups ? T : kGroups)); }
+// ------------------------------------------------------------------- host --
+// Packed rows beyond what the caches keep go past them (kOnce: 1 their loads, 2 their
+// stores), us: loads from 16 MB on (gradient 4096 x 2048, top 8, bf16 53 against 63, unsort
+// 28 / 30; 64 x 4096, top 8, fp32 11.6 / 8.7), stores from 192 MB on (sort 16384 x 4096,
+// top 8, bf16 212 / 242; 4096 x 2048 27.4 / 28.0, but what reads them then, 48.7 / 55 for
+// both).  Stores only where rows are whole lines of 16 bytes.
+constexpr int64_t kOnceLoads = (int64_t)16 << 20, kOnceStores = (int64_t)192 << 20;
+
+struct Shape {
+    int lanes, threads;
+    dim3 grid;
+};
+// `parts`: a row may be several work-groups' (512 threads; 128 where there are few rows:
+// sort 64 x 4096, top 8, fp32 4.5 us against 5.5).
+inline Shape shape_of(int64_t T, int64_t H, bool parts) {
+    const int64_t chunks = (H + kPer - 1) / kPer;
+    for (int l = 8; l <= 32; l *= 2)
+        if (chunks <= l) return {l, 256, dim3((unsigned)((T * l + 255) / 256))};
+    int threads = (int)(chunks < 1024 ? (chunks + 63) / 64 * 64 : 1024);
+    if (!parts) return {0, threads, dim3((unsigned)T)};
+    const int most = T * ((chunks + 511) / 512) < 512 ? 128 : 512;
+    if (threads > most) threads = most;
+    return {0, threads, dim3((unsigned)T, (unsigned)((chunks + threads - 1) / threads))};
+}
+
+// A launch has fewer than 2^32 threads: tokens of one launch, at most.
+constexpr int64_t kLaunchTokens = (int64_t)1 << 21;
+
+#define QUADS_LAUNCH(kernel, O, L, C, ...) \
+    hipLaunchKernelGGL((kernel<types..., O, L, C>), p.grid, dim3(p.threads), 0, s, __VA_ARGS__)
+#define QUADS_ROWS(kernel, once, ...)                                                          \
+    const Cut cut = cut_of(a.H);                                                               \
+    if (cut == kTiny) QUADS_LAUNCH(kernel, 0, 8, kTiny, __VA_ARGS__);                          \
+    else if (p.lanes == 8 && cut == kEven) QUADS_LAUNCH(kernel, 0, 8, kEven, __VA_ARGS__);     \
+    else if (p.lanes == 8) QUADS_LAUNCH(kernel, 0, 8, kOdd, __VA_ARGS__);                      \
+    else if (p.lanes == 16 && cut == kEven) QUADS_LAUNCH(kernel, 0, 16, kEven, __VA_ARGS__);   \
+    else if (p.lanes == 16) QUADS_LAUNCH(kernel, 0, 16, kOdd, __VA_ARGS__);                    \
+    else if (p.lanes == 32 && cut == kEven) QUADS_LAUNCH(kernel, 0, 32, kEven, __VA_ARGS__);   \
+    else if (p.lanes == 32) QUADS_LAUNCH(kernel, 0, 32, kOdd, __VA_ARGS__);                    \
+    else if (once && cut == kEven) QUADS_LAUNCH(kernel, once, 0, kEven, __VA_ARGS__);          \
+    else if (once) QUADS_LAUNCH(kernel, once, 0, kOdd, __VA_ARGS__);                           \
+    else if (cut == kEven) QUADS_LAUNCH(kernel, 0, 0, kEven, __VA_ARGS__);                     \
+    else QUADS_LAUNCH(kernel, 0, 0, kOdd, __VA_ARGS__);
+
+// `bytes`: of the packed rows that the slots name.
+template <int... types>
+void launch_sort(const Args& a, const int32_t* pos, int64_t bytes, hipStream_t s) {
+    const Shape p = shape_of(a.T, a.H, true);
+    if (bytes > kOnceStores) { QUADS_ROWS(k_sort, 2, a, pos) }
+    else { QUADS_ROWS(k_sort, 0, a, pos) }
+}
+template <int... types>
+void launch_unsort(const Args& a, const int32_t* pos, const float* w, int64_t bytes,
+                   hipStream_t s) {
+    const Shape p = shape_of(a.T, a.H, true);
+    if (bytes > kOnceLoads) { QUADS_ROWS(k_unsort, 1, a, pos, w) }
+    else { QUADS_ROWS(k_unsort, 0, a, pos, w) }
+}
+template <int... types>
+void launch_grad(const Args& a, const int32_t* pos, const float* w, int64_t bytes, hipStream_t s) {
+    const Shape p = shape_of(a.T, a.H, false);
+    if (bytes > kOnceStores) { QUADS_ROWS(k_unsort_grad, 3, a, pos, w) }
+    else if (bytes > kOnceLoads) { QUADS_ROWS(k_unsort_grad, 1, a, pos, w) }
+    else { QUADS_ROWS(k_unsort_grad, 0, a, pos, w) }
+}
+#undef QUADS_ROWS
+#undef QUADS_LAUNCH
 
 inline int check(int64_t T, int64_t H, int64_t ld, int32_t topk, int64_t rows) {
     if (T < 0 || T >= ((int64_t)1 << 24) || H < 1 || H >= kMaxH || ld < H || ld >= kMaxStride)
@@ -130,13 +249,16 @@ extern "C" int quads_moe_sort(const void* x, int dtype, int64_t T, int64_t H, in
     if (!ok_type(dtype)) return QUADS_EINVAL;
     if (T == 0 || rows == 0) return QUADS_OK;
     if (!ok_ptr(x) || !ok_ptr4(pos) || !ok_ptr(out) || x == out) return QUADS_EINVAL;
-    const Args a = {x, nullptr, out, nullptr, pos, nullptr, T, H, ldx, rows, topk};
     hipStream_t s = (hipStream_t)stream;
-    if (dtype == QUADS_OUT_BF16)
-        hipLaunchKernelGGL(k_sort<1>, grid(T), dim3(kThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL(k_sort<0>, grid(T), dim3(kThreads), 0, s, a);
-    QUADS_CHECK_LAUNCH();
+    const int size = dtype == QUADS_OUT_BF16 ? 2 : 4;
+    const int64_t bytes = T * topk * H * size;
+    for (int64_t t = 0; t < T; t += kLaunchTokens) {
+        const Args a = {(const char*)x + t * ldx * size, nullptr, out, nullptr,
+                        T - t < kLaunchTokens ? T - t : kLaunchTokens, H, ldx, rows, topk};
+        if (dtype == QUADS_OUT_BF16) launch_sort<1>(a, pos + t * topk, bytes, s);
+        else launch_sort<0>(a, pos + t * topk, bytes, s);
+        QUADS_CHECK_LAUNCH();
+    }
     return QUADS_OK;
 }
 
@@ -149,14 +271,20 @@ extern "C" int quads_moe_unsort(const void* y, int y_dtype, int64_t rows, const 
     if (T == 0) return QUADS_OK;
     if ((rows > 0 && !ok_ptr(y)) || !ok_ptr4(pos) || !ok_opt4(topk_w) || !ok_ptr(out) || y == out)
         return QUADS_EINVAL;
-    const Args a = {y, nullptr, out, nullptr, pos, topk_w, T, H, H, rows, topk};
     hipStream_t s = (hipStream_t)stream;
     const bool yb = y_dtype == QUADS_OUT_BF16, ob = out_dtype == QUADS_OUT_BF16;
-    if (yb && ob) hipLaunchKernelGGL((k_unsort<1, 1>), grid(T), dim3(kThreads), 0, s, a);
-    else if (yb) hipLaunchKernelGGL((k_unsort<1, 0>), grid(T), dim3(kThreads), 0, s, a);
-    else if (ob) hipLaunchKernelGGL((k_unsort<0, 1>), grid(T), dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_unsort<0, 0>), grid(T), dim3(kThreads), 0, s, a);
-    QUADS_CHECK_LAUNCH();
+    const int64_t bytes = T * topk * H * (yb ? 2 : 4);
+    for (int64_t t = 0; t < T; t += kLaunchTokens) {
+        const Args a = {y, nullptr, (char*)out + t * H * (ob ? 2 : 4), nullptr,
+                        T - t < kLaunchTokens ? T - t : kLaunchTokens, H, H, rows, topk};
+        const int32_t* p = pos + t * topk;
+        const float* w = topk_w ? topk_w + t * topk : nullptr;
+        if (yb && ob) launch_unsort<1, 1>(a, p, w, bytes, s);
+        else if (yb) launch_unsort<1, 0>(a, p, w, bytes, s);
+        else if (ob) launch_unsort<0, 1>(a, p, w, bytes, s);
+        else launch_unsort<0, 0>(a, p, w, bytes, s);
+        QUADS_CHECK_LAUNCH();
+    }
     return QUADS_OK;
 }
 
@@ -172,13 +300,19 @@ extern "C" int quads_moe_unsort_backward(const void* g, int g_dtype, const void*
     if (!ok_ptr(g) || (rows > 0 && dw && !ok_ptr(y)) || !ok_ptr4(pos) || !ok_opt4(topk_w) ||
         !ok_opt_ptr(dy) || !ok_opt4(dw) || dy == g)
         return QUADS_EINVAL;
-    const Args a = {g, y, dy, dw, pos, topk_w, T, H, H, rows, topk};
     hipStream_t s = (hipStream_t)stream;
     const bool gb = g_dtype == QUADS_OUT_BF16, yb = y_dtype == QUADS_OUT_BF16;
-    if (gb && yb) hipLaunchKernelGGL((k_unsort_grad<1, 1>), grid(T), dim3(kThreads), 0, s, a);
-    else if (gb) hipLaunchKernelGGL((k_unsort_grad<1, 0>), grid(T), dim3(kThreads), 0, s, a);
-    else if (yb) hipLaunchKernelGGL((k_unsort_grad<0, 1>), grid(T), dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_unsort_grad<0, 0>), grid(T), dim3(kThreads), 0, s, a);
-    QUADS_CHECK_LAUNCH();
+    const int64_t bytes = T * topk * H * (yb ? 2 : 4);
+    for (int64_t t = 0; t < T; t += kLaunchTokens) {
+        const Args a = {(const char*)g + t * H * (gb ? 2 : 4), y, dy, dw ? dw + t * topk : nullptr,
+                        T - t < kLaunchTokens ? T - t : kLaunchTokens, H, H, rows, topk};
+        const int32_t* p = pos + t * topk;
+        const float* w = topk_w ? topk_w + t * topk : nullptr;
+        if (gb && yb) launch_grad<1, 1>(a, p, w, bytes, s);
+        else if (gb) launch_grad<1, 0>(a, p, w, bytes, s);
+        else if (yb) launch_grad<0, 1>(a, p, w, bytes, s);
+        else launch_grad<0, 0>(a, p, w, bytes, s);
+        QUADS_CHECK_LAUNCH();
+    }
     return QUADS_OK;
 }

@@ -593,6 +593,24 @@ def test_unsort_backward_over_y(Q):
     assert torch.equal(y, dy) and torch.equal(dw, dw2)
 
 
+def test_sort_of_more_tokens_than_a_launch_has(Q):
+    t, h = 2 ** 21 + 5, 16
+    g = torch.Generator(device=DEV).manual_seed(0)
+    pos = torch.randperm(t, generator=g, device=DEV, dtype=torch.int32)
+    x = torch.randn((t, h), generator=g, device=DEV).bfloat16()
+    at = pos.long()
+    xs = Q.quads_moe_sort(x, pos, 1)
+    assert torch.equal(xs[at], x)
+    w = torch.rand((t, 1), generator=g, device=DEV)
+    out = Q.quads_moe_unsort(xs, pos, 1, w)
+    assert torch.equal(out, x.float() * w)                          # one product, rounded once
+    dy, dw = Q.quads_moe_unsort_backward(out, xs, pos, 1, w)
+    assert torch.equal(dy[at], (out * w).bfloat16())
+    want = (out.double() * x.double()).sum(1, keepdim=True)
+    assert ((dw.double() - want).abs() <= 25 * U * (out.double() * x.double()).abs().sum(1, keepdim=True)
+            + TINY).all()
+
+
 def test_sort_of_nothing(Q):
     z = torch.zeros((0, 16), device=DEV)
     pos = torch.zeros(0, dtype=torch.int32, device=DEV)
