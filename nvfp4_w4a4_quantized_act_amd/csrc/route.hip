@@ -5,9 +5,11 @@
 //   renorm 0: dz_v = a_i [v = id_i] - p_v A,   a_i = g_i w_i, A = sum a_i
 //   renorm 1: dz_v = a_i - w_i A at v = id_i
 //
-// A wave per token, its logits in registers (logit e in lane e % 64).  The order
-// is by one signed number per logit: the bits of a float, the lower 31 turned
-// over where it is negative.  The wave takes the largest number topk times.
+// kL lanes (8 .. 64) share a token, kV neighbouring logits in the registers of each.  The
+// order is by one unsigned number per logit, larger for a larger one: a float's bits, all
+// turned over where it is negative, the sign alone where it is not.  topk times the lanes
+// take their largest number, and the lowest lane that has it removes its first such logit.
+// What bounds it is that chain of topk steps, about 50 operations each, not its bytes.
 #include "block.h"
 
 namespace quads {
@@ -15,9 +17,9 @@ namespace routing {
 
 using namespace block;
 
-constexpr int kThreads = 256;
 constexpr int kMaxE = 4096, kMaxTopk = 64;
-constexpr int kGone = INT32_MIN;             // below every logit's number
+// Rows of many logits take a work-group of one wave: its shared memory holds them.
+constexpr int threads_of(int v) { return v > 16 ? 64 : 256; }
 
 struct Args {
     const void* z;
@@ -29,160 +31,170 @@ struct Args {
     int E, topk, renorm;
 };
 
-__device__ __forceinline__ float logit(const void* z, int bf16, int64_t at) {
-    return bf16 ? bf16_to_f32(((const uint16_t*)z)[at]) : ((const float*)z)[at];
+// 0 is below every logit's number: a masked one's (-inf) is 0x007FFFFF.  z + 0 makes -0 a
+// 0; a NaN of either sign stands above everything.
+__device__ __forceinline__ uint32_t order_of(float z) {
+    const uint32_t b = __float_as_uint(z + 0.0f);
+    return z != z ? 0xFFFFFFFFu : b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
 }
-// z + 0 makes -0 a 0; a NaN of either sign stands above everything.
-__device__ __forceinline__ int order_of(float z) {
-    const int b = (int)__float_as_uint(z + 0.0f);
-    return z != z ? INT32_MAX : b ^ ((b >> 31) & 0x7FFFFFFF);
-}
-__device__ __forceinline__ float value_of(int k) {
-    return __uint_as_float((uint32_t)(k ^ ((k >> 31) & 0x7FFFFFFF)));
-}
-__device__ __forceinline__ int wave_max(int v) {
-#pragma unroll
-    for (int off = 32; off; off >>= 1) {
-        const int o = __shfl_xor(v, off, 64);
-        v = o > v ? o : v;
-    }
-    return v;
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
-    return v;
+__device__ __forceinline__ float value_of(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 // exp(z - m), 0 for a masked logit even where nothing else is left.
 __device__ __forceinline__ float term(float z, float m) {
     return z == -INFINITY ? 0.0f : expf(z - m);
 }
-
+// The logits kV * lane .. of a token; -inf behind the last.
 template <int kBf16, int kV>
-__global__ __launch_bounds__(kThreads) void k_route(Args a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-    if (t >= a.T) return;
-    int key[kV];
+__device__ __forceinline__ void load_logits(const Args& a, int64_t t, int lane, float* z) {
+    const void* row = row_at<kBf16>(a.z, t * a.ld);
 #pragma unroll
-    for (int j = 0; j < kV; ++j) {
-        const int e = lane + 64 * j;
-        key[j] = e < a.E ? order_of(logit(a.z, kBf16, t * a.ld + e)) : kGone;
-    }
-    int top = key[0];
+    for (int j = 0; j < kV; j += kPer) {
+        const int e = kV * lane + j;
+        Raw<kBf16> r = {};
+        if (t < a.T && e < a.E) r = load<kBf16>(row, e, a.E - e);
 #pragma unroll
-    for (int j = 1; j < kV; ++j) top = key[j] > top ? key[j] : top;
-    const float m = value_of(wave_max(top));
-    float total = 0.0f;
-    if (!a.renorm) {
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-            total += key[j] == kGone ? 0.0f : term(value_of(key[j]), m);
-        total = wave_sum(total);
-    }
-    int id = 0;                              // lane i: the i-th expert and its term
-    float mine = 0.0f;
-    for (int i = 0; i < a.topk; ++i) {
-        int best = key[0];
-#pragma unroll
-        for (int j = 1; j < kV; ++j) best = key[j] > best ? key[j] : best;
-        best = wave_max(best);
-        int e = kMaxE;
-#pragma unroll
-        for (int j = kV - 1; j >= 0; --j) {
-            const uint64_t at = __ballot(key[j] == best);
-            if (at) e = 64 * j + __builtin_ctzll(at);
-        }
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-            if (lane + 64 * j == e) key[j] = kGone;
-        const float p = term(value_of(best), m);
-        if (a.renorm) total += p;
-        if (lane == i) {
-            id = e;
-            mine = p;
-        }
-    }
-    if (lane < a.topk) {
-        a.ids[t * a.topk + lane] = id;
-        a.w[t * a.topk + lane] = total == 0.0f ? 0.0f : mine / total;
+        for (int i = 0; i < kPer; ++i) z[j + i] = e + i < a.E ? r.get(i) : -INFINITY;
     }
 }
 
-template <int kBf16, int kV>
-__global__ __launch_bounds__(kThreads) void k_route_grad(Args a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-    if (t >= a.T) return;
-    int id = -1;
-    float w = 0.0f, gw = 0.0f;
-    if (lane < a.topk) {
-        id = a.ids[t * a.topk + lane];
-        if (id >= 0 && id < a.E) {
-            w = a.w[t * a.topk + lane];
-            gw = a.g[t * a.topk + lane] * w;
-        } else {
-            id = -1;
+template <int kBf16, int kL, int kV>
+__global__ __launch_bounds__(threads_of(kV)) void k_route(Args a) {
+    constexpr int kTokens = threads_of(kV) / kL;
+    __shared__ uint2 s_top[kTokens][kMaxTopk];               // (id, number), in order
+    const int token = threadIdx.x / kL, lane = threadIdx.x % kL;
+    const int64_t t = (int64_t)blockIdx.x * kTokens + token;
+    float z[kV];
+    uint32_t key[kV];
+    load_logits<kBf16, kV>(a, t, lane, z);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) key[j] = kV * lane + j < a.E ? order_of(z[j]) : 0u;
+    float m = 0.0f, total = 0.0f;
+    for (int i = 0; i < a.topk; ++i) {
+        uint32_t mine = key[0];
+#pragma unroll
+        for (int j = 1; j < kV; ++j) mine = larger(mine, key[j]);
+        const uint32_t best = lanes_max<kL>(mine);
+        if (i == 0) {
+            m = value_of(best);
+            if (!a.renorm) {
+#pragma unroll
+                for (int j = 0; j < kV; ++j) total += term(z[j], m);
+                total = lanes_sum<kL>(total);
+            }
         }
+        const uint64_t at = __ballot(mine == best) >> ((threadIdx.x & 63) - lane);
+        const bool have = (int)__builtin_ctzll(at) == lane;  // the token's lowest such lane
+        int e = kV;
+#pragma unroll
+        for (int j = kV - 1; j >= 0; --j) e = key[j] == best ? j : e;
+        if (have) s_top[token][i] = make_uint2((uint32_t)(kV * lane + e), best);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) key[j] = have && j == e ? 0u : key[j];
     }
-    const float sum = wave_sum(gw);
-    const float add = a.renorm ? gw - w * sum : gw;
-    float d[kV];
+    __syncthreads();
+    if (a.renorm) {
+        for (int i = lane; i < a.topk; i += kL) total += term(value_of(s_top[token][i].y), m);
+        total = lanes_sum<kL>(total);
+    }
+    if (t >= a.T) return;
+    for (int i = lane; i < a.topk; i += kL) {
+        const uint2 c = s_top[token][i];
+        a.ids[t * a.topk + i] = (int32_t)c.x;
+        a.w[t * a.topk + i] = total == 0.0f ? 0.0f : term(value_of(c.y), m) / total;
+    }
+}
+
+// What the slots add goes through shared memory: the first slot of an id has the sum over
+// all of its slots, in order, and puts it at the id's place (comparing every id with each
+// of a lane's logits instead: 65536 x 128, top 8, 16.6 us against 14.9;
+// 4096 x 4096 fp32 55 / 48).
+template <int kBf16, int kL, int kV>
+__global__ __launch_bounds__(threads_of(kV)) void k_route_grad(Args a) {
+    constexpr int kTokens = threads_of(kV) / kL;
+    __shared__ uint2 s_slot[kTokens][kMaxTopk];              // (id, a), in order
+    __shared__ float s_add[kTokens][kL * kV];
+    const int token = threadIdx.x / kL, lane = threadIdx.x % kL;
+    const int64_t t = (int64_t)blockIdx.x * kTokens + token;
+    float z[kV];
+    if (!a.renorm) load_logits<kBf16, kV>(a, t, lane, z);
+    float sum = 0.0f;
+    for (int i = lane; i < a.topk; i += kL) {
+        int id = -1;
+        float gw = 0.0f;
+        if (t < a.T) {
+            id = a.ids[t * a.topk + i];
+            if (id >= 0 && id < a.E) gw = a.g[t * a.topk + i] * a.w[t * a.topk + i];
+            else id = -1;
+        }
+        s_slot[token][i] = make_uint2((uint32_t)id, __float_as_uint(gw));
+        sum += gw;
+    }
+    sum = lanes_sum<kL>(sum);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) s_add[token][kV * lane + j] = 0.0f;
     if (a.renorm) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) d[j] = 0.0f;
-    } else {
-        float z[kV], m = -INFINITY, total = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const int e = lane + 64 * j;
-            z[j] = e < a.E ? logit(a.z, kBf16, t * a.ld + e) : -INFINITY;
-            m = fmaxf(m, z[j]);
+        for (int j = 0; j < kV; ++j) z[j] = 0.0f;
+        for (int i = lane; i < a.topk; i += kL) {
+            uint2& c = s_slot[token][i];
+            if ((int)c.x >= 0)
+                c.y = __float_as_uint(__uint_as_float(c.y) - a.w[t * a.topk + i] * sum);
         }
+    } else {
+        float m = z[0], total = 0.0f;
 #pragma unroll
-        for (int off = 32; off; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+        for (int j = 1; j < kV; ++j) m = fmaxf(m, z[j]);
+        m = value_of(lanes_max<kL>(order_of(m)));
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             z[j] = term(z[j], m);
             total += z[j];
         }
-        total = wave_sum(total);
+        total = lanes_sum<kL>(total);
         const float by = total == 0.0f ? 0.0f : -sum / total;
 #pragma unroll
-        for (int j = 0; j < kV; ++j) d[j] = z[j] * by;
+        for (int j = 0; j < kV; ++j) z[j] *= by;
     }
-    for (int i = 0; i < a.topk; ++i) {
-        const int e = __shfl(id, i, 64);
-        const float v = __shfl(add, i, 64);
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-            if (lane + 64 * j == e) d[j] += v;
-    }
-#pragma unroll
-    for (int j = 0; j < kV; ++j) {
-        const int e = lane + 64 * j;
-        if (e < a.E) {
-            if (kBf16) ((uint16_t*)a.dz)[t * a.E + e] = (uint16_t)bf16_bits(d[j], 0.0f);
-            else ((float*)a.dz)[t * a.E + e] = d[j];
+    __syncthreads();
+    for (int i = lane; i < a.topk; i += kL) {
+        const uint32_t id = s_slot[token][i].x;
+        float v = 0.0f;
+        bool first = (int)id >= 0;
+        for (int k = 0; k < a.topk; ++k) {
+            const uint2 c = s_slot[token][k];
+            v += c.x == id ? __uint_as_float(c.y) : 0.0f;
+            first = first && (c.x != id || k >= i);
         }
+        if (first) s_add[token][id] = v;
+    }
+    __syncthreads();
+    if (t >= a.T) return;
+    void* row = row_at<kBf16>(a.dz, t * a.E);
+#pragma unroll
+    for (int j = 0; j < kV; j += kPer) {
+        const int e = kV * lane + j;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) z[j + i] += s_add[token][e + i];
+        if (e < a.E) store<kBf16>(row, e, a.E - e, pack<kBf16>(z + j));
     }
 }
 
-template <int kBf16, int kV>
+template <int kBf16, int kL, int kV>
 void launch(const Args& a, bool grad, hipStream_t s) {
-    const dim3 grid((unsigned)((a.T + kThreads / 64 - 1) / (kThreads / 64)));
-    if (grad) hipLaunchKernelGGL((k_route_grad<kBf16, kV>), grid, dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_route<kBf16, kV>), grid, dim3(kThreads), 0, s, a);
+    constexpr int kTokens = threads_of(kV) / kL;
+    const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens)), block(threads_of(kV));
+    if (grad) hipLaunchKernelGGL((k_route_grad<kBf16, kL, kV>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_route<kBf16, kL, kV>), grid, block, 0, s, a);
 }
 template <int kBf16>
 void launch(const Args& a, bool grad, hipStream_t s) {
-    const int v = (a.E + 63) / 64;
-    if (v <= 1) launch<kBf16, 1>(a, grad, s);
-    else if (v <= 2) launch<kBf16, 2>(a, grad, s);
-    else if (v <= 4) launch<kBf16, 4>(a, grad, s);
-    else if (v <= 8) launch<kBf16, 8>(a, grad, s);
-    else if (v <= 16) launch<kBf16, 16>(a, grad, s);
-    else launch<kBf16, 64>(a, grad, s);
+    if (a.E <= 64) launch<kBf16, 8, 8>(a, grad, s);
+    else if (a.E <= 128) launch<kBf16, 16, 8>(a, grad, s);
+    else if (a.E <= 256) launch<kBf16, 32, 8>(a, grad, s);
+    else if (a.E <= 512) launch<kBf16, 64, 8>(a, grad, s);
+    else if (a.E <= 1024) launch<kBf16, 64, 16>(a, grad, s);
+    else launch<kBf16, 64, 64>(a, grad, s);
 }
 
 inline int check(int dtype, int64_t T, int32_t E, int64_t ld, int32_t topk, int renorm) {

@@ -355,3 +355,91 @@ def test_same_bits_every_time(Q):
     for _ in range(3):
         for a, b in zip(everything(Q, s), first):
             assert torch.equal(a, b)
+
+
+def test_bf16_bits(Q):
+    """bf16 as int16 or uint16 bit patterns: the same results, sums and gradients in that type."""
+    t, h, e, k = 12, 72, 16, 2
+    s = dict(x=randn(t, h, seed=1, dtype=torch.bfloat16), res=randn(t, h, seed=2, dtype=torch.bfloat16),
+             w=randn(h, seed=3, dtype=torch.bfloat16), g=randn(t, h, seed=4, dtype=torch.bfloat16),
+             z=randn(t, e, seed=5, dtype=torch.bfloat16), gw=randn(t, k, seed=6))
+    want = None
+    for dtype in (torch.bfloat16, torch.int16, torch.uint16):
+        v = {n: a.view(dtype) if a.dtype == torch.bfloat16 else a for n, a in s.items()}
+        n = Q.quads_rmsnorm(v["x"], v["w"], EPS, v["res"])
+        assert n["sum"].dtype == dtype and n["y"].dtype == torch.bfloat16
+        dx, dres, dw = Q.quads_rmsnorm_backward(v["g"], n["sum"], v["w"], EPS, v["g"])
+        assert dx.dtype == dres.dtype == dw.dtype == dtype
+        ids, tw = Q.quads_moe_route(v["z"], k)
+        dz = Q.quads_moe_route_backward(v["z"], ids, tw, v["gw"])
+        assert dz.dtype == dtype
+        _, _, pos = Q.quads_moe_pack(ids, e)
+        xs, xr = Q.quads_moe_sort(v["x"], pos, k), Q.quads_moe_sort(v["x"], pos, k, rows=t * k + 3)
+        o = Q.quads_moe_unsort(xs, pos, k, tw, Q.OUT_BF16)
+        dy, dtw = Q.quads_moe_unsort_backward(v["g"], xs, pos, k, tw)
+        assert xs.dtype == xr.dtype == dy.dtype == dtype and o.dtype == torch.bfloat16
+        got = [n["sum"], n["y"], dx, dw, ids, tw, dz, xs, xr, o, dy, dtw]
+        got = [a.view(torch.int16) if a.element_size() == 2 else a for a in got]
+        want = want or got
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_offsets_beyond_32_bits(Q):
+    """More than 2^31 channels (and more than 2^32 bytes): the last rows as a call on them alone."""
+    h, t = 4096, 2 ** 19 + 3
+    x = torch.empty((t, h), dtype=torch.bfloat16, device=DEV)
+    x[:] = randn(1, h, seed=1, dtype=torch.bfloat16)
+    x[-3:] = randn(3, h, seed=2, dtype=torch.bfloat16)
+    w = randn(h, seed=3, dtype=torch.bfloat16)
+    for out, key in ((Q.OUT_BF16, "y"), (Q.OUT_MX_FP8, "codes")):
+        r = Q.quads_rmsnorm(x, w, EPS, out_dtype=out)
+        a = Q.quads_rmsnorm(x[-3:].contiguous(), w, EPS, out_dtype=out)
+        assert torch.equal(r[key][-3:], a[key])
+        if out == Q.OUT_MX_FP8:
+            assert torch.equal(r["scales"][-3:], a["scales"])
+        del r
+    dx, _, _ = Q.quads_rmsnorm_backward(x, x, w, EPS, x)
+    b, _, _ = Q.quads_rmsnorm_backward(*[x[-3:].contiguous()] * 2, w, EPS, x[-3:].contiguous())
+    assert torch.equal(dx[-3:], b)
+    del dx
+    pos = torch.arange(t - 1, -1, -1, dtype=torch.int32, device=DEV)
+    xs = Q.quads_moe_sort(x, pos, 1)
+    assert torch.equal(xs[:3], x[-3:].flip(0)) and torch.equal(xs[-1], x[0])
+    o = Q.quads_moe_unsort(xs, pos, 1, out_dtype=Q.OUT_BF16)
+    assert torch.equal(o[-3:], x[-3:])
+    dy, dw = Q.quads_moe_unsort_backward(o, xs, pos, 1, torch.ones((t, 1), device=DEV))
+    assert torch.equal(dy[:3], x[-3:].flip(0))
+    n2 = (x[-3:].double() ** 2).sum(1)
+    assert ((dw[-3:, 0].double() - n2).abs() <= (h / 64 + 24) * U * n2).all()
+    del xs, o, dy
+    z = x.view(-1, 128)[: 2 ** 24 - 1]                              # 2^31 logits
+    ids, tw = Q.quads_moe_route(z, 8)
+    i2, w2 = Q.quads_moe_route(z[-5:].contiguous(), 8)
+    assert torch.equal(ids[-5:], i2) and torch.equal(tw[-5:], w2)
+    dz = Q.quads_moe_route_backward(z, ids, tw, tw, False)
+    d2 = Q.quads_moe_route_backward(z[-5:].contiguous(), i2, w2, w2, False)
+    assert torch.equal(dz[-5:], d2)
+
+
+def test_views_are_taken(Q):
+    """Column slices and transposed views of every input give what their copies give."""
+    t, h, k, e = 10, 48, 2, 8
+    x, g, y = randn(t, h + 5, seed=1)[:, 5:], randn(h, t, seed=2).t(), randn(t * k, 2 * h, seed=3)[:, ::2]
+    z = randn(e, t, seed=4).t()
+    c = [a.contiguous() for a in (x, g, y, z)]
+    ids, tw = Q.quads_moe_route(z, k)
+    assert torch.equal(ids, Q.quads_moe_route(c[3], k)[0])
+    _, _, pos = Q.quads_moe_pack(ids, e)
+    assert torch.equal(Q.quads_moe_sort(x, pos, k), Q.quads_moe_sort(c[0], pos, k))
+    assert torch.equal(Q.quads_moe_unsort(y, pos, k, tw), Q.quads_moe_unsort(c[2], pos, k, tw))
+    for a, b in zip(Q.quads_moe_unsort_backward(g, y, pos, k, tw),
+                    Q.quads_moe_unsort_backward(c[1], c[2], pos, k, tw)):
+        assert torch.equal(a, b)
+    w = randn(2 * h, seed=5)[::2]
+    for a, b in zip(Q.quads_rmsnorm_backward(g, x, w, EPS, g),
+                    Q.quads_rmsnorm_backward(c[1], c[0], w.contiguous(), EPS, c[1])):
+        assert torch.equal(a, b)
+    gz = randn(k, t, seed=6).t()
+    assert torch.equal(Q.quads_moe_route_backward(z, ids, tw, gz, False),
+                       Q.quads_moe_route_backward(c[3], ids, tw, gz.contiguous(), False))
