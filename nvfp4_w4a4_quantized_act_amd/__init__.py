@@ -604,7 +604,7 @@ def _call(fn, dev, *args):
     integer: building torch.cuda.current_stream's object takes 1.9 us, a tenth of a small
     call)."""
     stream = torch._C._cuda_getCurrentRawStream(dev.index)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:      # current_device() without its first lines
         status = getattr(lib(), fn)(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -789,44 +789,44 @@ def quads_topk_distill_grad(logits, t_val, t_id, weight=None, inv_temp=1.0, reno
 # bits; what is new is returned as torch.bfloat16, a gradient or a sum in its input's type.
 
 _FLOATS = (torch.float32, torch.bfloat16)
+_CODES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16, torch.int16: OUT_BF16,
+          torch.uint16: OUT_BF16}
+
+
+def _code(name, t):
+    code = _CODES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None:
+        raise TypeError(f"{name} must be a float32 or bf16 tensor (torch.bfloat16, int16 or "
+                        "uint16 bits)")
+    return code
 
 
 def _rows(name, t, shape=None, dev=None):
     """(t, dtype code, row stride) of a 2-D tensor with dense, 16-byte aligned rows; copied if
     it is not one already.  Any row stride is taken as it is."""
-    if dev is None:
-        dev = _gpu(name, t)
-    elif not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.dtype == torch.bfloat16:
-        code = OUT_BF16
-    elif t.dtype == torch.float32:
-        code = OUT_F32
-    elif t.dtype in (torch.int16, torch.uint16):
-        code = OUT_BF16
-    else:
-        raise TypeError(f"{name} must be float32 or bf16 (torch.bfloat16, int16 or uint16 bits)")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
+    code = _code(name, t)
+    s = t.shape
+    if len(s) != 2 or (shape is not None and s != shape):
         raise ValueError(f"{name} must have the shape "
                          f"{'[rows, channels]' if shape is None else tuple(shape)}, "
-                         f"not {tuple(t.shape)}")
-    if t.device != dev:
+                         f"not {tuple(s)}")
+    if dev is None:
+        _gpu(name, t)
+    elif t.device != dev:
         raise ValueError(f"{name} must be on {dev}, not on {t.device}")
-    n, h = t.shape
+    n, h = s
     if t.is_contiguous():
-        if t.data_ptr() % 16:
-            t = t.detach().clone(memory_format=torch.contiguous_format)
-        return t, code, h
+        return (t.detach().clone() if t.data_ptr() % 16 else t), code, h
     if n and h and (t.stride(1) != 1 or (n > 1 and not h <= t.stride(0) < 2**31)
                     or t.data_ptr() % 16):
         t = t.detach().clone(memory_format=torch.contiguous_format)
     return t, code, (t.stride(0) if n > 1 else h)
 
 
-def _dense(name, t, shape, dev):
+def _dense(name, t, shape=None, dev=None):
     """(t, dtype code) of dense rows."""
     t, code, ld = _rows(name, t, shape, dev)
-    if ld != shape[1]:
+    if ld != t.shape[1]:
         t = t.detach().clone(memory_format=torch.contiguous_format)
     return t, code
 
@@ -834,13 +834,9 @@ def _dense(name, t, shape, dev):
 def _weight(weight, h, dev):
     if weight is None:
         return None, OUT_F32
-    if not isinstance(weight, torch.Tensor) or weight.dtype not in (
-            torch.float32, torch.bfloat16, torch.int16, torch.uint16):
-        raise TypeError("weight must be float32 or bf16 (torch.bfloat16, int16 or uint16 bits)")
+    code = _code("weight", weight)
     w = _want("weight", weight, weight.dtype, (h,), dev)
-    if w.data_ptr() % 16:
-        w = w.detach().clone()
-    return w, OUT_F32 if w.dtype == torch.float32 else OUT_BF16
+    return (w.detach().clone() if w.data_ptr() % 16 else w), code
 
 
 def quads_rmsnorm_amax_groups(t, h):
@@ -856,12 +852,13 @@ def quads_rmsnorm(x, weight=None, eps=1e-6, residual=None, out_dtype=OUT_BF16, w
     wanted)."""
     x, xt, ldx = _rows("x", x)
     dev = x.device
-    t, h = x.shape
+    shape = x.shape
+    t, h = shape
     rt, ldr = OUT_F32, h
     out = {}
     total = None
     if residual is not None:
-        residual, rt, ldr = _rows("residual", residual, x.shape, dev)
+        residual, rt, ldr = _rows("residual", residual, shape, dev)
         if want_sum:
             total = out["sum"] = torch.empty(t, h, dtype=residual.dtype, device=dev)
     weight, wt = _weight(weight, h, dev)
@@ -986,10 +983,8 @@ def quads_moe_unsort(y, pos, topk, topk_w=None, out_dtype=OUT_F32):
     """Packed rows y [rows, H] back in token order: out[t] = sum over slots in order of
     topk_w[t, s] * y[pos[t * topk + s]] (without the weights for None) -> [T, H].  Slots whose
     pos is outside [0, rows) add nothing."""
-    dev = _gpu("y", y)
-    if y.dim() != 2:
-        raise ValueError("y must be [rows, H]")
-    y, code = _dense("y", y, y.shape, dev)
+    y, code = _dense("y", y)
+    dev = y.device
     rows, h = y.shape
     pos, topk_w, t = _slots(pos, topk, topk_w, dev)
     out = torch.empty(t, h, dtype=_FLOATS[1 if out_dtype == OUT_BF16 else 0], device=dev)
@@ -1003,10 +998,8 @@ def quads_moe_unsort_backward(g, y, pos, topk, topk_w, rows=None, want_dy=True, 
     y's type or None, dw fp32 [T, topk] or None).  rows as in quads_moe_sort: None says that pos
     is a permutation of y's rows; otherwise it is y's number of rows, and rows of dy without a
     slot are 0."""
-    dev = _gpu("y", y)
-    if y.dim() != 2:
-        raise ValueError("y must be [rows, H]")
-    y, yt = _dense("y", y, y.shape, dev)
+    y, yt = _dense("y", y)
+    dev = y.device
     n, h = y.shape
     pos, topk_w, t = _slots(pos, topk, topk_w, dev)
     g, gt = _dense("g", g, (t, h), dev)
