@@ -45,7 +45,7 @@ extern "C" {
  *   x, ldx, x_dtype                rows of x
  *   residual, ldr, res_dtype       NULL or the rows of the residual stream
  *   weight, w_dtype                NULL (ones) or [H]
- *   eps                            > 0, finite
+ *   eps                            1e-70 <= eps <= 1e70
  *   sum        NULL or out [T, H] in the residual's type: h (NULL without a
  *              residual).  May be residual, or x, where that is dense and of
  *              the residual's type
@@ -61,7 +61,8 @@ extern "C" {
  * 1 <= H < 2^26, T < 2^31.  The mean is formed in fp64; with QUADS_OUT_MX_FP8
  * so is y (each code and scale is that of the exact y unless it lies within
  * about 2^-50 of a border).  fp32 and bf16 outputs come from two fp32 products
- * (3 * 2^-24 of the value) and are rounded once.
+ * (3 * 2^-24 of the value; two bits more in rows whose root mean square is above
+ * 2^126) and are rounded once.
  */
 int64_t quads_rmsnorm_amax_groups(int64_t T, int64_t H);
 int quads_rmsnorm(const void* x, int x_dtype, int64_t T, int64_t H, int64_t ldx,
@@ -129,7 +130,8 @@ int quads_moe_route_backward(const void* logits, int dtype, int64_t T, int32_t E
  *   x          [T, H], `dtype`, row stride ldx; 1 <= H < 2^26, T < 2^24,
  *              1 <= topk <= 64, T * topk < 2^31
  *   pos        int32 [T * topk]: a value outside [0, rows) means that the slot
- *              is left out; of several slots with one row, some one is kept
+ *              is left out.  A row is named once at most (named more often, each
+ *              of its channels is one of its slots', any of them)
  *   out        [rows, H], 0 <= rows < 2^31.  Rows that no slot names are left
  *              as they were.  Not x.
  */
@@ -149,7 +151,7 @@ int quads_moe_unsort(const void* y, int y_dtype, int64_t rows, const int32_t* po
                      int out_dtype, void* stream);
 
 /*
- * Gradient of quads_moe_unsort:
+ * Gradient of quads_moe_unsort, for a pos that names a row once at most:
  *   dy[pos[t * topk + s]] = topk_w[t, s] g[t];  dw[t, s] = sum_j g_tj y[pos, j]
  *   g          [T, H], g_dtype
  *   y, y_dtype the forward call's (may be NULL when dw is)

@@ -17,21 +17,17 @@ using namespace block;
 
 constexpr int kNone = 2;                     // no residual
 
-// Sum over n waves of a work-group, from wave `first` on (one barrier, of the whole
-// work-group), in every thread of theirs.  s_part: two sets of one number per wave, taken
-// in turn by calls that follow one another (`set` 0, 1, 0, ..): a wave is past the barrier
-// of the call between when it writes a set again, and so every wave has read it.
+// Sum over a work-group of up to 16 waves (one barrier), in every thread.  s_part: two
+// sets of one number per wave, taken in turn by calls that follow one another (`set`
+// 0, 1, 0, ..): a wave is past the barrier of the call between when it writes a set
+// again, and so every wave has read it.
 constexpr int kMaxWaves = 16;
-__device__ __forceinline__ double group_sum(double v, double (*s_part)[kMaxWaves], int set,
-                                            int first, int n) {
+__device__ __forceinline__ double group_sum(double v, double (*s_part)[kMaxWaves], int set) {
     v = lanes_sum<64>(v);
     if ((threadIdx.x & 63) == 0) s_part[set][threadIdx.x >> 6] = v;
     __syncthreads();
     const int i = threadIdx.x & (kMaxWaves - 1);
-    return lanes_sum<kMaxWaves>(i < n ? s_part[set][first + i] : 0.0);
-}
-__device__ __forceinline__ double group_sum(double v, double (*s_part)[kMaxWaves], int set) {
-    return group_sum(v, s_part, set, 0, (int)(blockDim.x >> 6));
+    return lanes_sum<kMaxWaves>(i < (int)(blockDim.x >> 6) ? s_part[set][i] : 0.0);
 }
 
 // Eight channels of the weight in either type; 1 without one.
@@ -56,7 +52,8 @@ inline int check_sizes(int64_t T, int64_t H, int64_t ld) {
     if (T < 0 || T >= ((int64_t)1 << 31) || H < 1 || H >= kMaxH) return QUADS_ESHAPE;
     return ld < H || ld >= kMaxStride ? QUADS_ESHAPE : QUADS_OK;
 }
-inline bool ok_eps(double eps) { return eps > 0.0 && eps <= 1.7976931348623157e308; }
+// r is held in fp32 where it is not in fp64.
+inline bool ok_eps(double eps) { return eps >= 1e-70 && eps <= 1e70; }
 
 }  // namespace norm
 }  // namespace quads

@@ -214,8 +214,8 @@ def route(logits, topk, renorm=True):
     Differentiable in the logits, through the weights of the chosen experts."""
     _code(logits.dtype)
     w, ids = Route.apply(logits.reshape(-1, logits.shape[-1]), int(topk), bool(renorm))
-    lead = logits.shape[:-1]
-    return w.reshape(*lead, -1), ids.reshape(*lead, -1)
+    shape = logits.shape[:-1] + (int(topk),)
+    return w.reshape(shape), ids.reshape(shape)
 
 
 class SortTokens(torch.autograd.Function):
@@ -237,8 +237,8 @@ class SortTokens(torch.autograd.Function):
 def sort_tokens(x, pos, topk, rows=None):
     """Tokens x [T, H] (float32 or bf16) in expert order [rows, H]: row pos[t * topk + s] is x[t].
     rows None: pos is a permutation of the T * topk rows (`quads_moe_pack`'s).  With rows given,
-    slots whose pos is outside [0, rows) are left out and rows without a slot are 0.
-    Differentiable in x."""
+    slots whose pos is outside [0, rows) are left out and rows without a slot are 0; no row has
+    two slots.  Differentiable in x."""
     _code(x.dtype)
     return SortTokens.apply(x, pos, int(topk), rows)
 

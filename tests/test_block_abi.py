@@ -42,7 +42,7 @@ def test_norm_validation():
     assert call(h=0) == -2 and call(h=1 << 26, ldx=1 << 26) == -2
     assert call(ldx=63) == -2 and call(ldr=63) == -2 and call(ldx=1 << 31) == -2
     assert call(xt=2) == -1 and call(rt=2) == -1 and call(wt=-1) == -1 and call(yt=3) == -1
-    for eps in (0.0, -1.0, INF, NAN):
+    for eps in (0.0, -1.0, 9e-71, 2e70, INF, NAN):
         assert call(eps=eps) == -1
     assert call(x=None) == -1 and call(x=MIS) == -1 and call(res=MIS) == -1
     assert call(w=MIS) == -1 and call(total=MIS) == -1 and call(y=None) == -1 and call(y=MIS) == -1
@@ -69,7 +69,7 @@ def test_norm_backward_validation():
         return f(g, gt, h, ht, t, hh, ldh, w, wt, eps, gs, dx, dt, dres, dw, wsp, wsz, None)
     assert call(t=-1) == -2 and call(hh=0) == -2 and call(ldh=63) == -2
     assert call(gt=2) == -1 and call(ht=2) == -1 and call(dt=2) == -1 and call(wt=2) == -1
-    assert call(eps=0.0) == -1 and call(eps=NAN) == -1
+    assert call(eps=0.0) == -1 and call(eps=NAN) == -1 and call(eps=9e-71) == -1
     assert call(g=None) == -1 and call(h=MIS) == -1 and call(gs=MIS) == -1 and call(dx=None) == -1
     assert call(dres=MORE) == -1 and call(dres=MIS) == -1        # dres is not dx
     assert call(dx=FAKE) == -1                                   # dx over h

@@ -161,7 +161,7 @@ def test_norm_magnitudes(Q, by):
     """Squares below and beyond fp32's range."""
     for out in ("f32", "bf16", "fp8"):
         check_norm(Q, 6, 512, "f32", "f32", "f32", out, by=by, eps=1e-5)
-        check_norm(Q, 6, 512, "bf16", "bf16", "bf16", out, by=by, eps=1e-300)
+        check_norm(Q, 6, 512, "bf16", "bf16", "bf16", out, by=by, eps=1e-70)
 
 
 def test_norm_zero_rows_and_blocks(Q):
@@ -172,7 +172,11 @@ def test_norm_zero_rows_and_blocks(Q):
     codes, scales = OB.rmsnorm_mx(f64(x), None, EPS)
     assert np.array_equal(r["codes"].cpu().numpy(), codes)
     assert np.array_equal(r["scales"].cpu().numpy(), scales) and scales[0].tolist() == [0] * 4
-    assert not f64(Q.quads_rmsnorm(x)["y"][0]).any()
+    for eps in (1e-6, 1e-70):
+        for out in (Q.OUT_F32, Q.OUT_BF16):
+            assert not f64(Q.quads_rmsnorm(x, eps=eps, out_dtype=out)["y"][[0, 2]]).any()
+        dx, _, dw = Q.quads_rmsnorm_backward(x[[0, 2]], x[[0, 2]], torch.ones(128, device=DEV), eps)
+        assert not f64(dx).any() and not f64(dw).any()
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])

@@ -443,3 +443,17 @@ def test_views_are_taken(Q):
     gz = randn(k, t, seed=6).t()
     assert torch.equal(Q.quads_moe_route_backward(z, ids, tw, gz, False),
                        Q.quads_moe_route_backward(c[3], ids, tw, gz.contiguous(), False))
+
+
+def test_autograd_of_nothing(Q):
+    """No tokens: empty results, a zero gradient of the weight."""
+    x = torch.zeros((0, 32), device=DEV, requires_grad=True)
+    w = torch.ones(32, device=DEV, requires_grad=True)
+    z = torch.zeros((0, 8), device=DEV, requires_grad=True)
+    y, h = qat.rms_norm(x, w, EPS, residual=x)
+    tw, ids = qat.route(z, 2)
+    pos = torch.zeros(0, dtype=torch.int32, device=DEV)
+    o = qat.unsort_tokens(qat.sort_tokens(y, pos, 2), pos, 2, tw)
+    assert y.shape == h.shape == o.shape == (0, 32) and tw.shape == ids.shape == (0, 2)
+    gx, gw, gz = torch.autograd.grad(o.sum() + h.sum(), [x, w, z])
+    assert gx.shape == (0, 32) and gz.shape == (0, 8) and not gw.any()
