@@ -28,9 +28,12 @@ struct GradArgs {
 // 69 us against 74.5).  A work-group holds several rows at once, up to 1024 threads, and
 // takes more in turn: each thread keeps its channels' weight and their part of dweight in
 // registers all the while, and a work-group leaves one partial dweight at its end.  The
-// kernel runs at HBM's rate (16384 x 2048 bf16 with dweight 52.7 us, 5.1 TB/s; two kernels
+// kernel runs at HBM's rate (16384 x 2048 bf16 with dweight 51 us, 5.3 TB/s; two kernels
 // that each read g and h took four times as long); the next row's loads asked for before
-// the sums bring nothing (57.8 against 57.6 us with the join).
+// the sums bring nothing (57.8 against 57.6 us with the join).  bf16 rows of whole 16 bytes
+// are read past the caches: 16384 x 2048 57.4 us / 55.1, 8192 x 4096 58.2 / 54.9, 65536 x
+// 128 19.2 / 18.5; fp32's 32 bytes of a lane are two accesses to a line, 8192 x 8192 195 us
+// against 217.
 template <int kG, int kH, int kLanes, int kV, int kCut>
 __global__ __launch_bounds__(1024) void k_rms_grad_held(GradArgs a, int lanes_) {
     __shared__ double s_sq[2][kMaxWaves], s_dot[2][kMaxWaves];
@@ -58,10 +61,13 @@ __global__ __launch_bounds__(1024) void k_rms_grad_held(GradArgs a, int lanes_) 
             g[j] = Raw<kG>{};
             h[j] = s[j] = Raw<kH>{};
             if (live && p[j].n > 0) {
-                g[j] = load<kG, kCut != kTiny>(row_at<kG>(a.g, t * a.H), p[j].at, p[j].n);
-                h[j] = load<kH, kCut != kTiny>(row_at<kH>(a.h, t * a.ldh), p[j].at, p[j].n);
+                g[j] = load<kG, kCut != kTiny, kG && kCut == kEven>(row_at<kG>(a.g, t * a.H),
+                                                                    p[j].at, p[j].n);
+                h[j] = load<kH, kCut != kTiny, kH && kCut == kEven>(row_at<kH>(a.h, t * a.ldh),
+                                                                    p[j].at, p[j].n);
                 if (a.g_sum)
-                    s[j] = load<kH, kCut != kTiny>(row_at<kH>(a.g_sum, t * a.H), p[j].at, p[j].n);
+                    s[j] = load<kH, kCut != kTiny, kH && kCut == kEven>(
+                        row_at<kH>(a.g_sum, t * a.H), p[j].at, p[j].n);
             }
         }
         double sq = 0.0, dot = 0.0;

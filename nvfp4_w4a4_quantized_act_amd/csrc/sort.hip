@@ -9,6 +9,8 @@
 // once too, whole rows of it at places of its own.
 #include "block.h"
 
+#include <type_traits>
+
 namespace quads {
 namespace sorting {
 
@@ -53,9 +55,12 @@ __device__ __forceinline__ int64_t slot_row(const int32_t* pos, int64_t at, int6
 
 constexpr int kBatch = 8;                    // slots whose rows are asked for together
 
-template <int kT, int kOnce, int kLanes, int kCut>
+// Copies know no type: an fp32 row goes as twice as many 16-bit channels, 16 bytes a lane
+// next to one another (eight fp32 channels a lane, 4096 x 2048, top 8: 122 us against 54).
+template <int kOnce, int kLanes, int kCut>
 __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_sort(Args a,
                                                               const int32_t* __restrict__ pos) {
+    constexpr int kT = 1;
     const Place<kLanes, kCut> at(a);
     if (at.p.n <= 0) return;
     const Raw<kT> r = load<kT, kCut != kTiny>(row_at<kT>(a.a, at.t * a.ld), at.p.at, at.p.n);
@@ -165,9 +170,10 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort_grad(
 // ------------------------------------------------------------------- host --
 // Packed rows beyond what the caches keep go past them (kOnce: 1 their loads, 2 their
 // stores), us: loads from 16 MB on (gradient 4096 x 2048, top 8, bf16 53 against 63, unsort
-// 28 / 30; 64 x 4096, top 8, fp32 11.6 / 8.7), stores from 192 MB on (sort 16384 x 4096,
-// top 8, bf16 212 / 242; 4096 x 2048 27.4 / 28.0, but what reads them then, 48.7 / 55 for
-// both).  Stores only where rows are whole lines of 16 bytes.
+// 28 / 30; 16384 x 128, top 2, 7.9 / 7.0), stores from 192 MB on (sort 16384 x 4096, top 8,
+// bf16 212 / 242; 4096 x 2048 27.4 / 28.0, but with the call that reads them 55 / 48.7).
+// Stores only of whole 16 bytes, neither of fp32, whose 32 bytes of a lane are two accesses
+// to a line (the gradient 16384 x 4096, top 4, fp32 511 / 469).
 constexpr int64_t kOnceLoads = (int64_t)16 << 20, kOnceStores = (int64_t)192 << 20;
 
 struct Shape {
@@ -190,35 +196,44 @@ inline Shape shape_of(int64_t T, int64_t H, bool parts) {
 // A launch has fewer than 2^32 threads: tokens of one launch, at most.
 constexpr int64_t kLaunchTokens = (int64_t)1 << 21;
 
-#define QUADS_LAUNCH(kernel, O, L, C, ...) \
-    hipLaunchKernelGGL((kernel<types..., O, L, C>), p.grid, dim3(p.threads), 0, s, __VA_ARGS__)
-#define QUADS_ROWS(kernel, once, ...)                                                          \
-    const Cut cut = cut_of(a.H);                                                               \
-    if (cut == kTiny) QUADS_LAUNCH(kernel, 0, 8, kTiny, __VA_ARGS__);                          \
-    else if (p.lanes == 8 && cut == kEven) QUADS_LAUNCH(kernel, 0, 8, kEven, __VA_ARGS__);     \
-    else if (p.lanes == 8) QUADS_LAUNCH(kernel, 0, 8, kOdd, __VA_ARGS__);                      \
-    else if (p.lanes == 16 && cut == kEven) QUADS_LAUNCH(kernel, 0, 16, kEven, __VA_ARGS__);   \
-    else if (p.lanes == 16) QUADS_LAUNCH(kernel, 0, 16, kOdd, __VA_ARGS__);                    \
-    else if (p.lanes == 32 && cut == kEven) QUADS_LAUNCH(kernel, 0, 32, kEven, __VA_ARGS__);   \
-    else if (p.lanes == 32) QUADS_LAUNCH(kernel, 0, 32, kOdd, __VA_ARGS__);                    \
-    else if (once && cut == kEven) QUADS_LAUNCH(kernel, once, 0, kEven, __VA_ARGS__);          \
-    else if (once) QUADS_LAUNCH(kernel, once, 0, kOdd, __VA_ARGS__);                           \
-    else if (cut == kEven) QUADS_LAUNCH(kernel, 0, 0, kEven, __VA_ARGS__);                     \
-    else QUADS_LAUNCH(kernel, 0, 0, kOdd, __VA_ARGS__);
+template <int kValue>
+using Int = std::integral_constant<int, kValue>;
+// f(kOnce, kLanes, kCut) of rows of H channels; kOnce for work-groups of one token only.
+template <int kOnce, typename F>
+void with_shape(const Shape& p, int64_t H, F f) {
+    const Cut cut = cut_of(H);
+    if (cut == kTiny) f(Int<0>{}, Int<8>{}, Int<kTiny>{});
+    else if (p.lanes == 8 && cut == kEven) f(Int<0>{}, Int<8>{}, Int<kEven>{});
+    else if (p.lanes == 8) f(Int<0>{}, Int<8>{}, Int<kOdd>{});
+    else if (p.lanes == 16 && cut == kEven) f(Int<0>{}, Int<16>{}, Int<kEven>{});
+    else if (p.lanes == 16) f(Int<0>{}, Int<16>{}, Int<kOdd>{});
+    else if (p.lanes == 32 && cut == kEven) f(Int<0>{}, Int<32>{}, Int<kEven>{});
+    else if (p.lanes == 32) f(Int<0>{}, Int<32>{}, Int<kOdd>{});
+    else if (cut == kEven) f(Int<kOnce>{}, Int<0>{}, Int<kEven>{});
+    else f(Int<kOnce>{}, Int<0>{}, Int<kOdd>{});
+}
 
 // `bytes`: of the packed rows that the slots name.
-template <int... types>
-void launch_sort(const Args& a, const int32_t* pos, int64_t bytes, hipStream_t s) {
+inline void launch_sort(const Args& a, const int32_t* pos, int64_t bytes, hipStream_t s) {
     const Shape p = shape_of(a.T, a.H, true);
-    if (bytes > kOnceStores) { QUADS_ROWS(k_sort, 2, a, pos) }
-    else { QUADS_ROWS(k_sort, 0, a, pos) }
+    auto go = [&](auto once, auto lanes, auto cut) {
+        hipLaunchKernelGGL((k_sort<once(), lanes(), cut()>), p.grid, dim3(p.threads), 0, s, a, pos);
+    };
+    if (bytes > kOnceStores) with_shape<2>(p, a.H, go);
+    else with_shape<0>(p, a.H, go);
 }
-template <int... types>
+template <int kY, int kOut>
 void launch_unsort(const Args& a, const int32_t* pos, const float* w, int64_t bytes,
                    hipStream_t s) {
     const Shape p = shape_of(a.T, a.H, true);
-    if (bytes > kOnceLoads) { QUADS_ROWS(k_unsort, 1, a, pos, w) }
-    else { QUADS_ROWS(k_unsort, 0, a, pos, w) }
+    auto go = [&](auto once, auto lanes, auto cut) {
+        hipLaunchKernelGGL((k_unsort<kY, kOut, once(), lanes(), cut()>), p.grid, dim3(p.threads), 0,
+                           s, a, pos, w);
+    };
+    if constexpr (kY != 0) {
+        if (bytes > kOnceLoads) return with_shape<1>(p, a.H, go);
+    }
+    with_shape<0>(p, a.H, go);
 }
 // Slots of a work-group: all of them, fewer where there are few tokens (64 x 2048, top 8,
 // bf16: 6.7 us against 4.2; 64 x 4096 fp32 8.7 / 6.7).
@@ -226,16 +241,20 @@ inline int slots_of(int64_t T, int topk) {
     const int64_t per = T * topk / 512;
     return per < 1 ? 1 : (per < topk ? (int)per : topk);
 }
-template <int... types>
+template <int kG, int kY>
 void launch_grad(const Args& a, const int32_t* pos, const float* w, int64_t bytes, hipStream_t s) {
     Shape p = shape_of(a.T, a.H, false);
     if (!p.lanes) p.grid.y = (a.topk + a.per - 1) / a.per;
-    if (bytes > kOnceStores) { QUADS_ROWS(k_unsort_grad, 3, a, pos, w) }
-    else if (bytes > kOnceLoads) { QUADS_ROWS(k_unsort_grad, 1, a, pos, w) }
-    else { QUADS_ROWS(k_unsort_grad, 0, a, pos, w) }
+    auto go = [&](auto once, auto lanes, auto cut) {
+        hipLaunchKernelGGL((k_unsort_grad<kG, kY, once(), lanes(), cut()>), p.grid, dim3(p.threads),
+                           0, s, a, pos, w);
+    };
+    if constexpr (kY != 0) {
+        if (bytes > kOnceStores) return with_shape<3>(p, a.H, go);
+        if (bytes > kOnceLoads) return with_shape<1>(p, a.H, go);
+    }
+    with_shape<0>(p, a.H, go);
 }
-#undef QUADS_ROWS
-#undef QUADS_LAUNCH
 
 inline int check(int64_t T, int64_t H, int64_t ld, int32_t topk, int64_t rows) {
     if (T < 0 || T >= ((int64_t)1 << 24) || H < 1 || H >= kMaxH || ld < H || ld >= kMaxStride)
@@ -264,9 +283,9 @@ extern "C" int quads_moe_sort(const void* x, int dtype, int64_t T, int64_t H, in
     const int64_t bytes = T * topk * H * size;
     for (int64_t t = 0; t < T; t += kLaunchTokens) {
         const Args a = {(const char*)x + t * ldx * size, nullptr, out, nullptr,
-                        T - t < kLaunchTokens ? T - t : kLaunchTokens, H, ldx, rows, topk, topk};
-        if (dtype == QUADS_OUT_BF16) launch_sort<1>(a, pos + t * topk, bytes, s);
-        else launch_sort<0>(a, pos + t * topk, bytes, s);
+                        T - t < kLaunchTokens ? T - t : kLaunchTokens, H * size / 2,
+                        ldx * size / 2, rows, topk, topk};
+        launch_sort(a, pos + t * topk, bytes, s);
         QUADS_CHECK_LAUNCH();
     }
     return QUADS_OK;
