@@ -132,11 +132,15 @@ int quads_moe_route_backward(const void* logits, int dtype, int64_t T, int32_t E
  *   pos        int32 [T * topk]: a value outside [0, rows) means that the slot
  *              is left out.  A row is named once at most (named more often, each
  *              of its channels is one of its slots', any of them)
- *   out        [rows, H], 0 <= rows < 2^31.  Rows that no slot names are left
- *              as they were.  Not x.
+ *   out        [rows, H], 0 <= rows < 2^31; not x
+ *   zero_rest  0: rows of out that no slot names are left as they were;  1: they
+ *              are zeroed, with quads_moe_sort_ws bytes of workspace (4 a row for
+ *              large outputs, else 0; its content is of no account)
  */
+size_t quads_moe_sort_ws(int64_t rows, int64_t H, int dtype, int zero_rest);
 int quads_moe_sort(const void* x, int dtype, int64_t T, int64_t H, int64_t ldx,
-                   const int32_t* pos, int32_t topk, int64_t rows, void* out, void* stream);
+                   const int32_t* pos, int32_t topk, int64_t rows, int zero_rest, void* out,
+                   void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Back into token order: out[t] = sum over slots in order of
@@ -155,14 +159,16 @@ int quads_moe_unsort(const void* y, int y_dtype, int64_t rows, const int32_t* po
  *   dy[pos[t * topk + s]] = topk_w[t, s] g[t];  dw[t, s] = sum_j g_tj y[pos, j]
  *   g          [T, H], g_dtype
  *   y, y_dtype the forward call's (may be NULL when dw is)
- *   dy         NULL or out [rows, H] in y's type; rows that no slot names are
- *              left as they were; may be y
+ *   dy         NULL or out [rows, H] in y's type; may be y (zero_rest 0)
+ *   zero_rest, ws   rows of dy that no slot names, as in quads_moe_sort (the
+ *              workspace for y's type)
  *   dw         NULL or out fp32 [T, topk], summed in fp32; 0 where the slot is
  *              left out.  NULL when topk_w is
  */
 int quads_moe_unsort_backward(const void* g, int g_dtype, const void* y, int y_dtype,
                               int64_t rows, const int32_t* pos, const float* topk_w, int64_t T,
-                              int32_t topk, int64_t H, void* dy, float* dw, void* stream);
+                              int32_t topk, int64_t H, int zero_rest, void* dy, float* dw,
+                              void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

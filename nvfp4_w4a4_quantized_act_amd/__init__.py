@@ -123,10 +123,11 @@ _SIGNATURES = {
     "quads_moe_route": (_INT, [_P, _INT, _I64, _I32, _I64, _I32, _INT, _P, _P, _P]),
     "quads_moe_route_backward": (_INT, [_P, _INT, _I64, _I32, _I64, _P, _P, _P, _I32, _INT, _P,
                                         _P]),
-    "quads_moe_sort": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I32, _I64, _P, _P]),
+    "quads_moe_sort_ws": (_SZ, [_I64, _I64, _INT, _INT]),
+    "quads_moe_sort": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I32, _I64, _INT, _P, _P, _SZ, _P]),
     "quads_moe_unsort": (_INT, [_P, _INT, _I64, _P, _P, _I64, _I32, _I64, _P, _INT, _P]),
-    "quads_moe_unsort_backward": (_INT, [_P, _INT, _P, _INT, _I64, _P, _P, _I64, _I32, _I64, _P,
-                                         _P, _P]),
+    "quads_moe_unsort_backward": (_INT, [_P, _INT, _P, _INT, _I64, _P, _P, _I64, _I32, _I64, _INT,
+                                         _P, _P, _P, _SZ, _P]),
 }
 
 
@@ -954,14 +955,15 @@ def _slots(pos, topk, topk_w, dev):
     return pos, _want("topk_w", topk_w, torch.float32, (n // topk, topk), dev), n // topk
 
 
-def _packed(rows, n, h, dtype, dev):
-    """The packed rows of a call that writes the rows which pos names: every one (rows None: pos
-    is a permutation of them), or some, and the others are 0."""
+def _rest(rows, n, h, code, dev):
+    """(rows, zero_rest, workspace, its bytes) of a call that writes the packed rows which pos
+    names: every one (rows None: pos is a permutation of n rows), or some, and zeroes the others."""
     if rows is None:
-        return n, torch.empty(n, h, dtype=dtype, device=dev)
+        return n, 0, None, 0
     if rows < 0:
         raise ValueError("rows must not be negative")
-    return rows, torch.zeros(rows, h, dtype=dtype, device=dev)
+    nws = lib().quads_moe_sort_ws(rows, h, code, 1)
+    return rows, 1, _scratch(nws, dev), nws
 
 
 def quads_moe_sort(x, pos, topk, rows=None):
@@ -974,8 +976,10 @@ def quads_moe_sort(x, pos, topk, rows=None):
     pos, _, n = _slots(pos, topk, None, dev)
     if n != t:
         raise ValueError("pos must have topk entries per row of x")
-    rows, out = _packed(rows, t * topk, h, x.dtype, dev)
-    _call("quads_moe_sort", dev, _at(x), code, t, h, ldx, _at(pos), topk, rows, _at(out))
+    rows, rest, ws, nws = _rest(rows, t * topk, h, code, dev)
+    out = torch.empty(rows, h, dtype=x.dtype, device=dev)
+    _call("quads_moe_sort", dev, _at(x), code, t, h, ldx, _at(pos), topk, rows, rest, _at(out),
+          _at(ws), nws)
     return out
 
 
@@ -1005,10 +1009,11 @@ def quads_moe_unsort_backward(g, y, pos, topk, topk_w, rows=None, want_dy=True, 
     g, gt = _dense("g", g, (t, h), dev)
     if n != (t * topk if rows is None else rows):
         raise ValueError("y must have T * topk rows, or as many as rows says")
-    dy = _packed(rows, n, h, y.dtype, dev)[1] if want_dy else None
+    rest, ws, nws = _rest(rows, n, h, yt, dev)[1:] if want_dy else (0, None, 0)
+    dy = torch.empty(n, h, dtype=y.dtype, device=dev) if want_dy else None
     dw = None
     if want_dw and topk_w is not None:
         dw = torch.empty(t, topk, dtype=torch.float32, device=dev)
     _call("quads_moe_unsort_backward", dev, _at(g), gt, _at(y), yt, n, _at(pos), _at(topk_w), t,
-          topk, h, _at(dy), _at(dw))
+          topk, h, rest, _at(dy), _at(dw), _at(ws), nws)
     return dy, dw

@@ -25,7 +25,55 @@ struct Args {
     float* dw;
     int64_t T, H, ld, rows;
     int topk, per;                           // per: slots of a work-group of the gradient
+    const int32_t* slot_of;                  // [rows], where rows without a slot become 0
+    int64_t slots;                           // of the whole call
+    unsigned groups;                         // work-groups with tokens; behind them zero_rest's
 };
+
+// Rows without a slot become 0 in one of two ways.  Up to kFillBytes every row is zeroed
+// first; beyond, that would write most of them twice, and those without a slot are found
+// with an inverse of pos that nobody clears: slot_of[pos[i]] = i for every slot i, and
+// whatever the memory held elsewhere; row p has a slot if its entry is some i whose pos is
+// p.  Device time of the sort, all rows first / found, rows for 5/4 of the slots: 64 x 2048,
+// top 8, bf16 5.2 us / 8.5, 1000 x 1000, top 4, bf16 6.7 / 8.7, 4096 x 2048, top 8, bf16
+// 45.2 / 40.2, 16384 x 4096, top 8, bf16 385 / 318.
+constexpr int64_t kFillBytes = (int64_t)64 << 20;
+__global__ __launch_bounds__(256) void k_fill(uint16_t* __restrict__ out, int64_t n) {
+    const int64_t whole = n / kPer, first = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    for (int64_t i = first; i < whole; i += (int64_t)gridDim.x * 256)
+        reinterpret_cast<words4*>(out)[i] = words4{};
+    if (first < n - whole * kPer) out[whole * kPer + first] = 0;
+}
+__global__ __launch_bounds__(256) void k_mark(const int32_t* __restrict__ pos, int64_t n,
+                                              int64_t rows, int32_t* __restrict__ slot_of) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t p = pos[i];
+        if (p >= 0 && p < rows) slot_of[p] = (int32_t)i;
+    }
+}
+// The work-groups behind the tokens' zero the rows without a slot, each wave 16 rows at a
+// time.
+constexpr int kRestRows = 16;
+constexpr int64_t kRestGroups = 4096;
+template <int kT>
+__device__ __forceinline__ void zero_rest(const Args& a, const int32_t* __restrict__ pos) {
+    if (blockIdx.y) return;
+    const int lane = threadIdx.x & 63, waves = (int)(blockDim.x >> 6);
+    const int64_t first = (int64_t)(blockIdx.x - a.groups) * waves + (threadIdx.x >> 6);
+    const int64_t step = (int64_t)(gridDim.x - a.groups) * waves * kRestRows;
+    for (int64_t r0 = first * kRestRows; r0 < a.rows; r0 += step) {
+        const int64_t r = r0 + lane;
+        bool empty = false;
+        if (lane < kRestRows && r < a.rows) {
+            const int64_t i = a.slot_of[r];
+            empty = i < 0 || i >= a.slots || pos[i] != r;
+        }
+        for (uint64_t left = __ballot(empty); left; left &= left - 1) {
+            void* row = row_at<kT>(a.out, (r0 + __builtin_ctzll(left)) * a.H);
+            for (int64_t c = lane * kPer; c < a.H; c += 64 * kPer) store<kT>(row, c, a.H - c, Raw<kT>{});
+        }
+    }
+}
 
 // Which token and which eight channels a thread has.  kLanes threads to a token (8, 16,
 // 32), 256 / kLanes tokens to a work-group; 0: work-group (x, y) has channels
@@ -61,6 +109,7 @@ template <int kOnce, int kLanes, int kCut>
 __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_sort(Args a,
                                                               const int32_t* __restrict__ pos) {
     constexpr int kT = 1;
+    if (blockIdx.x >= a.groups) return zero_rest<kT>(a, pos);
     const Place<kLanes, kCut> at(a);
     if (at.p.n <= 0) return;
     const Raw<kT> r = load<kT, kCut != kTiny>(row_at<kT>(a.a, at.t * a.ld), at.p.at, at.p.n);
@@ -107,6 +156,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort_grad(
     Args a, const int32_t* __restrict__ pos, const float* __restrict__ w) {
     constexpr int kMaxWaves = kLanes ? 1 : 16;
     __shared__ float s_dot[kLanes ? 1 : kMaxTopk][kMaxWaves];
+    if (blockIdx.x >= a.groups) return zero_rest<kY>(a, pos);
     const Place<kLanes, kCut> at(a);
     const int from = kLanes ? 0 : blockIdx.y * a.per;
     const int end = kLanes || from + a.per > a.topk ? a.topk : from + a.per;
@@ -213,9 +263,33 @@ void with_shape(const Shape& p, int64_t H, F f) {
     else f(Int<kOnce>{}, Int<0>{}, Int<kOdd>{});
 }
 
+// Work-groups for the rows without a slot, behind those with tokens.
+inline void add_rest(Args& a, Shape& p) {
+    a.groups = p.grid.x;
+    if (!a.slot_of) return;
+    const int64_t each = p.threads / 64 * kRestRows, n = (a.rows + each - 1) / each;
+    p.grid.x += (unsigned)(n < kRestGroups ? n : kRestGroups);
+}
+// What comes before them: the whole output zeroed, or the inverse written (`bytes`: of the
+// output's rows).
+inline int before_rest(void* out, int64_t bytes, const int32_t* pos, int64_t slots, int64_t rows,
+                       void* ws, hipStream_t s) {
+    const bool fill = bytes <= kFillBytes;
+    const int64_t n = fill ? bytes / 2 : slots, each = fill ? 256 * kPer : 256;
+    const int64_t groups = (n + each - 1) / each;
+    const dim3 grid((unsigned)(groups < 4096 ? groups : 4096));
+    if (fill)
+        hipLaunchKernelGGL(k_fill, grid, dim3(256), 0, s, (uint16_t*)out, n);
+    else if (slots)
+        hipLaunchKernelGGL(k_mark, grid, dim3(256), 0, s, pos, slots, rows, (int32_t*)ws);
+    QUADS_CHECK_LAUNCH();
+    return QUADS_OK;
+}
+
 // `bytes`: of the packed rows that the slots name.
-inline void launch_sort(const Args& a, const int32_t* pos, int64_t bytes, hipStream_t s) {
-    const Shape p = shape_of(a.T, a.H, true);
+inline void launch_sort(Args& a, const int32_t* pos, int64_t bytes, hipStream_t s) {
+    Shape p = shape_of(a.T, a.H, true);
+    add_rest(a, p);
     auto go = [&](auto once, auto lanes, auto cut) {
         hipLaunchKernelGGL((k_sort<once(), lanes(), cut()>), p.grid, dim3(p.threads), 0, s, a, pos);
     };
@@ -242,9 +316,10 @@ inline int slots_of(int64_t T, int topk) {
     return per < 1 ? 1 : (per < topk ? (int)per : topk);
 }
 template <int kG, int kY>
-void launch_grad(const Args& a, const int32_t* pos, const float* w, int64_t bytes, hipStream_t s) {
+void launch_grad(Args& a, const int32_t* pos, const float* w, int64_t bytes, hipStream_t s) {
     Shape p = shape_of(a.T, a.H, false);
     if (!p.lanes) p.grid.y = (a.topk + a.per - 1) / a.per;
+    add_rest(a, p);
     auto go = [&](auto once, auto lanes, auto cut) {
         hipLaunchKernelGGL((k_unsort_grad<kG, kY, once(), lanes(), cut()>), p.grid, dim3(p.threads),
                            0, s, a, pos, w);
@@ -270,21 +345,39 @@ inline int check(int64_t T, int64_t H, int64_t ld, int32_t topk, int64_t rows) {
 
 using namespace quads;
 
+extern "C" size_t quads_moe_sort_ws(int64_t rows, int64_t H, int dtype, int zero_rest) {
+    if (!zero_rest || rows <= 0 || rows >= ((int64_t)1 << 31) || H < 1 || H >= block::kMaxH) return 0;
+    const int64_t bytes = rows * H * (dtype == QUADS_OUT_BF16 ? 2 : 4);
+    return bytes <= sorting::kFillBytes ? 0 : align_up((size_t)rows * 4, 256);
+}
+
 extern "C" int quads_moe_sort(const void* x, int dtype, int64_t T, int64_t H, int64_t ldx,
-                              const int32_t* pos, int32_t topk, int64_t rows, void* out,
-                              void* stream) {
+                              const int32_t* pos, int32_t topk, int64_t rows, int zero_rest,
+                              void* out, void* ws, size_t ws_bytes, void* stream) {
     using namespace sorting;
     if (int e = check(T, H, ldx, topk, rows)) return e;
-    if (!ok_type(dtype)) return QUADS_EINVAL;
-    if (T == 0 || rows == 0) return QUADS_OK;
-    if (!ok_ptr(x) || !ok_ptr4(pos) || !ok_ptr(out) || x == out) return QUADS_EINVAL;
+    if (!ok_type(dtype) || (zero_rest != 0 && zero_rest != 1)) return QUADS_EINVAL;
+    if (rows == 0 || (T == 0 && !zero_rest)) return QUADS_OK;
+    if (!ok_ptr(out) || (T > 0 && (!ok_ptr(x) || !ok_ptr4(pos) || x == out))) return QUADS_EINVAL;
+    const size_t need = quads_moe_sort_ws(rows, H, dtype, zero_rest);
+    if (need && (ws_bytes < need || !ok_ptr(ws))) return QUADS_EWORKSPACE;
     hipStream_t s = (hipStream_t)stream;
     const int size = dtype == QUADS_OUT_BF16 ? 2 : 4;
-    const int64_t bytes = T * topk * H * size;
-    for (int64_t t = 0; t < T; t += kLaunchTokens) {
-        const Args a = {(const char*)x + t * ldx * size, nullptr, out, nullptr,
-                        T - t < kLaunchTokens ? T - t : kLaunchTokens, H * size / 2,
-                        ldx * size / 2, rows, topk, topk};
+    const int64_t slots = T * topk, bytes = slots * H * size;
+    if (zero_rest)
+        if (int e = before_rest(out, rows * H * size, pos, slots, rows, ws, s)) return e;
+    if (T == 0 && !need) return QUADS_OK;
+    for (int64_t t = 0; t < T || t == 0; t += kLaunchTokens) {
+        Args a = {};
+        a.a = (const char*)x + t * ldx * size;
+        a.out = out;
+        a.T = T - t < kLaunchTokens ? T - t : kLaunchTokens;
+        a.H = H * size / 2;
+        a.ld = ldx * size / 2;
+        a.rows = rows;
+        a.topk = topk;
+        a.slot_of = need && t == 0 ? (const int32_t*)ws : nullptr;
+        a.slots = slots;
         launch_sort(a, pos + t * topk, bytes, s);
         QUADS_CHECK_LAUNCH();
     }
@@ -304,8 +397,13 @@ extern "C" int quads_moe_unsort(const void* y, int y_dtype, int64_t rows, const 
     const bool yb = y_dtype == QUADS_OUT_BF16, ob = out_dtype == QUADS_OUT_BF16;
     const int64_t bytes = T * topk * H * (yb ? 2 : 4);
     for (int64_t t = 0; t < T; t += kLaunchTokens) {
-        const Args a = {y, nullptr, (char*)out + t * H * (ob ? 2 : 4), nullptr,
-                        T - t < kLaunchTokens ? T - t : kLaunchTokens, H, H, rows, topk, topk};
+        Args a = {};
+        a.a = y;
+        a.out = (char*)out + t * H * (ob ? 2 : 4);
+        a.T = T - t < kLaunchTokens ? T - t : kLaunchTokens;
+        a.H = H;
+        a.rows = rows;
+        a.topk = topk;
         const int32_t* p = pos + t * topk;
         const float* w = topk_w ? topk_w + t * topk : nullptr;
         if (yb && ob) launch_unsort<1, 1>(a, p, w, bytes, s);
@@ -319,23 +417,42 @@ extern "C" int quads_moe_unsort(const void* y, int y_dtype, int64_t rows, const 
 
 extern "C" int quads_moe_unsort_backward(const void* g, int g_dtype, const void* y, int y_dtype,
                                          int64_t rows, const int32_t* pos, const float* topk_w,
-                                         int64_t T, int32_t topk, int64_t H, void* dy, float* dw,
+                                         int64_t T, int32_t topk, int64_t H, int zero_rest,
+                                         void* dy, float* dw, void* ws, size_t ws_bytes,
                                          void* stream) {
     using namespace sorting;
     if (int e = check(T, H, H, topk, rows)) return e;
-    if (!ok_type(g_dtype) || !ok_type(y_dtype)) return QUADS_EINVAL;
-    if (dw && !topk_w) return QUADS_EINVAL;
-    if (T == 0 || (!dy && !dw)) return QUADS_OK;
-    if (!ok_ptr(g) || (rows > 0 && dw && !ok_ptr(y)) || !ok_ptr4(pos) || !ok_opt4(topk_w) ||
-        !ok_opt_ptr(dy) || !ok_opt4(dw) || dy == g)
+    if (!ok_type(g_dtype) || !ok_type(y_dtype) || (zero_rest != 0 && zero_rest != 1))
         return QUADS_EINVAL;
+    if (dw && !topk_w) return QUADS_EINVAL;
+    const bool rest = zero_rest && dy && rows > 0;
+    if ((!dy && !dw) || (T == 0 && !rest)) return QUADS_OK;
+    if (!ok_opt_ptr(dy) || !ok_opt4(dw) ||
+        (T > 0 && (!ok_ptr(g) || (rows > 0 && dw && !ok_ptr(y)) || !ok_ptr4(pos) ||
+                   !ok_opt4(topk_w) || dy == g)))
+        return QUADS_EINVAL;
+    if (rest && dy == y) return QUADS_EINVAL;
+    const size_t need = quads_moe_sort_ws(rows, H, y_dtype, rest);
+    if (need && (ws_bytes < need || !ok_ptr(ws))) return QUADS_EWORKSPACE;
     hipStream_t s = (hipStream_t)stream;
     const bool gb = g_dtype == QUADS_OUT_BF16, yb = y_dtype == QUADS_OUT_BF16;
-    const int64_t bytes = T * topk * H * (yb ? 2 : 4);
-    for (int64_t t = 0; t < T; t += kLaunchTokens) {
-        const Args a = {(const char*)g + t * H * (gb ? 2 : 4), y, dy, dw ? dw + t * topk : nullptr,
-                        T - t < kLaunchTokens ? T - t : kLaunchTokens, H, H, rows, topk,
-                        slots_of(T, topk)};
+    const int64_t slots = T * topk, bytes = slots * H * (yb ? 2 : 4);
+    if (rest)
+        if (int e = before_rest(dy, rows * H * (yb ? 2 : 4), pos, slots, rows, ws, s)) return e;
+    if (T == 0 && !need) return QUADS_OK;
+    for (int64_t t = 0; t < T || t == 0; t += kLaunchTokens) {
+        Args a = {};
+        a.a = (const char*)g + t * H * (gb ? 2 : 4);
+        a.y = y;
+        a.out = dy;
+        a.dw = dw ? dw + t * topk : nullptr;
+        a.T = T - t < kLaunchTokens ? T - t : kLaunchTokens;
+        a.H = H;
+        a.rows = rows;
+        a.topk = topk;
+        a.per = slots_of(T, topk);
+        a.slot_of = need && t == 0 ? (const int32_t*)ws : nullptr;
+        a.slots = slots;
         const int32_t* p = pos + t * topk;
         const float* w = topk_w ? topk_w + t * topk : nullptr;
         if (gb && yb) launch_grad<1, 1>(a, p, w, bytes, s);

@@ -26,7 +26,8 @@ def test_library_exports_every_declared_symbol():
     names = set(re.findall(r"\b(quads_[a-z0-9_]+)\s*\(", src))
     assert names == {"quads_rmsnorm", "quads_rmsnorm_amax_groups", "quads_rmsnorm_backward",
                      "quads_rmsnorm_backward_ws", "quads_moe_route", "quads_moe_route_backward",
-                     "quads_moe_sort", "quads_moe_unsort", "quads_moe_unsort_backward"}
+                     "quads_moe_sort", "quads_moe_sort_ws", "quads_moe_unsort",
+                     "quads_moe_unsort_backward"}
     lib = Q.lib()
     assert all(hasattr(lib, n) for n in names)
     assert int(re.search(r"#define QUADS_OUT_MX_FP8 (\d+)", src).group(1)) == Q.OUT_MX_FP8
@@ -102,15 +103,21 @@ def test_route_validation():
 def test_sort_validation():
     lib = Q.lib()
 
-    def sort(x=FAKE, dt=1, t=4, h=8, ld=8, pos=FAKE, k=2, rows=8, out=MORE):
-        return lib.quads_moe_sort(x, dt, t, h, ld, pos, k, rows, out, None)
+    big = 1 << 25                                                # rows of 8 bf16: 512 MB
+    ws = lib.quads_moe_sort_ws(big, 8, 1, 1)
+    assert ws >= 4 * big and lib.quads_moe_sort_ws(big, 8, 1, 0) == 0
+    assert lib.quads_moe_sort_ws(8, 8, 1, 1) == 0 and lib.quads_moe_sort_ws(0, 8, 1, 1) == 0
+
+    def sort(x=FAKE, dt=1, t=4, h=8, ld=8, pos=FAKE, k=2, rows=8, out=MORE, zr=0, wsp=None, wsz=0):
+        return lib.quads_moe_sort(x, dt, t, h, ld, pos, k, rows, zr, out, wsp, wsz, None)
 
     def unsort(y=FAKE, yt=1, rows=8, pos=FAKE, w=FAKE, t=4, k=2, h=8, out=MORE, ot=0):
         return lib.quads_moe_unsort(y, yt, rows, pos, w, t, k, h, out, ot, None)
 
     def back(g=FAKE, gt=1, y=MORE, yt=1, rows=8, pos=FAKE, w=FAKE, t=4, k=2, h=8, dy=MORE,
-             dw=FAKE):
-        return lib.quads_moe_unsort_backward(g, gt, y, yt, rows, pos, w, t, k, h, dy, dw, None)
+             dw=FAKE, zr=0, wsp=None, wsz=0):
+        return lib.quads_moe_unsort_backward(g, gt, y, yt, rows, pos, w, t, k, h, zr, dy, dw, wsp,
+                                             wsz, None)
     for call in (sort, unsort, back):
         assert call(t=-1) == -2 and call(t=1 << 24) == -2
         assert call(k=0) == -2 and call(k=65) == -2 and call(rows=-1) == -2
@@ -126,6 +133,15 @@ def test_sort_validation():
     assert back(w=None) == -1                                    # dw of no weights
     assert back(dw=MIS2) == -1 and back(dy=MIS) == -1
     assert back(dy=None, dw=None) == 0 and sort(rows=0) == 0
+    for call in (sort, back):
+        assert call(zr=2) == -1
+        on = dict(zr=1, rows=big)
+        if call is back:
+            on["y"] = ctypes.c_void_p(0x30000)
+        assert call(**on) == -3 and call(**on, wsp=FAKE, wsz=ws - 1) == -3
+        assert call(**on, wsp=MIS, wsz=ws) == -3 and call(**on, t=0) == -3
+    assert back(zr=1) == -1                                      # zeroing y's rows under itself
+    assert back(zr=1, dy=None, dw=None) == 0
 
 
 def test_binding_refuses_host_tensors():

@@ -569,17 +569,80 @@ def test_sort_leaves_other_rows_and_nan_weights(Q):
     w = torch.tensor([[1.0, 2.0], [float("nan"), 3.0], [float("inf"), 4.0]], device=DEV)
     dw = torch.empty_like(w)
     o = torch.empty_like(x)
-    assert lib.quads_moe_sort(x.data_ptr(), 0, t, h, h, pos.data_ptr(), k, n, out.data_ptr(), None) == 0
+    assert lib.quads_moe_sort(x.data_ptr(), 0, t, h, h, pos.data_ptr(), k, n, 0, out.data_ptr(), None,
+                              0, None) == 0
     assert lib.quads_moe_unsort(y.data_ptr(), 0, n, pos.data_ptr(), w.data_ptr(), t, k, h, o.data_ptr(), 0,
                                 None) == 0
     assert lib.quads_moe_unsort_backward(x.data_ptr(), 0, y.data_ptr(), 0, n, pos.data_ptr(),
-                                         w.data_ptr(), t, k, h, dy.data_ptr(), dw.data_ptr(), None) == 0
+                                         w.data_ptr(), t, k, h, 0, dy.data_ptr(), dw.data_ptr(), None, 0,
+                                         None) == 0
     torch.cuda.synchronize()
     assert np.array_equal(f64(out), OB.sort(xr, posn, k, n, 9.0))
     want, size = OB.unsort(yr, posn, k, np.array([[1, 2], [0, 3], [0, 4.0]]))
     close(o, want, 2 * U * size + TINY)
     assert f64(dy)[[1, 2, 4, 6]].tolist() == [[9.0] * h] * 4
     assert f64(dw)[1, 0] == 0 and f64(dw)[2, 0] == 0 and np.isfinite(f64(dw)).all()
+
+
+@pytest.mark.parametrize("before", ["slots", "negative", "rows", "ones"])
+@pytest.mark.parametrize("h,room", [(1, 16), (12, 15), (250, 15), (2049, 15), (7, 300000), (100, 30000),
+                                    (250, 15000), (1001, 3000), (9000, 300)])
+def test_rows_without_a_slot_become_zero(Q, h, room, before):
+    """Whatever the workspace held: slots of the call (as an earlier call leaves them), numbers that
+    are none, row numbers.  `room` rows for each of 16 experts: outputs of 1 kB to 170 MB."""
+    lib, t, k = Q.lib(), 70, 3
+    posn, n = placement(t, k, 16, 1, capacity=room, left_out=0.2)
+    pos = torch.from_numpy(posn).to(DEV)
+    at = pos.long()
+    have = (at >= 0) & (at < n)
+    full = torch.zeros(n, dtype=torch.bool, device=DEV)
+    full[at[have]] = True
+    for dtype in ("bf16", "f32"):
+        code = 1 if dtype == "bf16" else 0
+        x, _ = rows(t, h, dtype, 0)
+        w = torch.rand((t, k), device=DEV)
+        y = torch.randn((n, h), device=DEV).to(TYPES[dtype])
+        nws = lib.quads_moe_sort_ws(n, h, code, 1)
+        size = n * h * y.element_size()
+        assert nws == 0 if size <= 64 << 20 else nws >= 4 * n
+        held = {"slots": torch.arange(nws // 4) % (t * k), "negative": torch.full((nws // 4,), -5),
+                "rows": torch.arange(nws // 4), "ones": torch.full((nws // 4,), 2 ** 31 - 1)}[before]
+        for call in ("sort", "gradient"):
+            ws = held.int().to(DEV)
+            out = torch.full((n, h), 9.0, dtype=TYPES[dtype], device=DEV)
+            torch.cuda.synchronize()
+            if call == "sort":
+                assert lib.quads_moe_sort(x.data_ptr(), code, t, h, h, pos.data_ptr(), k, n, 1,
+                                          out.data_ptr(), ws.data_ptr() if nws else None, nws, None) == 0
+                want = x.repeat_interleave(k, 0)
+            else:
+                dw = torch.empty_like(w)
+                assert lib.quads_moe_unsort_backward(x.data_ptr(), code, y.data_ptr(), code, n,
+                                                     pos.data_ptr(), w.data_ptr(), t, k, h, 1, out.data_ptr(),
+                                                     dw.data_ptr(), ws.data_ptr() if nws else None, nws,
+                                                     None) == 0
+                want = (x.float()[:, None] * w[..., None]).reshape(t * k, h).to(x.dtype)
+            torch.cuda.synchronize()
+            assert not out[~full].any()
+            assert torch.equal(out[at[have]], want[have])
+
+
+def test_more_rows_than_slots(Q):
+    """Most rows without a slot; no tokens at all."""
+    x, xr = rows(5, 300, "bf16", 0)
+    pos = torch.tensor([199999, 3, 70001, 0, 12345], dtype=torch.int32, device=DEV)
+    xs = Q.quads_moe_sort(x, pos, 1, rows=200000)
+    got = torch.nonzero(xs.float().abs().sum(1))[:, 0].tolist()
+    assert got == [0, 3, 12345, 70001, 199999]
+    assert torch.equal(xs[pos.long()], x)
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    for h in (300, 30000):                                       # 0.8 and 84 MB
+        y = torch.ones((0, h), device=DEV)
+        torch.full((700, h), 5.0, device=DEV)                    # the next allocation's memory
+        assert not Q.quads_moe_sort(y, none, 2, rows=700).any()
+        dy, dw = Q.quads_moe_unsort_backward(y, torch.ones((700, h), device=DEV), none, 2,
+                                             torch.ones((0, 2), device=DEV), rows=700)
+        assert dy.shape == (700, h) and not dy.any() and dw.shape == (0, 2)
 
 
 def test_unsort_backward_over_y(Q):
@@ -592,7 +655,8 @@ def test_unsort_backward_over_y(Q):
     dy, dw = Q.quads_moe_unsort_backward(g, y, pos, k, w)
     dw2 = torch.empty_like(dw)
     assert lib.quads_moe_unsort_backward(g.data_ptr(), 1, y.data_ptr(), 1, n, pos.data_ptr(),
-                                         w.data_ptr(), t, k, h, y.data_ptr(), dw2.data_ptr(), None) == 0
+                                         w.data_ptr(), t, k, h, 0, y.data_ptr(), dw2.data_ptr(), None, 0,
+                                         None) == 0
     torch.cuda.synchronize()
     assert torch.equal(y, dy) and torch.equal(dw, dw2)
 
