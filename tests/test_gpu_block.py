@@ -199,7 +199,7 @@ def test_norm_not_finite(Q, h, bad):
         assert np.isnan(rest).all() if np.isnan(bad) else not rest.any()
 
 
-@pytest.mark.parametrize("h", [64, 2048, 16384, 40000])
+@pytest.mark.parametrize("h", [5, 61, 64, 130, 1001, 2048, 2049, 5001, 8191, 16384, 16385, 40000, 40001])
 def test_norm_in_place(Q, h):
     """sum over the residual, y over x (through the C ABI)."""
     lib, t = Q.lib(), 7
@@ -294,7 +294,7 @@ def test_norm_grad_of_no_rows(Q):
     assert Q.quads_rmsnorm(x)["y"].shape == (0, 40)
 
 
-@pytest.mark.parametrize("h", [64, 2048, 12000])
+@pytest.mark.parametrize("h", [5, 61, 64, 130, 1001, 2048, 2049, 5001, 8191, 12000, 12001, 20001])
 def test_norm_grad_in_place(Q, h):
     lib, t = Q.lib(), 70
     for at in ("g", "g_sum"):
@@ -312,6 +312,26 @@ def test_norm_grad_in_place(Q, h):
                                           ws.data_ptr(), nws, None) == 0
         torch.cuda.synchronize()
         assert torch.equal(dx, want[0]) and torch.equal(dw, want[2])
+
+
+def test_norm_grad_writes_both(Q):
+    """dx and dres of one type, and of two, dres over g_sum (through the C ABI)."""
+    lib, t = Q.lib(), 20
+    for h in (100, 2048, 20000):
+        for dt in ("bf16", "f32"):
+            x, _, w, _, _ = norm_inputs(t, h, "bf16", None, "f32", 3)
+            g, _ = rows(t, h, "f32", 4)
+            s, _ = rows(t, h, "bf16", 5)
+            want = Q.quads_rmsnorm_backward(g, x, w, EPS, s, TYPES[dt])
+            nws = lib.quads_rmsnorm_backward_ws(t, h, 0)
+            ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=DEV)
+            dx = torch.empty((t, h), dtype=TYPES[dt], device=DEV)
+            torch.cuda.synchronize()
+            assert lib.quads_rmsnorm_backward(g.data_ptr(), 0, x.data_ptr(), 1, t, h, h, w.data_ptr(), 0,
+                                              EPS, s.data_ptr(), dx.data_ptr(), 1 if dt == "bf16" else 0,
+                                              s.data_ptr(), None, ws.data_ptr(), nws, None) == 0
+            torch.cuda.synchronize()
+            assert torch.equal(dx, want[0]) and torch.equal(s, want[1])
 
 
 def test_norm_grad_not_finite(Q):

@@ -32,7 +32,8 @@ def randn(*shape, seed=0, by=1.0, dtype=torch.float32):
     return (torch.randn(shape, generator=g) * by).to(dtype).to(DEV)
 
 
-@pytest.mark.parametrize("t,h", [(1, 64), (5, 256), (64, 2048), (700, 512), (4100, 128), (3, 20000)])
+@pytest.mark.parametrize("t,h", [(1, 64), (5, 256), (64, 2048), (700, 512), (4100, 128), (3, 20000), (3, 40000),
+                                 (70000, 128), (2500, 2048)])
 def test_norm_feeds_the_quantizers(Q, t, h):
     """Partial maxima give the codes of the dynamic quantizers, bit for bit."""
     x, res = randn(t, h, seed=1, dtype=torch.bfloat16), randn(t, h, seed=2, dtype=torch.bfloat16)
