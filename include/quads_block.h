@@ -58,7 +58,7 @@ extern "C" {
  *              |y| as bf16 bits for quads_nvfp4_quantize_partials and
  *              quads_rac_quantize_partials; amax_groups >=
  *              quads_rmsnorm_amax_groups(T, H), the rest is written 0
- * 1 <= H < 2^26, T < 2^31.  The mean is formed in fp64; with QUADS_OUT_MX_FP8
+ * 1 <= H < 2^24, T < 2^31.  The mean is formed in fp64; with QUADS_OUT_MX_FP8
  * so is y (each code and scale is that of the exact y unless it lies within
  * about 2^-50 of a border).  fp32 and bf16 outputs come from two fp32 products
  * (3 * 2^-24 of the value; two bits more in rows whose root mean square is above
@@ -127,7 +127,7 @@ int quads_moe_route_backward(const void* logits, int dtype, int64_t T, int32_t E
 /*
  * Tokens in packed (expert) order: out[pos[t * topk + s]] = x[t] for every
  * token t and slot s.  pos is quads_moe_pack's, or any other placement.
- *   x          [T, H], `dtype`, row stride ldx; 1 <= H < 2^26, T < 2^24,
+ *   x          [T, H], `dtype`, row stride ldx; 1 <= H < 2^24, T < 2^24,
  *              1 <= topk <= 64, T * topk < 2^31
  *   pos        int32 [T * topk]: a value outside [0, rows) means that the slot
  *              is left out.  A row is named once at most (named more often, each

@@ -236,7 +236,7 @@ __device__ __forceinline__ void* row_at(void* base, int64_t element) {
 // ------------------------------------------------------------------ host --
 inline bool ok_type(int t) { return t == QUADS_OUT_F32 || t == QUADS_OUT_BF16; }
 inline bool ok_opt4(const void* p) { return p == nullptr || ok_ptr4(p); }
-constexpr int64_t kMaxH = (int64_t)1 << 26;
+constexpr int64_t kMaxH = (int64_t)1 << 24;
 constexpr int64_t kMaxStride = (int64_t)1 << 31;
 
 }  // namespace block

@@ -219,7 +219,7 @@ __global__ __launch_bounds__(kLongThreads) void k_rms_long(Args a) {
         for (int64_t c = (int64_t)threadIdx.x * kPer; c < a.H; c += kLongThreads * kPer) {
             const int64_t n = a.H - c;
             float h[kPer], w[kPer];
-            if (kR != kNone && sum) {        // x or the residual may be gone: the sum took its place
+            if (kR != kNone && sum) {        // it may have taken x's or the residual's place
                 const Raw<kR & 1> q = load<kR & 1>(sum, c, n);
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) h[i] = q.get(i);
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(kLongThreads) void k_rms_long(Args a) {
                 add<kX, kR>(xr, rr, h);
             }
             load_weight(a.weight, a.w_dtype, c, n, w);
-            finish<kFp8>(a, t, c, (int)larger((int64_t)0, n < kPer ? n : (int64_t)kPer), h, w, rstd, most);
+            finish<kFp8>(a, t, c, (int)(n < kPer ? n : kPer), h, w, rstd, most);
         }
     }
     if (!kFp8 && a.amax_part) leave_amax(a, most);
@@ -260,8 +260,8 @@ inline Shape shape_of(int64_t H) {
 // weight once; calls that move more than the caches hold are faster with the rows in
 // order, a work-group for each (16384 x 4096 bf16: 92.5 us against 103.5, 16384 x 2048
 // 48.6 / 52.8, 4096 x 2048 15.6 / 14.7, 131072 x 128 15.5 / 13.7; at most 2^21 of them,
-// a launch has fewer than 2^32 threads).  Partial maxima are
-// read by every work-group of the quantizer: with them never more than 2048.
+// a launch has fewer than 2^32 threads).  Partial maxima are read by every work-group of
+// the quantizer: with them never more than 2048.
 constexpr int64_t kMaxGroups = 2048, kManyBytes = (int64_t)192 << 20;
 inline int64_t groups_of(int64_t T, int64_t H, int64_t bytes) {
     const Shape s = shape_of(H);
@@ -336,7 +336,8 @@ extern "C" int quads_rmsnorm(const void* x, int x_dtype, int64_t T, int64_t H, i
     if (sum && !residual) return QUADS_EINVAL;
     if (amax_part && amax_groups < quads_rmsnorm_amax_groups(T, H)) return QUADS_EWORKSPACE;
     if (T == 0) return QUADS_OK;
-    if (!ok_ptr(x) || !ok_opt_ptr(residual) || !ok_opt_ptr(weight) || !ok_opt_ptr(sum) || !ok_ptr(y))
+    if (!ok_ptr(x) || !ok_opt_ptr(residual) || !ok_opt_ptr(weight) || !ok_opt_ptr(sum) ||
+        !ok_ptr(y))
         return QUADS_EINVAL;
     if (out_dtype == QUADS_OUT_MX_FP8 && !ok_ptr(scales)) return QUADS_EINVAL;
     // in place only over rows that lie as the output's do

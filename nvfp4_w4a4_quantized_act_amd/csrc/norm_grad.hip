@@ -20,6 +20,7 @@ struct GradArgs {
     double eps, inv_h;
     int w_dtype, dx_dtype;
 };
+
 // ---- rows of up to 16384 channels: one read of g, h and g_sum, one write ----------------
 //
 // A row stays in the registers of the threads that share it (kLanes, or 64 n of them)
@@ -215,8 +216,8 @@ __global__ __launch_bounds__(kThreads) void k_rms_grad_apply(GradArgs a) {
 }
 
 // dweight from the partial sums of `runs` work-groups or runs of rows: 16 channels a
-// work-group, the runs over its 64 sixteenths, joined in fp64 (64 channels a work-group
-// of 16 waves: 4096 x 2048 bf16 21.4 us in all).
+// work-group, the runs over its 64 groups of 16 threads, joined in fp64 (64 channels a work-group
+// of 16 waves: 4096 x 2048 bf16 21.4 us with the gradient, 20.9 so).
 __global__ __launch_bounds__(1024) void k_rms_join_weight(const float* part, int runs, int64_t H,
                                                           void* dweight, int bf16) {
     __shared__ double s_sum[kMaxWaves][16];
@@ -342,8 +343,8 @@ extern "C" int quads_rmsnorm_backward(const void* g, int g_dtype, const void* h,
     const size_t stat = grad_shape(T, H).v ? 0 : align_up((size_t)T * 8, 256);
     float* part = dweight ? (float*)((char*)ws + stat) : nullptr;
     GradArgs a = {g, h, weight, g_sum, dx, dres, (float2*)ws, part, T, H, ldh,
-                  (T + runs - 1) / runs, (int)runs, eps, 1.0 / (double)H, weight ? w_dtype : kNoWeight,
-                  dx_dtype};
+                  (T + runs - 1) / runs, (int)runs, eps, 1.0 / (double)H,
+                  weight ? w_dtype : kNoWeight, dx_dtype};
     const bool gb = g_dtype == QUADS_OUT_BF16, hb = h_dtype == QUADS_OUT_BF16;
     if (gb && hb) launch_grad<1, 1>(a, s);
     else if (gb) launch_grad<1, 0>(a, s);

@@ -46,7 +46,8 @@ __global__ __launch_bounds__(256) void k_fill(uint16_t* __restrict__ out, int64_
 }
 __global__ __launch_bounds__(256) void k_mark(const int32_t* __restrict__ pos, int64_t n,
                                               int64_t rows, int32_t* __restrict__ slot_of) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;
+         i += (int64_t)gridDim.x * 256) {
         const int64_t p = pos[i];
         if (p >= 0 && p < rows) slot_of[p] = (int32_t)i;
     }
@@ -70,7 +71,8 @@ __device__ __forceinline__ void zero_rest(const Args& a, const int32_t* __restri
         }
         for (uint64_t left = __ballot(empty); left; left &= left - 1) {
             void* row = row_at<kT>(a.out, (r0 + __builtin_ctzll(left)) * a.H);
-            for (int64_t c = lane * kPer; c < a.H; c += 64 * kPer) store<kT>(row, c, a.H - c, Raw<kT>{});
+            for (int64_t c = lane * kPer; c < a.H; c += 64 * kPer)
+                store<kT>(row, c, a.H - c, Raw<kT>{});
         }
     }
 }
@@ -85,8 +87,9 @@ struct Place {
     __device__ __forceinline__ explicit Place(const Args& a) {
         int c;
         if (kLanes) {
-            t = (int64_t)blockIdx.x * (256 / (kLanes ? kLanes : 1)) + threadIdx.x / (kLanes ? kLanes : 1);
-            c = threadIdx.x % (kLanes ? kLanes : 1);
+            constexpr int kL = kLanes ? kLanes : 1;
+            t = (int64_t)blockIdx.x * (256 / kL) + threadIdx.x / kL;
+            c = threadIdx.x % kL;
         } else {
             t = blockIdx.x;
             c = blockIdx.y * blockDim.x + threadIdx.x;
@@ -115,7 +118,9 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_sort(Args a,
     const Raw<kT> r = load<kT, kCut != kTiny>(row_at<kT>(a.a, at.t * a.ld), at.p.at, at.p.n);
     for (int s = 0; s < a.topk; ++s) {
         const int64_t p = slot_row(pos, at.t * a.topk + s, a.rows);
-        if (p >= 0) store<kT, kCut != kTiny, (kOnce & 2) && kCut == kEven>(row_at<kT>(a.out, p * a.H), at.p.at, at.p.n, r);
+        if (p >= 0)
+            store<kT, kCut != kTiny, (kOnce & 2) && kCut == kEven>(row_at<kT>(a.out, p * a.H),
+                                                                   at.p.at, at.p.n, r);
     }
 }
 
@@ -136,7 +141,8 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort(Args a,
             r[s] = Raw<kY>{};
             by[s] = 0.0f;
             if (p >= 0) {
-                r[s] = load<kY, kCut != kTiny, (kOnce & 1) != 0>(row_at<kY>(a.a, p * a.H), at.p.at, at.p.n);
+                r[s] = load<kY, kCut != kTiny, (kOnce & 1) != 0>(row_at<kY>(a.a, p * a.H),
+                                                                 at.p.at, at.p.n);
                 by[s] = w ? w[slot] : 1.0f;
             }
         }
@@ -154,7 +160,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort(Args a,
 template <int kG, int kY, int kOnce, int kLanes, int kCut>
 __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort_grad(
     Args a, const int32_t* __restrict__ pos, const float* __restrict__ w) {
-    constexpr int kMaxWaves = kLanes ? 1 : 16;
+    constexpr int kMaxWaves = kLanes ? 1 : 16, kL = kLanes ? kLanes : 64;
     __shared__ float s_dot[kLanes ? 1 : kMaxTopk][kMaxWaves];
     if (blockIdx.x >= a.groups) return zero_rest<kY>(a, pos);
     const Place<kLanes, kCut> at(a);
@@ -176,7 +182,8 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort_grad(
                                                                     : -1;
                 y[s] = Raw<kY>{};
                 if (a.dw && row[s] >= 0 && p.n > 0)
-                    y[s] = load<kY, kCut != kTiny, (kOnce & 1) != 0>(row_at<kY>(a.y, row[s] * a.H), p.at, p.n);
+                    y[s] = load<kY, kCut != kTiny, (kOnce & 1) != 0>(
+                        row_at<kY>(a.y, row[s] * a.H), p.at, p.n);
             }
 #pragma unroll
             for (int s = 0; s < kBatch; ++s) {
@@ -187,16 +194,17 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort_grad(
                     float d[kPer];
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) d[i] = by * g.get(i);
-                    store<kY, kCut != kTiny, (kOnce & 2) && kCut == kEven>(row_at<kY>(a.out, row[s] * a.H), p.at, p.n, pack<kY>(d));
+                    store<kY, kCut != kTiny, (kOnce & 2) && kCut == kEven>(
+                        row_at<kY>(a.out, row[s] * a.H), p.at, p.n, pack<kY>(d));
                 }
                 if (a.dw) {
                     float dot = 0.0f;
 #pragma unroll
                     for (int i = 0; i < kPer; ++i)
                         if (kCut != kOdd || i >= p.from) dot = fmaf(g.get(i), y[s].get(i), dot);
-                    dot = lanes_sum<kLanes ? kLanes : 64>(dot);
+                    dot = lanes_sum<kL>(row[s] >= 0 ? dot : 0.0f);   // g may not be finite
                     if (kLanes) {
-                        if (threadIdx.x % (kLanes ? kLanes : 1) == 0 && at.t < a.T) a.dw[slot] = dot;
+                        if (threadIdx.x % kL == 0 && at.t < a.T) a.dw[slot] = dot;
                     } else if ((threadIdx.x & 63) == 0) {
                         float& all = s_dot[kLanes ? 0 : s0 + s][kLanes ? 0 : threadIdx.x >> 6];
                         all = first ? dot : all + dot;
@@ -346,7 +354,8 @@ inline int check(int64_t T, int64_t H, int64_t ld, int32_t topk, int64_t rows) {
 using namespace quads;
 
 extern "C" size_t quads_moe_sort_ws(int64_t rows, int64_t H, int dtype, int zero_rest) {
-    if (!zero_rest || rows <= 0 || rows >= ((int64_t)1 << 31) || H < 1 || H >= block::kMaxH) return 0;
+    if (!zero_rest || rows <= 0 || rows >= ((int64_t)1 << 31) || H < 1 || H >= block::kMaxH)
+        return 0;
     const int64_t bytes = rows * H * (dtype == QUADS_OUT_BF16 ? 2 : 4);
     return bytes <= sorting::kFillBytes ? 0 : align_up((size_t)rows * 4, 256);
 }

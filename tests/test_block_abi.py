@@ -40,7 +40,7 @@ def test_norm_validation():
              total=FAKE, y=MORE, yt=1, sc=None, am=None, na=0):
         return f(x, xt, t, h, ldx, res, rt, ldr, w, wt, eps, total, y, yt, sc, am, na, None)
     assert call(t=-1) == -2 and call(t=1 << 31) == -2
-    assert call(h=0) == -2 and call(h=1 << 26, ldx=1 << 26) == -2
+    assert call(h=0) == -2 and call(h=1 << 24, ldx=1 << 24) == -2
     assert call(ldx=63) == -2 and call(ldr=63) == -2 and call(ldx=1 << 31) == -2
     assert call(xt=2) == -1 and call(rt=2) == -1 and call(wt=-1) == -1 and call(yt=3) == -1
     for eps in (0.0, -1.0, 9e-71, 2e70, INF, NAN):
@@ -123,6 +123,7 @@ def test_sort_validation():
         assert call(k=0) == -2 and call(k=65) == -2 and call(rows=-1) == -2
         assert call(rows=1 << 31) == -2 and call(pos=None) == -1 and call(pos=MIS2) == -1
         assert call(t=0) == 0
+    assert sort(h=1 << 24, ld=1 << 24) == -2 and unsort(h=1 << 24) == -2
     assert sort(h=0, ld=0) == -2 and unsort(h=0) == -2 and back(h=0) == -2 and sort(ld=7) == -2
     assert sort(dt=2) == -1 and unsort(yt=2) == -1 and unsort(ot=2) == -1
     assert back(gt=2) == -1 and back(yt=-1) == -1

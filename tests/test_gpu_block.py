@@ -602,6 +602,13 @@ def test_sort_leaves_other_rows_and_nan_weights(Q):
     close(o, want, 2 * U * size + TINY)
     assert f64(dy)[[1, 2, 4, 6]].tolist() == [[9.0] * h] * 4
     assert f64(dw)[1, 0] == 0 and f64(dw)[2, 0] == 0 and np.isfinite(f64(dw)).all()
+    for h in (20, 900):                                          # a gradient that is not finite
+        g = torch.full((t, h), float("inf"), device=DEV)
+        g[:, 3] = float("nan")
+        y = torch.ones((n, h), device=DEV)
+        dy, dw = Q.quads_moe_unsort_backward(g, y, pos, k, w, rows=n)
+        assert f64(dw)[1, 0] == 0 and f64(dw)[2, 0] == 0 and np.isnan(f64(dw)[0]).all()
+        assert not f64(dy)[[1, 2, 4, 6]].any()
 
 
 @pytest.mark.parametrize("before", ["slots", "negative", "rows", "ones"])
