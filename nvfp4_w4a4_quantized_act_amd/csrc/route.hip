@@ -40,68 +40,142 @@ __device__ __forceinline__ uint32_t order_of(float z) {
 __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
-// exp(z - m), 0 for a masked logit even where nothing else is left.
+// What exponents are taken from: the largest logit, 0 where every one is masked (whose
+// terms are then 0, as a masked logit's are).
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
+// exp(z - m): a weight's numerator, and a term of a sum over all experts, by the hardware's
+// 2^x, off by up to 1.5 * 2^-24 of z - m (16 operations and 3).
+__device__ __forceinline__ float numerator(float z, float m) { return expf(z - m); }
 __device__ __forceinline__ float term(float z, float m) {
-    return z == -INFINITY ? 0.0f : expf(z - m);
+    return __builtin_amdgcn_exp2f((z - m) * 1.44269504f);
 }
 // The logits kV * lane .. of a token; -inf behind the last.
 template <int kBf16, int kV>
 __device__ __forceinline__ void load_logits(const Args& a, int64_t t, int lane, float* z) {
     const void* row = row_at<kBf16>(a.z, t * a.ld);
+    const uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;
 #pragma unroll
     for (int j = 0; j < kV; j += kPer) {
         const int e = kV * lane + j;
-        Raw<kBf16> r = {};
+        Raw<kBf16> r;
+        for (int i = 0; i < (kBf16 ? 1 : 2); ++i) r.q[i] = words4{none, none, none, none};
         if (t < a.T && e < a.E) r = load<kBf16>(row, e, a.E - e);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) z[j + i] = e + i < a.E ? r.get(i) : -INFINITY;
+        for (int i = 0; i < kPer; ++i) z[j + i] = r.get(i);
+        if (e < a.E && a.E - e < kPer) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) z[j + i] = i < a.E - e ? z[j + i] : -INFINITY;
+        }
     }
 }
 
+// Both values, not their places: a choice between two registers of an array becomes a
+// search through it.
+__device__ __forceinline__ uint32_t pick(bool c, uint32_t a, uint32_t b) { return c ? a : b; }
+// A lane's eight numbers, the largest first (19 exchanges).
+__device__ __forceinline__ void sort8(uint32_t* k) {
+    constexpr int kPairs[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6},
+                                   {5, 7}, {1, 2}, {5, 6}, {0, 4}, {1, 5}, {2, 6}, {3, 7},
+                                   {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+    for (int i = 0; i < 19; ++i) {
+        const uint32_t x = k[kPairs[i][0]], y = k[kPairs[i][1]];
+        k[kPairs[i][0]] = larger(x, y);
+        k[kPairs[i][1]] = x < y ? x : y;
+    }
+}
+
+// Up to 512 experts (kV 8) the numbers carry their place: a bf16 logit's 16 bits above the
+// place's complement, an fp32 logit's upper bits above it.  They differ, larger ones and
+// among equal ones lower places come first, and a step is the lanes' maximum and a lane's
+// shift, about 16 operations where finding and removing the first equal number takes 50.
+// fp32 numbers that differ only in the bits below tell so by equal bits above: their wave
+// takes the steps that compare all bits (as every wave does beyond 512 experts).
 template <int kBf16, int kL, int kV>
 __global__ __launch_bounds__(threads_of(kV)) void k_route(Args a) {
     constexpr int kTokens = threads_of(kV) / kL;
-    __shared__ uint2 s_top[kTokens][kMaxTopk];               // (id, number), in order
+    constexpr bool kPlaced = kV == 8, kWithValue = kPlaced && kBf16;
+    constexpr uint32_t kPlace = kWithValue ? 0xFFFFu : kL * kV - 1;
+    __shared__ uint32_t s_top[kTokens][kMaxTopk];            // kPlace - place in the lower bits
+    __shared__ __align__(16) float s_z[kWithValue ? 1 : kTokens][kWithValue ? 4 : kL * kV];
     const int token = threadIdx.x / kL, lane = threadIdx.x % kL;
     const int64_t t = (int64_t)blockIdx.x * kTokens + token;
     float z[kV];
     uint32_t key[kV];
     load_logits<kBf16, kV>(a, t, lane, z);
+    // places behind the last expert are as masked ones, and stand behind those
+    uint32_t most = 0;
 #pragma unroll
-    for (int j = 0; j < kV; ++j) key[j] = kV * lane + j < a.E ? order_of(z[j]) : 0u;
-    float m = 0.0f, total = 0.0f;
-    for (int i = 0; i < a.topk; ++i) {
-        uint32_t mine = key[0];
+    for (int j = 0; j < kV; ++j) {
+        key[j] = order_of(z[j]);
+        most = larger(most, key[j]);
+    }
+    const float m = base_of(value_of(lanes_max<kL>(most)));
+    if (!kWithValue) {
 #pragma unroll
-        for (int j = 1; j < kV; ++j) mine = larger(mine, key[j]);
-        const uint32_t best = lanes_max<kL>(mine);
-        if (i == 0) {
-            m = value_of(best);
-            if (!a.renorm) {
+        for (int j = 0; j < kV; j += 4)
+            *reinterpret_cast<float4*>(&s_z[token][kV * lane + j]) =
+                make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+    }
+    float total = 0.0f;
+    if (!a.renorm) {
 #pragma unroll
-                for (int j = 0; j < kV; ++j) total += term(z[j], m);
-                total = lanes_sum<kL>(total);
-            }
+        for (int j = 0; j < kV; ++j) total += term(z[j], m);
+        total = lanes_sum<kL>(total);
+    }
+    bool whole = !kPlaced;                                   // compare all bits
+    if constexpr (kPlaced) {
+        const uint32_t place = kPlace - (uint32_t)(kV * lane);
+        uint32_t k[kV];
+#pragma unroll
+        for (int j = 0; j < kV; ++j) k[j] = (key[j] & ~kPlace) | (place - j);
+        sort8(k);
+        uint32_t before = 0;
+        for (int i = 0; i < a.topk; ++i) {
+            const uint32_t best = lanes_max<kL>(k[0]);
+            if (lane == 0) s_top[token][i] = best;
+            if (!kBf16) whole = whole || ((best ^ before) & ~kPlace) == 0;
+            before = best;
+            const bool have = k[0] == best;
+#pragma unroll
+            for (int j = 0; j + 1 < kV; ++j) k[j] = pick(have, k[j + 1], k[j]);
+            k[kV - 1] = pick(have, 0u, k[kV - 1]);
         }
-        const uint64_t at = __ballot(mine == best) >> ((threadIdx.x & 63) - lane);
-        const bool have = (int)__builtin_ctzll(at) == lane;  // the token's lowest such lane
-        int e = kV;
+        if (!kBf16) {                                        // the next one decides nothing?
+            const uint32_t next = lanes_max<kL>(k[0]);
+            whole = whole || ((next ^ before) & ~kPlace) == 0;
+        }
+    }
+    if (!kWithValue && __ballot(whole)) {
+        for (int i = 0; i < a.topk; ++i) {
+            uint32_t mine = key[0];
 #pragma unroll
-        for (int j = kV - 1; j >= 0; --j) e = key[j] == best ? j : e;
-        if (have) s_top[token][i] = make_uint2((uint32_t)(kV * lane + e), best);
+            for (int j = 1; j < kV; ++j) mine = larger(mine, key[j]);
+            const uint32_t best = lanes_max<kL>(mine);
+            const uint64_t at = __ballot(mine == best) >> ((threadIdx.x & 63) - lane);
+            const bool have = (int)__builtin_ctzll(at) == lane;  // the token's lowest such lane
+            int e = kV;
 #pragma unroll
-        for (int j = 0; j < kV; ++j) key[j] = have && j == e ? 0u : key[j];
+            for (int j = kV - 1; j >= 0; --j) e = key[j] == best ? j : e;
+            if (have) s_top[token][i] = kPlace - (uint32_t)(kV * lane + e);
+#pragma unroll
+            for (int j = 0; j < kV; ++j) key[j] = have && j == e ? 0u : key[j];
+        }
     }
     __syncthreads();
+    auto chosen = [&](int i) {                               // its numerator
+        const uint32_t c = s_top[token][i];
+        if (kWithValue) return numerator(value_of((int)c < 0 ? c & ~kPlace : c | kPlace), m);
+        return numerator(s_z[kWithValue ? 0 : token][kPlace - (c & kPlace)], m);
+    };
     if (a.renorm) {
-        for (int i = lane; i < a.topk; i += kL) total += term(value_of(s_top[token][i].y), m);
+        for (int i = lane; i < a.topk; i += kL) total += chosen(i);
         total = lanes_sum<kL>(total);
     }
     if (t >= a.T) return;
     for (int i = lane; i < a.topk; i += kL) {
-        const uint2 c = s_top[token][i];
-        a.ids[t * a.topk + i] = (int32_t)c.x;
-        a.w[t * a.topk + i] = total == 0.0f ? 0.0f : term(value_of(c.y), m) / total;
+        a.ids[t * a.topk + i] = (int32_t)(kPlace - (s_top[token][i] & kPlace));
+        a.w[t * a.topk + i] = total == 0.0f ? 0.0f : chosen(i) / total;
     }
 }
 
@@ -145,7 +219,7 @@ __global__ __launch_bounds__(threads_of(kV)) void k_route_grad(Args a) {
         float m = z[0], total = 0.0f;
 #pragma unroll
         for (int j = 1; j < kV; ++j) m = fmaxf(m, z[j]);
-        m = value_of(lanes_max<kL>(order_of(m)));
+        m = base_of(value_of(lanes_max<kL>(order_of(m))));
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             z[j] = term(z[j], m);

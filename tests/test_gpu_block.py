@@ -454,6 +454,22 @@ def test_route_row_stride_and_equal_logits(Q):
         assert ids.tolist() == [list(range(8))] * 3 and torch.equal(w, torch.full_like(w, 0.125))
 
 
+@pytest.mark.parametrize("e", [8, 64, 65, 128, 200, 256, 512, 700, 2000])
+def test_route_logits_one_step_apart(Q, e):
+    """Neighbouring fp32 numbers, of both signs, with equal ones among them."""
+    for seed, base in ((0, 1.0), (1, -2.5), (2, 1e-38), (3, -3e38)):
+        rng = np.random.default_rng(seed)
+        v = np.full((41, e), np.float32(base)).view(np.int32) + rng.integers(-40, 40, size=(41, e)).astype(np.int32)
+        z = torch.from_numpy(v.view(np.float32)).to(DEV)
+        z[5, : e // 2] = z[5, e // 2: 2 * (e // 2)]
+        z[6:9] = torch.randn(3, e, device=DEV)
+        for topk in (1, 5, min(e, 8)):
+            ids, w = Q.quads_moe_route(z, topk, True)
+            eids, ew = OB.route(f64(z), topk, True)
+            assert np.array_equal(ids.cpu().numpy(), eids)
+            close(w, ew, route_errors(f64(z), eids, topk, True)[1])
+
+
 @pytest.mark.parametrize("bad", [float("nan"), -float("nan"), float("inf")])
 def test_route_not_finite(Q, bad):
     for e in (16, 100, 1000):
