@@ -8,8 +8,9 @@
 // kL lanes (8 .. 64) share a token, kV neighbouring logits in the registers of each.  The
 // order is by one unsigned number per logit, larger for a larger one: a float's bits, all
 // turned over where it is negative, the sign alone where it is not.  topk times the lanes
-// take their largest number, and the lowest lane that has it removes its first such logit.
-// What bounds it is that chain of topk steps, about 50 operations each, not its bytes.
+// take their largest number, and the lane that has it removes it.  What bounds it is the
+// vector units, 330 operations for eight steps of bf16 logits, not its bytes (65536 x 128,
+// top 8, bf16 11.9 us, 1.8 TB/s; the gradient 13.3 us, 3.0 TB/s).
 #include "block.h"
 
 namespace quads {
@@ -88,7 +89,8 @@ __device__ __forceinline__ void sort8(uint32_t* k) {
 // Up to 512 experts (kV 8) the numbers carry their place: a bf16 logit's 16 bits above the
 // place's complement, an fp32 logit's upper bits above it.  They differ, larger ones and
 // among equal ones lower places come first, and a step is the lanes' maximum and a lane's
-// shift, about 16 operations where finding and removing the first equal number takes 50.
+// shift, about 16 operations where finding and removing the first equal number takes 50
+// (in all 65536 x 128 bf16 11.9 us / 20, 16384 x 256 fp32 10.2 / 12.6).
 // fp32 numbers that differ only in the bits below tell so by equal bits above: their wave
 // takes the steps that compare all bits (as every wave does beyond 512 experts).
 template <int kBf16, int kL, int kV>
