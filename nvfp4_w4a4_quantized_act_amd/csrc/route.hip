@@ -86,13 +86,30 @@ __device__ __forceinline__ void sort8(uint32_t* k) {
     }
 }
 
+// The place of the first of eight numbers that is `best`; that one becomes 0 if `have`, and
+// `most` the largest of them then.
+__device__ __forceinline__ int take(bool have, uint32_t* k, uint32_t best, uint32_t& most) {
+    int e = 8;
+#pragma unroll
+    for (int j = 7; j >= 0; --j) e = k[j] == best ? j : e;
+    most = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        k[j] = pick(have && j == e, 0u, k[j]);
+        most = larger(most, k[j]);
+    }
+    return e;
+}
+
 // Up to 512 experts (kV 8) the numbers carry their place: a bf16 logit's 16 bits above the
 // place's complement, an fp32 logit's upper bits above it.  They differ, larger ones and
 // among equal ones lower places come first, and a step is the lanes' maximum and a lane's
 // shift, about 16 operations where finding and removing the first equal number takes 50
 // (in all 65536 x 128 bf16 11.9 us / 20, 16384 x 256 fp32 10.2 / 12.6).
 // fp32 numbers that differ only in the bits below tell so by equal bits above: their wave
-// takes the steps that compare all bits (as every wave does beyond 512 experts).
+// takes the steps that compare all bits.  So does every wave beyond 512 experts, by the
+// largest of eights, of which a step changes one (looking through all 64 numbers of a lane
+// in each step 4096 x 4096 fp32, top 8, 51 us against 32, 64 x 4096 17 / 8).
 template <int kBf16, int kL, int kV>
 __global__ __launch_bounds__(threads_of(kV)) void k_route(Args a) {
     constexpr int kTokens = threads_of(kV) / kL;
@@ -148,20 +165,45 @@ __global__ __launch_bounds__(threads_of(kV)) void k_route(Args a) {
             whole = whole || ((next ^ before) & ~kPlace) == 0;
         }
     }
-    if (!kWithValue && __ballot(whole)) {
+    if constexpr (kPlaced && !kBf16) {
+        if (__ballot(whole)) {
+            for (int i = 0; i < a.topk; ++i) {
+                uint32_t mine = key[0];
+#pragma unroll
+                for (int j = 1; j < kV; ++j) mine = larger(mine, key[j]);
+                const uint32_t best = lanes_max<kL>(mine);
+                const uint64_t at = __ballot(mine == best) >> ((threadIdx.x & 63) - lane);
+                const bool have = (int)__builtin_ctzll(at) == lane;  // the token's lowest such lane
+                const int e = take(have, key, best, mine);
+                if (have) s_top[token][i] = kPlace - (uint32_t)(kV * lane + e);
+            }
+        }
+    }
+    if constexpr (!kPlaced) {                                // a wave is one token's
+        constexpr int kParts = kV / 8;
+        uint32_t part[kParts];                               // the largest of eight numbers
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+            part[q] = key[8 * q];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) part[q] = larger(part[q], key[8 * q + j]);
+        }
         for (int i = 0; i < a.topk; ++i) {
-            uint32_t mine = key[0];
+            uint32_t mine = part[0];
 #pragma unroll
-            for (int j = 1; j < kV; ++j) mine = larger(mine, key[j]);
+            for (int q = 1; q < kParts; ++q) mine = larger(mine, part[q]);
             const uint32_t best = lanes_max<kL>(mine);
-            const uint64_t at = __ballot(mine == best) >> ((threadIdx.x & 63) - lane);
-            const bool have = (int)__builtin_ctzll(at) == lane;  // the token's lowest such lane
-            int e = kV;
+            const int winner = __builtin_ctzll(__ballot(mine == best));
+            int in = 0;
 #pragma unroll
-            for (int j = kV - 1; j >= 0; --j) e = key[j] == best ? j : e;
-            if (have) s_top[token][i] = kPlace - (uint32_t)(kV * lane + e);
+            for (int q = kParts - 1; q >= 0; --q) in = part[q] == best ? q : in;
+            in = __builtin_amdgcn_readlane(in, winner);
 #pragma unroll
-            for (int j = 0; j < kV; ++j) key[j] = have && j == e ? 0u : key[j];
+            for (int q = 0; q < kParts; ++q) {
+                if (q != in) continue;
+                const int e = take(lane == winner, key + 8 * q, best, part[q]);
+                if (lane == winner) s_top[token][i] = kPlace - (uint32_t)(kV * lane + 8 * q + e);
+            }
         }
     }
     __syncthreads();
