@@ -148,16 +148,26 @@ def _code(dtype):
 
 
 class RMSNorm(torch.autograd.Function):
-    """(y, h) of h = x + residual, y = h / sqrt(mean h^2 + eps) * weight, over rows."""
+    """(y, h) of h = x + residual, y = h / sqrt(mean h^2 + eps) * weight, over the last dimension.
+
+    The leading dimensions are taken in here: an input's gradient must reach autograd as the one
+    tensor object that dx and dres are, so that the first leaf copies it.  Reshaped outside, it
+    would become two views of one memory, which both leaves keep, and add to twice.
+    """
 
     @staticmethod
     def forward(ctx, x, residual, weight, eps, out_dtype):
-        r = quads_rmsnorm(x, weight, eps, residual, _code(out_dtype))
-        h = r.get("sum")
+        n, shape = x.shape[-1], x.shape
+        rows = x.reshape(-1, n)
+        r = quads_rmsnorm(rows, weight, eps, None if residual is None else residual.reshape(-1, n),
+                          _code(out_dtype))
+        # not views: they may be changed in place as any operator's results
+        y, h = (v if v is None or v.shape == shape else torch.ops.aten._unsafe_view(v, shape)
+                for v in (r["y"], r.get("sum")))
         ctx.save_for_backward(x if h is None else h, weight)
         ctx.eps, ctx.x_dtype, ctx.added = eps, x.dtype, h is not None
         ctx.set_materialize_grads(False)
-        return r["y"], h
+        return y, h
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -167,8 +177,14 @@ class RMSNorm(torch.autograd.Function):
             if g_sum is None:
                 return None, None, None, None, None
             return g_sum.to(ctx.x_dtype), g_sum, None, None, None
-        dx, dres, dw = quads_rmsnorm_backward(g, h, weight, ctx.eps, g_sum, ctx.x_dtype,
-                                              ctx.needs_input_grad[2])
+        n = h.shape[-1]
+        dx, dres, dw = quads_rmsnorm_backward(g.reshape(-1, n), h.reshape(-1, n), weight, ctx.eps,
+                                              None if g_sum is None else g_sum.reshape(-1, n),
+                                              ctx.x_dtype, ctx.needs_input_grad[2])
+        one = dres is dx
+        dx = dx.view(h.shape)
+        if ctx.added:
+            dres = dx if one else dres.view(h.shape)
         return dx, dres if ctx.added else None, dw, None, None
 
 
@@ -184,10 +200,8 @@ def rms_norm(x, weight=None, eps=1e-6, residual=None, out_dtype=None):
         raise ValueError("residual must have the shape of x")
     if out_dtype is None:
         out_dtype = x.dtype if residual is None else residual.dtype
-    n = x.shape[-1]
-    y, h = RMSNorm.apply(x.reshape(-1, n), None if residual is None else residual.reshape(-1, n),
-                         weight, float(eps), out_dtype)
-    return y.reshape(x.shape) if residual is None else (y.reshape(x.shape), h.reshape(x.shape))
+    y, h = RMSNorm.apply(x, residual, weight, float(eps), out_dtype)
+    return y if residual is None else (y, h)
 
 
 class Route(torch.autograd.Function):
