@@ -209,7 +209,8 @@ inline Cut cut_of(int64_t H) { return H % kPer == 0 ? kEven : (H < kPer ? kTiny 
 // The eight channels of a thread in a row of len channels: elements at .. at + 7, of
 // which those from `from` on are its own.  The row's last, partial eight (kOdd) start
 // earlier and share channels with the eight before: what both compute is the same, so
-// both may store it, and sums leave out what is not the thread's own.  (Reading and
+// both may store it, where no other thread reads what was there any more (else store_own),
+// and sums leave out what is not the thread's own.  (Reading and
 // storing a partial eight element by element takes a row's work-group three latencies
 // more, 16384 x 1001 bf16 21.3 us against 15.9, 8192 x 5001 93 against 79.)
 struct Piece {
@@ -221,6 +222,16 @@ __device__ __forceinline__ Piece piece(int c, int len) {
     if (kCut == kTiny) return {c, 0, len - c};
     if (kCut == kEven || len - c >= kPer) return {c, 0, kPer};
     return {len - kPer, c - (len - kPer), kPer};
+}
+// The piece's own channels alone.
+template <int kBf16>
+__device__ __forceinline__ void store_own(void* row, const Piece& p, const Raw<kBf16>& r) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (i < p.from || i >= p.n) continue;
+        if (kBf16) ((uint16_t*)row)[p.at + i] = (uint16_t)(r.q[0][i >> 1] >> (16 * (i & 1)));
+        else ((uint32_t*)row)[p.at + i] = r.q[kBf16 ? 0 : i >> 2][i & 3];
+    }
 }
 
 // Element address of a row, whatever the type.

@@ -156,7 +156,9 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort(Args a,
 }
 
 // kLanes 0: a work-group per token and `per` slots, its threads over the row, again where it
-// is longer.
+// is longer.  dy may be y: a thread has loaded its channels of a slot's row when it stores
+// them, but another wave, or a later turn over the row, may have the last, partial eight,
+// and must then leave alone the channels that it shares with the eight before.
 template <int kG, int kY, int kOnce, int kLanes, int kCut>
 __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort_grad(
     Args a, const int32_t* __restrict__ pos, const float* __restrict__ w) {
@@ -194,8 +196,12 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort_grad(
                     float d[kPer];
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) d[i] = by * g.get(i);
-                    store<kY, kCut != kTiny, (kOnce & 2) && kCut == kEven>(
-                        row_at<kY>(a.out, row[s] * a.H), p.at, p.n, pack<kY>(d));
+                    void* out = row_at<kY>(a.out, row[s] * a.H);
+                    if (kCut == kOdd && p.from > 0 && a.out == a.y)
+                        store_own<kY>(out, p, pack<kY>(d));
+                    else
+                        store<kY, kCut != kTiny, (kOnce & 2) && kCut == kEven>(out, p.at, p.n,
+                                                                               pack<kY>(d));
                 }
                 if (a.dw) {
                     float dot = 0.0f;
