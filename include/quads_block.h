@@ -106,6 +106,9 @@ int quads_rmsnorm_backward(const void* g, int g_dtype, const void* h, int h_dtyp
  * order, only where fewer than topk others are left).  In a token with every
  * logit -inf every weight is 0; with +inf or NaN the weights are NaN (or 0)
  * and the ids distinct and in [0, E).
+ * Weights are formed in fp32: numerators exp(z - max z) by expf, the terms of the
+ * sum over all experts (renorm 0) by 2^x of a rounded product, each off by up to
+ * 2.5 * 2^-24 |z - max z| of itself.
  */
 int quads_moe_route(const void* logits, int dtype, int64_t T, int32_t E, int64_t ld, int32_t topk,
                     int renorm, int32_t* topk_ids, float* topk_w, void* stream);
@@ -118,7 +121,8 @@ int quads_moe_route(const void* logits, int dtype, int64_t T, int32_t E, int64_t
  *   logits     the forward call's (may be NULL with renorm 1)
  *   dlogits    out [T, E] in `dtype`, dense; may be logits where ld == E
  * A token with every logit -inf has gradient 0.  An id outside [0, E) is left
- * out of both sums.
+ * out of both sums.  A p_v is off by the rounding of z_v - max z in fp32 and 2
+ * ulps besides, however unlikely the expert (0 below 2^-126 of the largest).
  */
 int quads_moe_route_backward(const void* logits, int dtype, int64_t T, int32_t E, int64_t ld,
                              const int32_t* topk_ids, const float* topk_w, const float* g,
