@@ -882,10 +882,10 @@ def quads_rmsnorm(x, weight=None, eps=1e-6, residual=None, out_dtype=OUT_BF16, w
 
 
 def quads_rmsnorm_backward(g, h, weight=None, eps=1e-6, g_sum=None, dx_dtype=None,
-                           want_dweight=True):
+                           want_dweight=True, want_dres=True):
     """Gradient of quads_rmsnorm from the gradient g [T, H] of its y and g_sum (or None) of its
     sum -> (dx, dres, dweight).  h is the call's sum (x without a residual); dx has the type
-    dx_dtype (h's), dres is dx unless the types differ."""
+    dx_dtype (h's), dres is dx unless the types differ (then None if not wanted)."""
     h, ht, ldh = _rows("h", h)
     dev = h.device
     t, n = h.shape
@@ -901,13 +901,13 @@ def quads_rmsnorm_backward(g, h, weight=None, eps=1e-6, g_sum=None, dx_dtype=Non
         raise TypeError("dx_dtype must be float32 or bf16")
     dt = OUT_F32 if dx_dtype == torch.float32 else OUT_BF16
     dx = torch.empty(t, n, dtype=dx_dtype, device=dev)
-    dres = torch.empty(t, n, dtype=h.dtype, device=dev) if dt != ht else None
+    dres = torch.empty(t, n, dtype=h.dtype, device=dev) if dt != ht and want_dres else None
     dw = torch.empty_like(weight) if want_dweight and weight is not None else None
     nws = lib().quads_rmsnorm_backward_ws(t, n, int(dw is not None))
     ws = _scratch(nws, dev)
     _call("quads_rmsnorm_backward", dev, _at(g), gt, _at(h), ht, t, n, ldh, _at(weight), wt, eps,
           _at(g_sum), _at(dx), dt, _at(dres), _at(dw), _at(ws), nws)
-    return dx, (dx if dres is None else dres), dw
+    return dx, (dx if dt == ht else dres), dw
 
 
 def quads_moe_route(logits, topk, renorm=True):

@@ -173,19 +173,24 @@ class RMSNorm(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, g, g_sum):
         h, weight = ctx.saved_tensors
+        for_x, for_res, for_w = ctx.needs_input_grad[:3]
+        for_res = for_res and ctx.added
         if g is None:
             if g_sum is None:
                 return None, None, None, None, None
-            return g_sum.to(ctx.x_dtype), g_sum, None, None, None
-        n = h.shape[-1]
-        dx, dres, dw = quads_rmsnorm_backward(g.reshape(-1, n), h.reshape(-1, n), weight, ctx.eps,
-                                              None if g_sum is None else g_sum.reshape(-1, n),
-                                              ctx.x_dtype, ctx.needs_input_grad[2])
+            return g_sum.to(ctx.x_dtype) if for_x else None, g_sum if for_res else None, None, None, None
+        n, any_rows = h.shape[-1], for_x or for_res
+        # an input that needs no gradient gets none; where only the weight does, dx is written all
+        # the same, in the narrow type, and without h's other gradient
+        g_sum = g_sum.reshape(-1, n) if any_rows and g_sum is not None else None
+        dx, dres, dw = quads_rmsnorm_backward(
+            g.reshape(-1, n), h.reshape(-1, n), weight, ctx.eps, g_sum,
+            ctx.x_dtype if for_x else h.dtype if for_res else torch.bfloat16, for_w, for_res)
         one = dres is dx
         dx = dx.view(h.shape)
-        if ctx.added:
+        if for_res:
             dres = dx if one else dres.view(h.shape)
-        return dx, dres if ctx.added else None, dw, None, None
+        return dx if for_x else None, dres if for_res else None, dw, None, None
 
 
 def rms_norm(x, weight=None, eps=1e-6, residual=None, out_dtype=None):

@@ -21,7 +21,8 @@ def plain_norm(x, weight=None, eps=EPS, residual=None, out_dtype=1, want_sum=Tru
     return out
 
 
-def plain_norm_backward(g, h, weight=None, eps=EPS, g_sum=None, dx_dtype=None, want_dweight=True):
+def plain_norm_backward(g, h, weight=None, eps=EPS, g_sum=None, dx_dtype=None, want_dweight=True,
+                        want_dres=True):
     """quads_rmsnorm_backward's binding: dres is dx unless the types differ."""
     assert g.dim() == 2 and h.shape == g.shape and (g_sum is None or g_sum.shape == g.shape)
     v = h.float()
@@ -32,7 +33,7 @@ def plain_norm_backward(g, h, weight=None, eps=EPS, g_sum=None, dx_dtype=None, w
         d = d + g_sum.float()
     dx = d.to(dx_dtype or h.dtype)
     dw = (g.float() * n).sum(0).to(weight.dtype) if want_dweight and weight is not None else None
-    return dx, (dx if dx.dtype == h.dtype else d.to(h.dtype)), dw
+    return dx, (dx if dx.dtype == h.dtype else d.to(h.dtype) if want_dres else None), dw
 
 
 @pytest.fixture
@@ -109,3 +110,65 @@ def test_types_and_results_changed_in_place(norm, shape):
     (plain(*ref)[0] * 2).sum().backward()
     for a, b in zip((x, r, w), ref):
         assert torch.allclose(a.grad, b.grad, rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("of", ["y", "h", "both"])
+@pytest.mark.parametrize("xt,rt", [(torch.float32, torch.float32), (torch.float32, torch.bfloat16),
+                                   (torch.bfloat16, torch.float32)])
+def test_only_wanted_gradients_are_formed(norm, monkeypatch, xt, rt, of):
+    """For each choice of inputs that need a gradient: those of the call that forms all, and no
+    tensor of another's type is asked for."""
+    asked = []
+
+    def spy(*args, **kw):
+        out = plain_norm_backward(*args, **kw)
+        asked.append([v for v in out if v is not None])
+        return out
+    monkeypatch.setattr(qat, "quads_rmsnorm_backward", spy)
+    g = torch.Generator().manual_seed(3)
+    values = [torch.randn(2, 3, 8, generator=g).to(xt), torch.randn(2, 3, 8, generator=g).to(rt),
+              torch.randn(8, generator=g)]
+    gy, gh = (torch.randn(2, 3, 8, generator=g).to(rt) for _ in range(2))
+
+    def grads(which, residual=True):
+        v = [t.clone().requires_grad_(n in which) for n, t in zip("xrw", values)]
+        out = norm(v[0], v[2], EPS, v[1])
+        pick = {"y": ([0], [gy]), "h": ([1], [gh]), "both": ([0, 1], [gy, gh])}[of]
+        results = [out[i] for i in pick[0]]
+        if not any(t.requires_grad for t in results):
+            return {}
+        torch.autograd.backward(results, pick[1])
+        return {n: t.grad for n, t in zip("xrw", v)}
+    want = grads("xrw")
+    for which in ("x", "r", "w", "xr", "xw", "rw"):
+        asked.clear()
+        got = grads(which)
+        for n in "xrw":
+            if n not in which:
+                assert got.get(n) is None
+            elif want[n] is None:
+                assert got[n] is None
+            else:
+                assert torch.equal(got[n], want[n])
+        if of != "h":
+            (made,) = asked
+            full = {id(t) for t in made if t.dim() == 2}
+            assert len(full) == (2 if {"x", "r"} <= set(which) and xt != rt else 1)
+            assert any(t.dim() == 1 for t in made) == ("w" in which)
+            if which == "w":
+                assert all(t.dtype == torch.bfloat16 for t in made if t.dim() == 2)
+
+
+def test_without_a_residual(norm):
+    x, _, w = leaves((2, 2, 8))
+    for _ in range(2):
+        norm(x, w, EPS).sin().sum().backward()
+    ref = [v.detach().clone().requires_grad_(True) for v in (x, w)]
+    for _ in range(2):
+        plain(ref[0], torch.zeros(2, 2, 8), ref[1])[0].sin().sum().backward()
+    for a, b in zip((x, w), ref):
+        assert torch.allclose(a.grad, b.grad, rtol=1e-5, atol=1e-5)
+    x = x.detach()
+    w.grad = None
+    norm(x, w, EPS).sum().backward()
+    assert x.grad is None and w.grad is not None

@@ -90,3 +90,26 @@ def test_rows_that_are_not_dense():
                                [gy.contiguous(), gh.contiguous()])
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("of", ["y", "h", "both"])
+@pytest.mark.parametrize("xt,rt", [(F32, F32), (F32, BF16), (BF16, F32)])
+def test_any_choice_of_inputs_gets_the_same_gradients(xt, rt, of):
+    values = [randn((3, 7, 96), 1, xt), randn((3, 7, 96), 2, rt), randn((96,), 3)]
+    gy, gh = randn((3, 7, 96), 4, rt), randn((3, 7, 96), 5, rt)
+
+    def grads(which):
+        v = [t.clone().requires_grad_(n in which) for n, t in zip("xrw", values)]
+        out = qat.rms_norm(v[0], v[2], EPS, v[1])
+        pick = {"y": [(out[0], gy)], "h": [(out[1], gh)], "both": [(out[0], gy), (out[1], gh)]}[of]
+        pick = [p for p in pick if p[0].requires_grad]
+        if pick:
+            torch.autograd.backward([p[0] for p in pick], [p[1] for p in pick])
+        return {n: t.grad for n, t in zip("xrw", v)}
+    want = grads("xrw")
+    for which in ("x", "r", "w", "xr", "xw", "rw"):
+        for n, got in grads(which).items():
+            if n not in which or want[n] is None:
+                assert got is None
+            else:
+                assert torch.equal(got, want[n])
