@@ -81,8 +81,9 @@ int quads_rmsnorm(const void* x, int x_dtype, int64_t T, int64_t H, int64_t ldx,
  *   dres       NULL or out [T, H]: dh in h's type, for a residual of another
  *              type than x.  Not dx; may be g_sum
  *   dweight    NULL or out [H] in w_dtype (a NULL weight has none)
- * Sums over channels are fp64; the sum over tokens is fp32 in runs of rows
- * joined in fp64, in an order that the sizes alone decide.
+ * Sums over channels are fp64; the sum over tokens is fp32 in chains of at most
+ * 64 + 127 additions (rows, then parts of a work-group) joined in fp64, in an
+ * order that the sizes alone decide.
  * ws: quads_rmsnorm_backward_ws bytes (0 without dweight for rows that one
  * work-group holds).
  */

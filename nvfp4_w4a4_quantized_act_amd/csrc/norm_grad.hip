@@ -15,8 +15,8 @@ struct GradArgs {
     float2* stat;                            // [T]: r, c
     float* part;                             // [runs, H], with dweight
     int64_t T, H, ldh;
-    int64_t rows;                            // of a run of rows
-    int runs;
+    int64_t rows;                            // of a run of rows, or of a stretch
+    int runs, wide;                          // work-groups of a stretch
     double eps, inv_h;
     int w_dtype, dx_dtype;
 };
@@ -52,7 +52,10 @@ __global__ __launch_bounds__(1024) void k_rms_grad_held(GradArgs a, int lanes_) 
         if (p[j].n > 0) load_weight(a.weight, a.w_dtype, p[j].at, p[j].n, w[j]);
     }
     int set = 0;
-    for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < a.T; t0 += (int64_t)gridDim.x * rows) {
+    const int64_t stretch = blockIdx.x / (unsigned)a.wide, first = stretch * a.rows;
+    const int64_t end = first + a.rows < a.T ? first + a.rows : a.T;
+    for (int64_t t0 = first + (blockIdx.x - stretch * a.wide) * rows; t0 < end;
+         t0 += (int64_t)a.wide * rows) {
         const int64_t t = t0 + row;
         const bool live = t < a.T;
         Raw<kG> g[kV];
@@ -180,13 +183,14 @@ __global__ __launch_bounds__(kThreads) void k_rms_grad_stat(GradArgs a) {
 }
 
 // dh, and the weight gradient's partial sums, of eight channels a thread in the
-// rows of run blockIdx.y.  Each value of g and g_sum is read before its place is
-// written, by the same thread.
+// rows of a run; `cols` neighbouring work-groups have one run.  Each value of g and
+// g_sum is read before its place is written, by the same thread.
 template <int kG, int kH>
-__global__ __launch_bounds__(kThreads) void k_rms_grad_apply(GradArgs a) {
-    const int64_t c = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kPer;
+__global__ __launch_bounds__(kThreads) void k_rms_grad_apply(GradArgs a, unsigned cols) {
+    const unsigned run = blockIdx.x / cols;
+    const int64_t c = ((int64_t)(blockIdx.x - run * cols) * kThreads + threadIdx.x) * kPer;
     if (c >= a.H) return;
-    const int64_t n = a.H - c, t0 = blockIdx.y * a.rows;
+    const int64_t n = a.H - c, t0 = run * a.rows;
     const int64_t t1 = t0 + a.rows < a.T ? t0 + a.rows : a.T;
     float w[kPer], acc[kPer] = {};
     load_weight(a.weight, a.w_dtype, c, n, w);
@@ -212,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void k_rms_grad_apply(GradArgs a) {
         else
             store<0>(row_at<0>(a.dx, t * a.H), c, n, pack<0>(d));
     }
-    if (a.part) store<0>(a.part + blockIdx.y * a.H, c, n, pack<0>(acc));
+    if (a.part) store<0>(a.part + run * a.H, c, n, pack<0>(acc));
 }
 
 // dweight from the partial sums of `runs` work-groups or runs of rows: 16 channels a
@@ -261,15 +265,29 @@ inline GradShape grad_shape(int64_t T, int64_t H) {
 // threads a CU, two of up to 768 where each still has 16 rows (8192 x 5000 bf16 73 us
 // against 80, 777 x 5001 fp32 26.7 / 23.8: more partial sums); two of 1024 would not fit
 // with their 80 registers, and took 16384 x 2048 bf16 from 57.6 to 59.1 us.  All with the
-// same number of rows, nearly.
-constexpr int64_t kMaxGroups = 2048;
-inline int64_t grad_runs(int64_t T, int64_t H) {
+// same number of rows, nearly.  Where a thread would add up more than kChain rows in fp32,
+// whose rounding would grow with T (512 rows off by up to 124 * 2^-24, 64 by 64), the rows
+// are cut into stretches, one after another, each with work-groups of its own (every
+// work-group's rows over all of T instead: 262144 x 4096 bf16 1735 us against 1579).
+constexpr int64_t kMaxGroups = 2048, kChain = 64;
+struct Runs {
+    int64_t stretches, wide, turns;          // work-groups of a stretch, and the rows in turn of each
+};
+inline Runs grad_stretches(int64_t T, int64_t H) {
     const GradShape p = grad_shape(T, H);
-    if (!p.v) return T < 8 ? 1 : (T / 8 < 512 ? T / 8 : 512);
+    if (!p.v) {
+        const int64_t n = T < 8 ? 1 : (T / 8 < 512 ? T / 8 : 512), least = (T + kChain - 1) / kChain;
+        return {1, n > least ? n : least, 0};
+    }
     const int64_t rows = p.threads / p.lanes, n = (T + rows - 1) / rows;
     const int64_t most = p.threads <= 768 && n >= 8192 ? 512 : 256;
-    const int64_t turns = (n + most - 1) / most;
-    return (n + turns - 1) / turns;
+    const int64_t stretches = (n + most * kChain - 1) / (most * kChain);
+    const int64_t each = (n + stretches - 1) / stretches, turns = (each + most - 1) / most;
+    return {stretches, (each + turns - 1) / turns, turns};
+}
+inline int64_t grad_runs(int64_t T, int64_t H) {
+    const Runs r = grad_stretches(T, H);
+    return r.stretches * r.wide;
 }
 
 template <int kG, int kH>
@@ -296,7 +314,8 @@ void launch_grad(const GradArgs& a, hipStream_t s) {
     const int64_t rows = a.T < kMaxGroups ? a.T : kMaxGroups;
     hipLaunchKernelGGL((k_rms_grad_stat<kG, kH>), dim3((unsigned)rows), block, 0, s, a);
     const unsigned cols = (unsigned)((a.H + kThreads * kPer - 1) / (kThreads * kPer));
-    hipLaunchKernelGGL((k_rms_grad_apply<kG, kH>), dim3(cols, (unsigned)a.runs), block, 0, s, a);
+    const dim3 grid(cols * (unsigned)a.runs);
+    hipLaunchKernelGGL((k_rms_grad_apply<kG, kH>), grid, block, 0, s, a, cols);
 }
 
 }  // namespace norm
@@ -339,11 +358,14 @@ extern "C" int quads_rmsnorm_backward(const void* g, int g_dtype, const void* h,
         return QUADS_EINVAL;
     const size_t need = quads_rmsnorm_backward_ws(T, H, dweight != nullptr);
     if (need && (ws_bytes < need || !ok_ptr(ws))) return QUADS_EWORKSPACE;
-    const int64_t runs = grad_runs(T, H);
-    const size_t stat = grad_shape(T, H).v ? 0 : align_up((size_t)T * 8, 256);
+    const GradShape p = grad_shape(T, H);
+    const Runs r = grad_stretches(T, H);
+    const int64_t runs = r.stretches * r.wide;
+    const int64_t rows = p.v ? r.turns * r.wide * (p.threads / p.lanes) : (T + runs - 1) / runs;
+    const size_t stat = p.v ? 0 : align_up((size_t)T * 8, 256);
     float* part = dweight ? (float*)((char*)ws + stat) : nullptr;
     GradArgs a = {g, h, weight, g_sum, dx, dres, (float2*)ws, part, T, H, ldh,
-                  (T + runs - 1) / runs, (int)runs, eps, 1.0 / (double)H,
+                  rows, (int)runs, (int)r.wide, eps, 1.0 / (double)H,
                   weight ? w_dtype : kNoWeight, dx_dtype};
     const bool gb = g_dtype == QUADS_OUT_BF16, hb = h_dtype == QUADS_OUT_BF16;
     if (gb && hb) launch_grad<1, 1>(a, s);
