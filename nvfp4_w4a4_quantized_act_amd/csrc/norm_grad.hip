@@ -38,7 +38,7 @@ struct GradArgs {
 template <int kG, int kH, int kLanes, int kV, int kCut>
 __global__ __launch_bounds__(1024) void k_rms_grad_held(GradArgs a, int lanes_) {
     __shared__ double s_sq[2][kMaxWaves], s_dot[2][kMaxWaves];
-    __shared__ float s_acc[kV == 1 ? 1024 * kPer : 1];
+    __shared__ __align__(16) float s_acc[kV == 1 ? 1024 * kPer : 1];
     const int lanes = kLanes ? kLanes : lanes_;
     const int rows = (int)blockDim.x / lanes;
     const int row = threadIdx.x / lanes, lane = threadIdx.x - row * lanes;
