@@ -1,4 +1,4 @@
-// Token-to-expert packing and the MoE combine.
+// Token-to-expert packing.
 //
 // Packing is a stable counting sort of the T*topk (token, slot) pairs by
 // expert id.  Up to 4096 pairs and 512 experts: one work-group, one launch
@@ -9,9 +9,6 @@
 // them into expert offsets and per-chunk bases, and a scatter in which one
 // wave walks its chunk 64 entries at a time, ranking equal ids with ballots
 // so that equal ids keep their flattened order.
-//
-// Combine: out[t] = sum over slots (in order) of w[t, slot] * y[pos[t, slot]],
-// eight output features per thread, fp32 fused multiply-adds.
 #include "common.h"
 
 namespace quads {
@@ -411,44 +408,6 @@ __global__ __launch_bounds__(1024) void k_pack_small(const int32_t* __restrict__
     }
 }
 
-// ---------------------------------------------------------------- combine --
-template <bool kBf16>
-__global__ __launch_bounds__(256) void k_combine(const void* __restrict__ y,
-                                                 const int32_t* __restrict__ pos,
-                                                 const float* __restrict__ w, int64_t T, int topk,
-                                                 int64_t N, float* __restrict__ out) {
-    const int64_t groups = N / 8;
-    const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (gid >= T * groups) return;
-    const int64_t t = gid / groups;
-    const int64_t c = (gid - t * groups) * 8;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < topk; ++s) {
-        const float ws = w[t * topk + s];
-        const int64_t p = pos[t * topk + s];
-        float v[8];
-        if (kBf16) {
-            const uint4 q = *reinterpret_cast<const uint4*>((const uint16_t*)y + p * N + c);
-            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(u[i] << 16);
-                v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-            }
-        } else {
-            const float4* q = reinterpret_cast<const float4*>((const float*)y + p * N + c);
-            const float4 a = q[0], b = q[1];
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(ws, v[i], acc[i]);
-    }
-    float4* o = reinterpret_cast<float4*>(out + t * N + c);
-    o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-}
-
 }  // namespace quads
 
 using namespace quads;
@@ -494,26 +453,5 @@ extern "C" int quads_moe_pack(const int32_t* topk_ids, int64_t T, int32_t topk, 
                            (int)E, cnt, offsets, row_token, pos);
         QUADS_CHECK_LAUNCH();
     }
-    return QUADS_OK;
-}
-
-extern "C" int quads_moe_combine(const void* y, int y_dtype, const int32_t* pos,
-                                 const float* topk_w, int64_t T, int32_t topk, int64_t N,
-                                 float* out, void* stream) {
-    if (y_dtype != QUADS_OUT_F32 && y_dtype != QUADS_OUT_BF16) return QUADS_EINVAL;
-    if (T < 0 || topk < 1 || N <= 0 || N % 8) return QUADS_ESHAPE;
-    if (T > 0 && (!ok_ptr(y) || !ok_ptr(pos) || !ok_ptr(topk_w) || !ok_ptr(out)))
-        return QUADS_EINVAL;
-    if (T == 0) return QUADS_OK;
-    hipStream_t s = (hipStream_t)stream;
-    const int64_t threads = T * (N / 8);
-    const dim3 grid((unsigned)((threads + 255) / 256));
-    if (y_dtype == QUADS_OUT_BF16)
-        hipLaunchKernelGGL(k_combine<true>, grid, dim3(256), 0, s, y, pos, topk_w, T, (int)topk, N,
-                           out);
-    else
-        hipLaunchKernelGGL(k_combine<false>, grid, dim3(256), 0, s, y, pos, topk_w, T, (int)topk,
-                           N, out);
-    QUADS_CHECK_LAUNCH();
     return QUADS_OK;
 }

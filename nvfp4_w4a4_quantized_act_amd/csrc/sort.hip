@@ -1,4 +1,5 @@
-// Tokens in packed (expert) order and back, and the gradient of the way back.
+// Tokens in packed (expert) order and back, and the gradient of the way back.  The MoE
+// combine of quads.h is the way back with weights and fp32 output.
 //
 //   sort     out[pos[t, s]] = x[t]
 //   unsort   out[t] = sum_s w[t, s] y[pos[t, s]]
@@ -23,7 +24,7 @@ struct Args {
     const void* y;                           // of the gradient
     void* out;                               // packed rows, token rows, or dy
     float* dw;
-    int64_t T, H, ld, rows;
+    int64_t T, H, ld, rows;                  // ld: of x, and of y and out on the way back
     int topk, per;                           // per: slots of a work-group of the gradient
     const int32_t* slot_of;                  // [rows], where rows without a slot become 0
     int64_t slots;                           // of the whole call
@@ -141,18 +142,19 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_unsort(Args a,
             r[s] = Raw<kY>{};
             by[s] = 0.0f;
             if (p >= 0) {
-                r[s] = load<kY, kCut != kTiny, (kOnce & 1) != 0>(row_at<kY>(a.a, p * a.H),
+                r[s] = load<kY, kCut != kTiny, (kOnce & 1) != 0>(row_at<kY>(a.a, p * a.ld),
                                                                  at.p.at, at.p.n);
                 by[s] = w ? w[slot] : 1.0f;
             }
         }
 #pragma unroll
         for (int s = 0; s < kBatch; ++s) {
+            if (s0 + s >= a.topk) break;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) acc[i] = fmaf(by[s], r[s].get(i), acc[i]);
         }
     }
-    store<kOut, kCut != kTiny>(row_at<kOut>(a.out, at.t * a.H), at.p.at, at.p.n, pack<kOut>(acc));
+    store<kOut, kCut != kTiny>(row_at<kOut>(a.out, at.t * a.ld), at.p.at, at.p.n, pack<kOut>(acc));
 }
 
 // kLanes 0: a work-group per token and `per` slots, its threads over the row, again where it
@@ -354,6 +356,34 @@ inline int check(int64_t T, int64_t H, int64_t ld, int32_t topk, int64_t rows) {
     return QUADS_OK;
 }
 
+// The way back, in launches of at most kLaunchTokens tokens and kPartChannels channels.
+constexpr int64_t kPartChannels = (int64_t)1 << 24;
+inline int back(const void* y, int y_dtype, int64_t rows, const int32_t* pos, const float* topk_w,
+                int64_t T, int32_t topk, int64_t H, void* out, int out_dtype, hipStream_t s) {
+    const bool yb = y_dtype == QUADS_OUT_BF16, ob = out_dtype == QUADS_OUT_BF16;
+    const int64_t bytes = T * topk * H * (yb ? 2 : 4);
+    for (int64_t t = 0; t < T; t += kLaunchTokens) {
+        for (int64_t c = 0; c < H; c += kPartChannels) {
+            Args a = {};
+            a.a = (const char*)y + c * (yb ? 2 : 4);
+            a.out = (char*)out + (t * H + c) * (ob ? 2 : 4);
+            a.T = T - t < kLaunchTokens ? T - t : kLaunchTokens;
+            a.H = H - c < kPartChannels ? H - c : kPartChannels;
+            a.ld = H;
+            a.rows = rows;
+            a.topk = topk;
+            const int32_t* p = pos + t * topk;
+            const float* w = topk_w ? topk_w + t * topk : nullptr;
+            if (yb && ob) launch_unsort<1, 1>(a, p, w, bytes, s);
+            else if (yb) launch_unsort<1, 0>(a, p, w, bytes, s);
+            else if (ob) launch_unsort<0, 1>(a, p, w, bytes, s);
+            else launch_unsort<0, 0>(a, p, w, bytes, s);
+            QUADS_CHECK_LAUNCH();
+        }
+    }
+    return QUADS_OK;
+}
+
 }  // namespace sorting
 }  // namespace quads
 
@@ -408,26 +438,20 @@ extern "C" int quads_moe_unsort(const void* y, int y_dtype, int64_t rows, const 
     if (T == 0) return QUADS_OK;
     if ((rows > 0 && !ok_ptr(y)) || !ok_ptr4(pos) || !ok_opt4(topk_w) || !ok_ptr(out) || y == out)
         return QUADS_EINVAL;
-    hipStream_t s = (hipStream_t)stream;
-    const bool yb = y_dtype == QUADS_OUT_BF16, ob = out_dtype == QUADS_OUT_BF16;
-    const int64_t bytes = T * topk * H * (yb ? 2 : 4);
-    for (int64_t t = 0; t < T; t += kLaunchTokens) {
-        Args a = {};
-        a.a = y;
-        a.out = (char*)out + t * H * (ob ? 2 : 4);
-        a.T = T - t < kLaunchTokens ? T - t : kLaunchTokens;
-        a.H = H;
-        a.rows = rows;
-        a.topk = topk;
-        const int32_t* p = pos + t * topk;
-        const float* w = topk_w ? topk_w + t * topk : nullptr;
-        if (yb && ob) launch_unsort<1, 1>(a, p, w, bytes, s);
-        else if (yb) launch_unsort<1, 0>(a, p, w, bytes, s);
-        else if (ob) launch_unsort<0, 1>(a, p, w, bytes, s);
-        else launch_unsort<0, 0>(a, p, w, bytes, s);
-        QUADS_CHECK_LAUNCH();
-    }
-    return QUADS_OK;
+    return sorting::back(y, y_dtype, rows, pos, topk_w, T, topk, H, out, out_dtype,
+                         (hipStream_t)stream);
+}
+
+// Any number of slots, tokens and rows' eights; pos names T * topk rows.
+extern "C" int quads_moe_combine(const void* y, int y_dtype, const int32_t* pos,
+                                 const float* topk_w, int64_t T, int32_t topk, int64_t N,
+                                 float* out, void* stream) {
+    if (y_dtype != QUADS_OUT_F32 && y_dtype != QUADS_OUT_BF16) return QUADS_EINVAL;
+    if (T < 0 || topk < 1 || N <= 0 || N % 8) return QUADS_ESHAPE;
+    if (T > 0 && (!ok_ptr(y) || !ok_ptr(pos) || !ok_ptr(topk_w) || !ok_ptr(out)))
+        return QUADS_EINVAL;
+    return sorting::back(y, y_dtype, T * topk, pos, topk_w, T, topk, N, out, QUADS_OUT_F32,
+                         (hipStream_t)stream);
 }
 
 extern "C" int quads_moe_unsort_backward(const void* g, int g_dtype, const void* y, int y_dtype,
