@@ -52,8 +52,10 @@ extern "C" {
  *   y, out_dtype   out [T, H]: fp32, bf16, or QUADS_OUT_MX_FP8: E4M3 codes
  *              uint8 with a scale byte per 32 channels in `scales` [T, H/32]
  *              (H % 32 == 0), the format and rules of quads_mx_quantize applied
- *              to y itself, not to its bf16 rounding.  y may be x or residual,
- *              where that is dense and of y's type and not sum
+ *              to y itself, not to its bf16 rounding; a NaN gets a NaN code, an
+ *              infinite y saturates, and their block has the scale byte 254, the
+ *              largest (quads_mx_quantize asks for finite input).  y may be x or
+ *              residual, where that is dense and of y's type and not sum
  *   amax_part  NULL, or (bf16 only) out uint32 [amax_groups]: partial maxima of
  *              |y| as bf16 bits for quads_nvfp4_quantize_partials and
  *              quads_rac_quantize_partials; amax_groups >=
@@ -61,8 +63,9 @@ extern "C" {
  * 1 <= H < 2^24, T < 2^31.  The mean is formed in fp64; with QUADS_OUT_MX_FP8
  * so is y (each code and scale is that of the exact y unless it lies within
  * about 2^-50 of a border).  fp32 and bf16 outputs come from two fp32 products
- * (3 * 2^-24 of the value; two bits more in rows whose root mean square is above
- * 2^126) and are rounded once.
+ * (3 * 2^-24 of the value, and 2^-149 (|weight| + 1) where h / sqrt(..) or y is
+ * subnormal; two bits more in rows whose root mean square is above 2^126) and
+ * are rounded once.
  */
 int64_t quads_rmsnorm_amax_groups(int64_t T, int64_t H);
 int quads_rmsnorm(const void* x, int x_dtype, int64_t T, int64_t H, int64_t ldx,
