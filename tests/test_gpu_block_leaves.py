@@ -113,3 +113,40 @@ def test_any_choice_of_inputs_gets_the_same_gradients(xt, rt, of):
                 assert got is None
             else:
                 assert torch.equal(got, want[n])
+
+
+@pytest.mark.parametrize("rows", [None, 40])
+@pytest.mark.parametrize("which", ["y", "w", "yw"])
+def test_way_back_with_some_inputs_and_twice(which, rows):
+    """Only the gradients that are wanted, the same bits for any choice, doubled by a second pass."""
+    t, k, h = 11, 3, 77
+    n = rows or t * k
+    pos = torch.randperm(n, generator=torch.Generator().manual_seed(0))[:t * k].int().to(DEV)
+    values = {"y": randn((n, h), 1), "w": randn((t, k), 2)}
+    g = randn((t, h), 3)
+
+    def results(needed):
+        v = {name: a.clone().requires_grad_(name in needed) for name, a in values.items()}
+        return v, qat.unsort_tokens(v["y"], pos, k, v["w"], rows=rows)
+    v, o = results("yw")
+    want = dict(zip("yw", torch.autograd.grad(o, [v["y"], v["w"]], g)))
+    v, o = results(which)
+    o.backward(g)
+    o = qat.unsort_tokens(v["y"], pos, k, v["w"], rows=rows)
+    o.backward(g)
+    for name in "yw":
+        assert v[name].grad is None if name not in which else torch.equal(v[name].grad, 2 * want[name])
+    dy, dw, _ = OB.unsort_grad(f64(g), f64(values["y"]), pos.cpu().numpy(), k, f64(values["w"]))
+    assert np.allclose(f64(want["y"]), dy, rtol=1e-6, atol=0) and np.allclose(f64(want["w"]), dw, atol=1e-4)
+
+
+def test_sort_and_route_twice():
+    t, k, h, e = 9, 2, 50, 16
+    x, z = randn((t, h), 1).requires_grad_(True), randn((3, 3, e), 2).requires_grad_(True)
+    pos = torch.randperm(t * k, generator=torch.Generator().manual_seed(0)).int().to(DEV)
+    gx, gw = randn((t * k, h), 3), randn((3, 3, k), 4)
+    one = torch.autograd.grad([qat.sort_tokens(x, pos, k), qat.route(z, k, False)[0]], [x, z], [gx, gw])
+    for _ in range(2):
+        qat.sort_tokens(x, pos, k).backward(gx)
+        qat.route(z, k, False)[0].backward(gw)
+    assert torch.equal(x.grad, 2 * one[0]) and torch.equal(z.grad, 2 * one[1])
