@@ -125,8 +125,8 @@ int quads_moe_route(const void* logits, int dtype, int64_t T, int32_t E, int64_t
  *   logits     the forward call's (may be NULL with renorm 1)
  *   dlogits    out [T, E] in `dtype`, dense; may be logits where ld == E
  * A token with every logit -inf has gradient 0.  An id outside [0, E) is left
- * out of both sums.  A p_v is off by the rounding of z_v - max z in fp32 and 2
- * ulps besides, however unlikely the expert (0 below 2^-126 of the largest).
+ * out of both sums.  The exponential in p_v is off by the rounding of z_v - max z
+ * in fp32 and 2 ulps, however unlikely the expert (0 below 2^-126).
  */
 int quads_moe_route_backward(const void* logits, int dtype, int64_t T, int32_t E, int64_t ld,
                              const int32_t* topk_ids, const float* topk_w, const float* g,

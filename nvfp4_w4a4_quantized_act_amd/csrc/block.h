@@ -209,10 +209,10 @@ inline Cut cut_of(int64_t H) { return H % kPer == 0 ? kEven : (H < kPer ? kTiny 
 // The eight channels of a thread in a row of len channels: elements at .. at + 7, of
 // which those from `from` on are its own.  The row's last, partial eight (kOdd) start
 // earlier and share channels with the eight before: what both compute is the same, so
-// both may store it, where no other thread reads what was there any more (else store_own),
-// and sums leave out what is not the thread's own.  (Reading and
-// storing a partial eight element by element takes a row's work-group three latencies
-// more, 16384 x 1001 bf16 21.3 us against 15.9, 8192 x 5001 93 against 79.)
+// both may store it once no other thread reads what was there any more (else store_own),
+// and sums leave out what is not the thread's own.  (Reading and storing a partial eight
+// element by element takes a row's work-group three latencies more, 16384 x 1001 bf16
+// 21.3 us against 15.9, 8192 x 5001 93 against 79.)
 struct Piece {
     int at, from, n;                         // n: how many there are, 0 .. 8
 };
