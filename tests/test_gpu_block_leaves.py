@@ -150,3 +150,35 @@ def test_sort_and_route_twice():
         qat.sort_tokens(x, pos, k).backward(gx)
         qat.route(z, k, False)[0].backward(gw)
     assert torch.equal(x.grad, 2 * one[0]) and torch.equal(z.grad, 2 * one[1])
+
+
+def test_leading_dimensions_captured():
+    """Forward, gradients and the combine of rows in a graph, replayed with eager work between."""
+    from nvfp4_w4a4_quantized_act_amd import quads_moe_combine
+    x, r = randn((2, 5, 96), 1).requires_grad_(True), randn((2, 5, 96), 2, BF16).requires_grad_(True)
+    w = randn((96,), 3).requires_grad_(True)
+    gy, gh = randn((2, 5, 96), 4, BF16), randn((2, 5, 96), 5, BF16)
+    pos, tw = torch.tensor([3, 0, 4, 1, 2, 9, 8, 7, 6, 5], dtype=torch.int32, device=DEV), randn((5, 2), 6)
+
+    def step():
+        y, h = qat.rms_norm(x, w, EPS, r)
+        out = quads_moe_combine(y.detach().view(10, 96), pos, tw, y_dtype=1)
+        return [y.detach(), h.detach(), out, *torch.autograd.grad([y, h], [x, r, w], [gy, gh])]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for turn in range(3):
+        with torch.no_grad():
+            x.copy_(randn((2, 5, 96), 20 + turn))
+            r.copy_(randn((2, 5, 96), 30 + turn, BF16))
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
